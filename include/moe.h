@@ -52,6 +52,7 @@ extern "C" {
 #endif
 
 typedef uint16_t moe_bf16;                 /* raw bf16 bits */
+typedef uint8_t moe_e4m3;                  /* raw 8-bit floating-point bits: 1 sign, 4 exponent, 3 mantissa */
 typedef struct CUstream_st* moe_stream_t;  /* the same type as cudaStream_t */
 typedef struct CUevent_st* moe_event_t;    /* the same type as cudaEvent_t */
 
@@ -64,6 +65,9 @@ typedef enum {
     MOE_ERR_TIMEOUT = 5,       /* a bounded device wait ran out (device) */
     MOE_ERR_DEVICE_BOUNDS = 6  /* a device index check failed (device) */
 } moe_status;
+
+/* Element types of the entry points that take more than one. */
+typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype;
 
 typedef struct {
     int64_t T;         /* tokens */
@@ -434,6 +438,107 @@ moe_status moe_layer_forward_host(const moe_dims* dims, const moe_bf16* x_host, 
 
 /* The chunk count moe_layer_forward_host uses for n_chunks = 0 (host only). */
 int32_t moe_host_chunks(const moe_dims* dims);
+
+/*
+ * ------------------------------------------------------------------ 8 bits --
+ * The layer with its expert products in 8-bit floating point. A value v is
+ * held as e4m3 q with its block's fp32 scale, v = q * scale:
+ *   activations [R, n]: a scale for each row's block of 128 columns,
+ *                       scale[R, ceil(n/128)];
+ *   weights [G, N, K]:  a scale for each 128 x 128 block, scale[G, ceil(N/128),
+ *                       ceil(K/128)]. K is contiguous (the transpose of the
+ *                       bf16 weights above).
+ * Quantizing a block: scale = max(largest |v|, 2^-100) / 448, q = v / scale to
+ * nearest (ties to even); a NaN or infinity in a block makes all of it NaN or
+ * is carried as NaN. Sizes are multiples of 16, the last block may be shorter.
+ * The products accumulate in fp32 and apply the scales in fp32.
+ *
+ * Conventions are those of the other entry points. The workspace `ws` of the
+ * products (moe_fp8_workspace_size(NULL) bytes, for any sizes) and of
+ * moe_fp8_layer_forward (moe_fp8_workspace_size(dims)) must hold zeros in its
+ * first moe_fp8_workspace_size(NULL) bytes before its first use, and again
+ * after moe_check has returned MOE_ERR_TIMEOUT for it; the calls leave them as
+ * the next call needs them. Two calls that share a workspace must not overlap.
+ */
+
+/* Bytes of the 8-bit entry points' workspace: of the products for dims NULL,
+ * else of moe_fp8_layer_forward (0 for invalid dims). */
+size_t moe_fp8_workspace_size(const moe_dims* dims);
+
+/*
+ * The residual's addition, the root-mean-square norm and its 8-bit output:
+ *   r = x + residual (x where residual is null), in fp32
+ *   y = r / sqrt(mean(r^2) + eps) * weight       (weight null = 1), in fp32
+ * In:  x[T,H] and residual[T,H] (nullable) of type dtype, rows x_stride and
+ *      residual_stride elements apart; weight[H] of type dtype (nullable).
+ * Out: sum[T,H] = r rounded to dtype, rows sum_stride apart (nullable; may be
+ *      the memory of x or of residual with the same stride); y[T,H] rounded to dtype
+ *      (nullable, contiguous); q[T,H] and scale[T,ceil(H/128)]: y quantized
+ *      (from fp32, not from its rounding).
+ * H a multiple of 16 up to 32768; pointers but scale 16-byte aligned and row
+ * strides multiples of 16 bytes.
+ */
+moe_status moe_add_rmsnorm_fp8(int64_t T, int32_t H, moe_dtype dtype, const void* x, int64_t x_stride,
+                               const void* residual, int64_t residual_stride, const void* weight, float eps, void* sum,
+                               int64_t sum_stride, void* y, moe_e4m3* q, float* scale, moe_stream_t stream);
+
+/*
+ * A weight's layout for the products, made once: w[G,K,N] (bf16, as the other
+ * entry points take them) to q[G,N,K] and its block scales.
+ */
+moe_status moe_fp8_quantize_weight(int32_t G, int32_t K, int32_t N, const moe_bf16* w, moe_e4m3* q, float* scale,
+                                   moe_stream_t stream);
+
+/*
+ * Grouped product: out[p,:] = a[p,:] w[g]^T for the rows p of group g,
+ * offsets[g] <= p < offsets[g+1] (offsets null = one group of R rows; G is
+ * then 1). Rows outside [offsets[0], offsets[G]) are not written. Offsets that
+ * decrease or leave [0, R] set MOE_ERR_DEVICE_BOUNDS in the device error word
+ * and nothing is computed.
+ * In:  a[R,K], a_scale; offsets[G+1] (device); w[G,N,K], w_scale.
+ * Out: out[R,N] in bf16 or fp32 (out_dtype).
+ */
+moe_status moe_fp8_matmul(int64_t R, int32_t K, int32_t N, int32_t G, const moe_e4m3* a, const float* a_scale,
+                          const int32_t* offsets, const moe_e4m3* w, const float* w_scale, moe_dtype out_dtype,
+                          void* out, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Gated product: h[p,:] = silu(a[p,:] w1[g]^T) * (a[p,:] w3[g]^T) for the rows
+ * of each group as in moe_fp8_matmul, both projections, the activation, the
+ * product and its quantization in one kernel.
+ * In:  a[R,K], a_scale; offsets[G+1]; w1, w3 [G,F,K] and their scales.
+ * Out: h[R,F], h_scale[R,ceil(F/128)]: quantized from fp32.
+ */
+moe_status moe_fp8_gated(int64_t R, int32_t K, int32_t F, int32_t G, const moe_e4m3* a, const float* a_scale,
+                         const int32_t* offsets, const moe_e4m3* w1, const float* w1_scale, const moe_e4m3* w3,
+                         const float* w3_scale, moe_e4m3* h, float* h_scale, void* ws, size_t ws_bytes,
+                         moe_stream_t stream);
+
+/* One expert set's 8-bit weights: w1, w3 [E,F,H], w2 [E,H,F] and their scales
+ * (moe_fp8_quantize_weight of W1, W3, W2). */
+typedef struct {
+    const moe_e4m3* w1;
+    const float* w1_scale;
+    const moe_e4m3* w3;
+    const float* w3_scale;
+    const moe_e4m3* w2;
+    const float* w2_scale;
+} moe_fp8_ffn;
+
+/*
+ * The whole layer on 8-bit experts: route (on x in bf16, as moe_layer_forward)
+ * -> sort, quantized rows to dispatch order -> gated product -> product,
+ * weighted and scattered -> (the shared expert, when F_shared > 0) -> combine.
+ * In:  x[T,H] (bf16: the router's input) and the same rows quantized, xq[T,H]
+ *      and xq_scale: y, q and scale of moe_add_rmsnorm_fp8; Wg, bias, gating
+ *      as in moe_layer_forward_ex; routed (dims->E experts of width F), shared
+ *      (one of width F_shared; null without one).
+ * Out: out[T,H] (bf16); routing (nullable).
+ */
+moe_status moe_fp8_layer_forward(const moe_dims* dims, const moe_bf16* x, const moe_e4m3* xq, const float* xq_scale,
+                                 const moe_bf16* Wg, const float* bias, const moe_gating* gating,
+                                 const moe_fp8_ffn* routed, const moe_fp8_ffn* shared, moe_bf16* out,
+                                 const moe_routing_out* routing, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

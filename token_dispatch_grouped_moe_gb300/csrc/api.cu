@@ -11,36 +11,16 @@
 #include <vector>
 #include <algorithm>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "../../include/moe.h"
 #include "kernels.cuh"
 #include "ptx.cuh"
+#include "api.h"
 
 namespace moe {
 namespace {
 
 constexpr int kVersion = 300;   // 0.3.0
 constexpr int kMaxDevices = 64;
-
-// ---------------------------------------------------------------- tracing --
-
-// An NVTX range over the host code that enqueues one stage: a profiler or
-// tracer that records NVTX (ncu --nvtx, Nsight Systems) attributes each
-// kernel to the stage that launched it ("moe/route", "moe/gemm0", ...). With
-// no tool attached, a push/pop pair is a couple of branches (NVTX v3 is
-// header-only and loads no library unless a tool asks for it).
-struct Range {
-    explicit Range(const char* name) { nvtxRangePushA(name); }
-    ~Range() { nvtxRangePop(); }
-    void next(const char* name)   // close this range and open the next stage's
-    {
-        nvtxRangePop();
-        nvtxRangePushA(name);
-    }
-    Range(const Range&) = delete;
-    Range& operator=(const Range&) = delete;
-};
 
 // ------------------------------------------------------------ device info --
 
@@ -53,6 +33,8 @@ std::atomic<int> g_x_perm_copy{MOE_X_PERM_COPY_AUTO};
 std::atomic<int> g_router{MOE_ROUTER_OPT_AUTO};
 std::atomic<unsigned long long> g_launch_count{0};
 
+}  // namespace
+
 int num_sms_current()
 {
     int dev = 0;
@@ -64,6 +46,8 @@ int num_sms_current()
     g_num_sms[dev].store(n, std::memory_order_relaxed);
     return n;
 }
+
+namespace {
 
 // ---------------------------------------------------------- tensor maps --
 
@@ -103,6 +87,21 @@ bool encode_map_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t ou
                     swizzle_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
                     : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                           : CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+bool encode_map_e4m3(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t groups,
+                     uint32_t box_inner, uint32_t box_rows)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {inner, rows, groups};
+    cuuint64_t strides[2] = {inner, inner * rows};
+    cuuint32_t box[3] = {box_inner, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, groups ? 3 : 2, const_cast<void*>(base), dims, strides, box,
+                    estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
@@ -201,8 +200,6 @@ moe_plan plan_of(const moe_dims& d)
 
 // ------------------------------------------------------------ workspace --
 
-size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
-
 struct Layout {
     size_t err, tile, hist, idx, w, counts, offsets, src, inv, xp, h, hs, slot, arrive, sgate, logits, ready;
     size_t tc_wgt, tc_wnorm, tc_nflag, tc_tok, tc_cand, tc_ftok, tc_fcand, tc_fsel, tc_fselv, tc_pairs, tc_lg,
@@ -253,14 +250,14 @@ Layout layout_of(const moe_dims& d)
 
 // ----------------------------------------------------------- validation --
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 moe_status check_ws(const moe_dims& d, void* ws, size_t ws_bytes)
 {
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOE_ERR_WORKSPACE;
     if (ws_bytes < layout_of(d).total) return MOE_ERR_WORKSPACE;
     return MOE_OK;
 }
+
+}  // namespace
 
 moe_status finish(cudaError_t e, void* ws, cudaStream_t s)
 {
@@ -272,17 +269,7 @@ moe_status finish(cudaError_t e, void* ws, cudaStream_t s)
     return MOE_OK;
 }
 
-#define MOE_TRY(expr)                                  \
-    do {                                               \
-        cudaError_t e_ = (expr);                       \
-        if (e_ != cudaSuccess) return MOE_ERR_CUDA;    \
-    } while (0)
-
-#define MOE_TRY_STATUS(expr)                           \
-    do {                                               \
-        moe_status s_ = (expr);                        \
-        if (s_ != MOE_OK) return s_;                   \
-    } while (0)
+namespace {
 
 unsigned char* bytes(void* p) { return static_cast<unsigned char*>(p); }
 
@@ -485,6 +472,49 @@ moe_status check_dims(const moe_dims* d)
 
 namespace moe {
 
+Routed routed_of(const moe_dims& d, const moe_routing_out* routing, unsigned char* w)
+{
+    const Layout L = layout_of(d);
+    auto pick_i = [&](int32_t* user, size_t off) { return user ? user : reinterpret_cast<int32_t*>(w + off); };
+    Routed r;
+    r.topk_idx = pick_i(routing ? routing->topk_idx : nullptr, L.idx);
+    r.topk_w = (routing && routing->topk_w) ? routing->topk_w : reinterpret_cast<float*>(w + L.w);
+    r.counts = pick_i(routing ? routing->counts : nullptr, L.counts);
+    r.offsets = pick_i(routing ? routing->offsets : nullptr, L.offsets);
+    r.src_row = pick_i(routing ? routing->src_row : nullptr, L.src);
+    r.inv_pos = pick_i(routing ? routing->inv_pos : nullptr, L.inv);
+    r.tile_start = reinterpret_cast<int32_t*>(w + L.tile);
+    r.x_perm = w + L.xp;
+    r.h = w + L.h;
+    r.h_shared = w + L.hs;
+    r.slot = reinterpret_cast<float*>(w + L.slot);
+    r.shared_gate = reinterpret_cast<float*>(w + L.sgate);
+    return r;
+}
+
+moe_status route_and_sort(const moe_dims& d, int router, const moe_bf16* x, const moe_bf16* Wg, const float* bias,
+                          const moe_gating* gating, const Routed& r, unsigned char* w, uint32_t* err, int sms,
+                          const moe_stage_events* events, Range& stage, cudaStream_t s)
+{
+    const Layout L = layout_of(d);
+    record(events ? events->before_route : nullptr, s);
+    RouteArgs ra{x, Wg, bias, r.topk_idx, r.topk_w, d.T, d.H, d.E, d.k};
+    ra.renorm = gating ? (gating->renormalize != 0) : 1;
+    ra.err = err;
+    ra.logits = reinterpret_cast<float*>(w + L.logits);
+    if (router == MOE_ROUTER_TENSOR)
+        MOE_TRY(launch_route_tc(ra, tc_args_of(L, w), sms, s));
+    else
+        MOE_TRY(launch_route(ra, sms, s));
+
+    stage.next("moe/permute");
+    record(events ? events->before_permute : nullptr, s);
+    PermuteArgs pa{r.topk_idx, r.counts, r.offsets, r.src_row, r.inv_pos, r.tile_start,
+                   reinterpret_cast<int32_t*>(w + L.hist), err, d.T * d.k, d.E};
+    MOE_TRY(launch_permute(pa, s));
+    return MOE_OK;
+}
+
 // The layer call with an optional router override (router_force >= 0): the
 // host-buffer call runs every chunk with the router kernel family the whole
 // batch would take, so that a chunk's gate weights are the whole batch's
@@ -515,15 +545,8 @@ moe_status layer_forward_impl(const moe_dims* dims, const moe_bf16* x, const moe
     const Layout L = layout_of(d);
     unsigned char* w = bytes(ws);
     uint32_t* err = reinterpret_cast<uint32_t*>(w + L.err);
-    auto pick_i = [&](int32_t* user, size_t off) { return user ? user : reinterpret_cast<int32_t*>(w + off); };
-    int32_t* idx = pick_i(routing ? routing->topk_idx : nullptr, L.idx);
-    float* tw = (routing && routing->topk_w) ? routing->topk_w : reinterpret_cast<float*>(w + L.w);
-    int32_t* counts = pick_i(routing ? routing->counts : nullptr, L.counts);
-    int32_t* offsets = pick_i(routing ? routing->offsets : nullptr, L.offsets);
-    int32_t* src = pick_i(routing ? routing->src_row : nullptr, L.src);
-    int32_t* inv = pick_i(routing ? routing->inv_pos : nullptr, L.inv);
-    int32_t* tile = reinterpret_cast<int32_t*>(w + L.tile);
-    float* slot = reinterpret_cast<float*>(w + L.slot);
+    const Routed rt = routed_of(d, routing, w);
+    float* slot = rt.slot;
     const int64_t R = d.T * d.k;
     const int32_t n_slots = d.k + (d.F_shared > 0 ? 1 : 0);
     int32_t* arrive = reinterpret_cast<int32_t*>(w + L.arrive);
@@ -540,21 +563,7 @@ moe_status layer_forward_impl(const moe_dims* dims, const moe_bf16* x, const moe
 
     Range layer_range("moe/layer_forward");
     Range stage("moe/route");
-    record(events ? events->before_route : nullptr, s);
-    RouteArgs ra{x, Wg, bias, idx, tw, d.T, d.H, d.E, d.k};
-    ra.renorm = gating ? (gating->renormalize != 0) : 1;
-    ra.err = err;
-    ra.logits = reinterpret_cast<float*>(w + L.logits);
-    if (plan.router == MOE_ROUTER_TENSOR)
-        MOE_TRY(launch_route_tc(ra, tc_args_of(L, w), sms, s));
-    else
-        MOE_TRY(launch_route(ra, sms, s));
-
-    stage.next("moe/permute");
-    record(events ? events->before_permute : nullptr, s);
-    PermuteArgs pa{idx, counts, offsets, src, inv, tile, reinterpret_cast<int32_t*>(w + L.hist), err,
-                   R, d.E};
-    MOE_TRY(launch_permute(pa, s));
+    MOE_TRY_STATUS(route_and_sort(d, plan.router, x, Wg, bias, gating, rt, w, err, sms, events, stage, s));
 
     const bool permuted = (plan.gemm0_a == MOE_GEMM0_A_PERMUTED);
     const bool cp_gather = (plan.gemm0_a == MOE_GEMM0_A_CP_GATHER);
@@ -562,15 +571,15 @@ moe_status layer_forward_impl(const moe_dims* dims, const moe_bf16* x, const moe
     // x_perm: copied by GEMM0's copy warps while it runs, or by a kernel first
     const bool copy_inline = permuted && plan.x_perm_copy == MOE_X_PERM_COPY_INLINE;
     if (permuted && !copy_inline)
-        MOE_TRY(launch_scatter_rows(x, idx, inv, offsets + d.E, xp, d.T, d.H, d.k, d.E, err, sms, s));
+        MOE_TRY(launch_scatter_rows(x, rt.topk_idx, rt.inv_pos, rt.offsets + d.E, xp, d.T, d.H, d.k, d.E, err, sms, s));
 
     // both routed GEMMs in one launch (dense A only)
     const bool fuse_gemms = plan.gemm_fusion == MOE_GEMM_FUSION_ON;
 
     stage.next("moe/experts");
     record(events ? events->before_gemm0 : nullptr, s);
-    MOE_TRY_STATUS(run_expert_gemms(d, (int32_t)R, d.F, d.E, d.k, x, permuted ? xp : nullptr, src,
-                                    tile, offsets, W1, W3, W2, tw, slot,
+    MOE_TRY_STATUS(run_expert_gemms(d, (int32_t)R, d.F, d.E, d.k, x, permuted ? xp : nullptr, rt.src_row,
+                                    rt.tile_start, rt.offsets, W1, W3, W2, rt.topk_w, slot,
                                     reinterpret_cast<uint16_t*>(w + L.h), err, sms, s,
                                     events ? events->before_gemm1 : nullptr,
                                     // with a shared expert, only its GEMM1 (the last) combines

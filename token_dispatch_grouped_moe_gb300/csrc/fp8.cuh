@@ -1,0 +1,163 @@
+// fp8.cuh -- what the 8-bit kernels share: block scales, e4m3 conversion and
+// packed fp32 arithmetic (device), and the kernels' launchers (host). Internal.
+//
+// A value v of a block of 128 is held as e4m3 q with the block's fp32 scale:
+//   scale = max(largest |v| of the block, 2^-100) / 448,  q = e4m3(v / scale),
+// rounded to nearest, ties to even (448 is the largest e4m3 value; the floor
+// keeps the scale and its reciprocal finite for a block of zeros). A NaN in a
+// block makes its scale and so the whole block NaN.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/moe.h"
+
+namespace moe {
+
+constexpr int kFp8Block = 128;        // values that share one scale
+constexpr float kE4m3Max = 448.0f;
+constexpr float kAmaxMin = 0x1p-100f;
+
+// K splits of the products (fp8_gemm.cu): at most kFp8MaxItems parts of one
+// 128 x 256 fp32 tile each in the workspace.
+constexpr int kFp8MaxSplit = 16;
+constexpr int kFp8MaxItems = 320;
+constexpr int kFp8ItemCost = 3;       // fixed cost of an item, in K blocks
+constexpr int kFp8JoinCost = 4;       // and of joining the parts of a tile
+constexpr size_t kFp8PartBytes = (size_t)128 * 256 * 4;
+
+// The workspace of the 8-bit products: the error word, the tiles' tickets
+// (zero between calls), the parts.
+constexpr size_t kFp8TicketOffset = 256;
+constexpr size_t kFp8PartOffset = 256 + ((size_t)kFp8MaxItems * 4 + 255) / 256 * 256;
+constexpr size_t kFp8WorkspaceBytes = kFp8PartOffset + kFp8MaxItems * kFp8PartBytes;
+
+enum Fp8GemmMode { kFp8Gated = 0, kFp8ProductBf16 = 1, kFp8ProductF32 = 2 };
+
+struct Fp8GemmArgs {
+    int32_t R;                  // rows of A
+    int32_t N;                  // output columns (gated: F)
+    int32_t K;
+    int32_t G;                  // groups (experts)
+    const int32_t* offsets;     // [G+1], or null: one group of R rows
+    const float* a_scale;       // [R, ceil(K/128)]
+    const float* w0_scale;      // [G, ceil(N/128), ceil(K/128)]  (gated: of W1)
+    const float* w1_scale;      // gated: of W3
+    void* out;                  // gated: e4m3 [R, N]; product: bf16 or fp32 [R, N] or slot[k, T, N]
+    float* out_scale;           // gated: [R, ceil(N/128)]
+    const int32_t* src_row;     // product: scatter to slots, or null
+    const float* topk_w;        // product with src_row: the gate weights by assignment
+    int32_t k;
+    int64_t T;
+    int32_t* ticket;            // [kFp8MaxItems], zero
+    float4* part;               // [kFp8MaxItems] parts of kFp8PartBytes
+    uint32_t* err;
+};
+
+// tmA: A [R, K] e4m3, box 128 x 128; tmB0 / tmB1: weights [G, N, K], box 128 x
+// 256 (gated: 128 x 64 of W1 and of W3); 128-byte swizzle.
+cudaError_t launch_fp8_gemm(Fp8GemmMode mode, const CUtensorMap& tmA, const CUtensorMap& tmB0,
+                            const CUtensorMap& tmB1, const Fp8GemmArgs& a, int num_sms, cudaStream_t s);
+
+struct Fp8NormArgs {
+    const void* x;              // [T, H], rows x_stride elements apart
+    const void* residual;       // or null
+    const void* weight;         // [H] or null (ones)
+    void* sum;                  // x + residual, rounded to the type, or null
+    void* y;                    // [T, H] or null
+    uint8_t* q;                 // [T, H] e4m3
+    float* scale;               // [T, ceil(H/128)]
+    int64_t T, x_stride, residual_stride, sum_stride;
+    int32_t H;
+    float eps;
+};
+cudaError_t launch_fp8_norm(moe_dtype dtype, const Fp8NormArgs& a, cudaStream_t s);
+
+// w [E, K, N] bf16 -> q [E, N, K] e4m3 and the scales [E, ceil(N/128), ceil(K/128)] of its 128 x 128 blocks
+cudaError_t launch_fp8_quantize_weight(const uint16_t* w, uint8_t* q, float* scale, int32_t E, int32_t K, int32_t N,
+                                       cudaStream_t s);
+
+// q_perm[p] = q[src_row[p] / k] and its scales, for the assignments with an id
+// in [0, E), from the token side (each row read once)
+cudaError_t launch_fp8_dispatch(const uint8_t* q, const float* scale, const int32_t* topk_idx, const int32_t* inv_pos,
+                                const int32_t* r_valid, uint8_t* q_perm, float* scale_perm, int64_t T, int32_t H,
+                                int32_t k, int32_t E, uint32_t* err, int num_sms, cudaStream_t s);
+
+#ifdef __CUDACC__
+// maximum that keeps a NaN of either operand
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float fp8_scale(float amax) { return max_nan(amax, kAmaxMin) / kE4m3Max; }
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
+{
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+__device__ __forceinline__ uint64_t pack_f32x2(uint32_t lo, uint32_t hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+// two fp32 fused multiply-adds: a * b + c in each half
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// x / (1 + e^-x); e^-x = inf for x below about -88 gives -0
+__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
+
+__device__ __forceinline__ void store8(float* dst, const float (&o)[8])
+{
+    *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<float4*>(dst + 4) = make_float4(o[4], o[5], o[6], o[7]);
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float a, float b)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16* dst, const float (&o)[8])
+{
+    *reinterpret_cast<uint4*>(dst) =
+        make_uint4(bf16x2(o[0], o[1]), bf16x2(o[2], o[3]), bf16x2(o[4], o[5]), bf16x2(o[6], o[7]));
+}
+
+__device__ __forceinline__ uint32_t f16x2(float a, float b)
+{
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void store8(__half* dst, const float (&o)[8])
+{
+    *reinterpret_cast<uint4*>(dst) =
+        make_uint4(f16x2(o[0], o[1]), f16x2(o[2], o[3]), f16x2(o[4], o[5]), f16x2(o[6], o[7]));
+}
+#endif
+
+}  // namespace moe

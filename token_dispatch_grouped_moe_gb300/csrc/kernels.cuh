@@ -75,6 +75,12 @@ cudaError_t launch_route_tc(const RouteArgs& a, RouteTcArgs c, int num_sms, cuda
 bool encode_map_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
                    uint32_t box_outer, int swizzle_bytes);
 
+// A TMA tensor map of row-major e4m3 matrices [groups, rows, inner] (groups 0:
+// one matrix, a 2D map) with box {box_inner, box_rows}, a 128-byte swizzle;
+// elements outside each matrix read as zero.
+bool encode_map_e4m3(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t groups,
+                     uint32_t box_inner, uint32_t box_rows);
+
 // scale[t] = 1 / (1 + exp(-x[t] . wsg)) (the shared expert's sigmoid gate)
 cudaError_t launch_shared_gate(const uint16_t* x, const uint16_t* wsg, float* scale, int64_t T,
                                int32_t H, int num_sms, cudaStream_t s);

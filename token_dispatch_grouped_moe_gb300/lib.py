@@ -25,7 +25,8 @@ EXPORTS = ["moe_version", "moe_status_string", "moe_workspace_size", "moe_check"
            "moe_permute", "moe_expert_ffn", "moe_combine", "moe_layer_forward", "moe_set_option",
            "moe_get_option", "moe_permute_static", "moe_route_ex", "moe_layer_forward_ex",
            "moe_layer_plan", "moe_selftest_wait_timeout", "moe_launch_count", "moe_selftest_route_tc",
-           "moe_layer_forward_host", "moe_host_chunks"]
+           "moe_layer_forward_host", "moe_host_chunks", "moe_fp8_workspace_size", "moe_add_rmsnorm_fp8",
+           "moe_fp8_quantize_weight", "moe_fp8_matmul", "moe_fp8_gated", "moe_fp8_layer_forward"]
 
 OPT_GEMM0_A = 0
 GEMM0_A_PERMUTED = 0      # dispatch copies token rows to x_perm; GEMM0 loads dense tiles
@@ -83,6 +84,10 @@ class Plan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("router", "gemm0_a", "combine", "gemm_fusion", "tile_m",
                                               "tile_n", "tile_k", "stages", "cta_group",
                                               "cta_group_gemm1", "x_perm_copy")]
+
+
+class Fp8Ffn(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w1", "w1_scale", "w3", "w3_scale", "w2", "w2_scale")]
 
 
 ROUTER_STREAM, ROUTER_SLICED, ROUTER_CLUSTER, ROUTER_BLOCK, ROUTER_TENSOR = 0, 1, 2, 3, 4
@@ -145,6 +150,20 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_layer_forward_host.argtypes = [D, P, P, P, P, P, P, P, P, P, P, P, P, i32, P, sz, P]
     lib.moe_host_chunks.restype = i32
     lib.moe_host_chunks.argtypes = [D]
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    lib.moe_fp8_workspace_size.restype = sz
+    lib.moe_fp8_workspace_size.argtypes = [D]
+    lib.moe_add_rmsnorm_fp8.restype = ctypes.c_int
+    lib.moe_add_rmsnorm_fp8.argtypes = [i64, i32, i32, P, i64, P, i64, P, f32, P, i64, P, P, P, P]
+    lib.moe_fp8_quantize_weight.restype = ctypes.c_int
+    lib.moe_fp8_quantize_weight.argtypes = [i32, i32, i32, P, P, P, P]
+    lib.moe_fp8_matmul.restype = ctypes.c_int
+    lib.moe_fp8_matmul.argtypes = [i64, i32, i32, i32, P, P, P, P, P, i32, P, P, sz, P]
+    lib.moe_fp8_gated.restype = ctypes.c_int
+    lib.moe_fp8_gated.argtypes = [i64, i32, i32, i32, P, P, P, P, P, P, P, P, P, P, sz, P]
+    lib.moe_fp8_layer_forward.restype = ctypes.c_int
+    lib.moe_fp8_layer_forward.argtypes = [D, P, P, P, P, P, ctypes.POINTER(Gating), ctypes.POINTER(Fp8Ffn),
+                                          ctypes.POINTER(Fp8Ffn), P, ctypes.POINTER(RoutingOut), P, sz, P]
     _lib = lib
     return lib
 
@@ -425,3 +444,224 @@ class MoELayer:
         return layer_forward(self.dims(T), x, self.Wg, self.W1, self.W3, self.W2, self.workspace(T),
                              self.bias, self.W1s, self.W3s, self.W2s, out=out, routing=routing,
                              events=events, stream=stream)
+
+
+# ------------------------------------------------------------------ 8 bits --
+
+FP8 = torch.float8_e4m3fn
+FP8_BLOCK = 128   # values that share one scale
+_DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _fp8_blocks(n: int) -> int:
+    return (n + FP8_BLOCK - 1) // FP8_BLOCK
+
+
+def _expect(t, name, shape, dtype, device):
+    """Argument check: a contiguous tensor of this shape and type on this device."""
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _rows(t, name, shape, dtype, device):
+    """Argument check: rows of contiguous elements, any row stride."""
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)} on {device} with contiguous rows, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def fp8_workspace_size(dims: Dims | None = None) -> int:
+    return int(load().moe_fp8_workspace_size(None if dims is None else ctypes.byref(dims)))
+
+
+def fp8_workspace(dims: Dims | None = None, device=None) -> torch.Tensor:
+    """A zeroed workspace of :func:`fp8_matmul` and :func:`fp8_gated` (any
+    sizes), or of :func:`fp8_layer_forward` for ``dims``."""
+    n = fp8_workspace_size(dims)
+    if n == 0:
+        raise MoeError(1, "fp8_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def add_rmsnorm_fp8(x, weight=None, residual=None, eps=1e-6, want_y=True, sum_out=None, stream=None):
+    """r = x + residual, y = r / sqrt(mean(r^2) + eps) * weight for the rows of
+    x [T,H] (bf16, fp16 or fp32; any row stride), and y in e4m3 with a scale
+    for each row's block of 128. Returns (r, y, q, scale): r is None without a
+    residual (``sum_out`` gives its memory: x and residual are allowed), y None
+    with ``want_y=False``."""
+    T, H = x.shape
+    dev = x.device
+    if x.dtype not in _DTYPE:
+        raise ValueError(f"x: bf16, fp16 or fp32 expected, got {x.dtype}")
+    _rows(x, "x", (T, H), x.dtype, dev)
+    if weight is not None:
+        _expect(weight, "weight", (H,), x.dtype, dev)
+    if residual is not None:
+        _rows(residual, "residual", (T, H), x.dtype, dev)
+        if sum_out is None:
+            sum_out = torch.empty(T, H, dtype=x.dtype, device=dev)
+    if sum_out is not None:
+        _rows(sum_out, "sum_out", (T, H), x.dtype, dev)
+    y = torch.empty(T, H, dtype=x.dtype, device=dev) if want_y else None
+    q = torch.empty(T, H, dtype=FP8, device=dev)
+    scale = torch.empty(T, _fp8_blocks(H), dtype=torch.float32, device=dev)
+    _ok(load().moe_add_rmsnorm_fp8(T, H, _DTYPE[x.dtype], x.data_ptr(), x.stride(0),
+                                   None if residual is None else residual.data_ptr(),
+                                   0 if residual is None else residual.stride(0),
+                                   None if weight is None else weight.data_ptr(), eps,
+                                   None if sum_out is None else sum_out.data_ptr(),
+                                   0 if sum_out is None else sum_out.stride(0),
+                                   None if y is None else y.data_ptr(), q.data_ptr(), scale.data_ptr(),
+                                   _stream(stream)), "moe_add_rmsnorm_fp8")
+    return sum_out, y, q, scale
+
+
+def fp8_quantize_weight(w, stream=None):
+    """w [G,K,N] bf16 -> (q [G,N,K] e4m3, scale [G, ceil(N/128), ceil(K/128)]):
+    a weight's layout for the 8-bit products, made once."""
+    G, K, N = w.shape
+    _expect(w, "w", (G, K, N), torch.bfloat16, w.device)
+    q = torch.empty(G, N, K, dtype=FP8, device=w.device)
+    scale = torch.empty(G, _fp8_blocks(N), _fp8_blocks(K), dtype=torch.float32, device=w.device)
+    _ok(load().moe_fp8_quantize_weight(G, K, N, w.data_ptr(), q.data_ptr(), scale.data_ptr(), _stream(stream)),
+        "moe_fp8_quantize_weight")
+    return q, scale
+
+
+def _check_product(a, a_scale, weights, offsets, ws):
+    """The checks that the two products share; (R, K, N, G)."""
+    R, K = a.shape
+    w = weights[0][1]
+    G, N = w.shape[0], w.shape[1]
+    dev = a.device
+    _expect(a, "a", (R, K), FP8, dev)
+    _expect(a_scale, "a_scale", (R, _fp8_blocks(K)), torch.float32, dev)
+    for name, q, scale in weights:
+        _expect(q, name, (G, N, K), FP8, dev)
+        _expect(scale, name + "_scale", (G, _fp8_blocks(N), _fp8_blocks(K)), torch.float32, dev)
+    if offsets is not None:
+        _expect(offsets, "offsets", (G + 1,), torch.int32, dev)
+    _expect(ws, "ws", (ws.numel(),), torch.uint8, dev)
+    return R, K, N, G
+
+
+def fp8_matmul(a, a_scale, w, w_scale, ws, offsets=None, out_dtype=torch.bfloat16, out=None, stream=None):
+    """out[p] = a[p] w[g]^T for the rows p of group g, offsets[g] <= p <
+    offsets[g+1] (one group without offsets): a [R,K] and w [G,N,K] in e4m3
+    with their block scales, out [R,N] bf16 or fp32. Rows outside every group
+    are not written."""
+    R, K, N, G = _check_product(a, a_scale, (("w", w, w_scale),), offsets, ws)
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"out_dtype: bf16 or fp32 expected, got {out_dtype}")
+    if out is None:
+        out = torch.empty(R, N, dtype=out_dtype, device=a.device)
+    else:
+        _expect(out, "out", (R, N), out_dtype, a.device)
+    _ok(load().moe_fp8_matmul(R, K, N, G, a.data_ptr(), a_scale.data_ptr(),
+                              None if offsets is None else offsets.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+                              _DTYPE[out_dtype], out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)),
+        "moe_fp8_matmul")
+    return out
+
+
+def fp8_gated(a, a_scale, w1, w1_scale, w3, w3_scale, ws, offsets=None, stream=None):
+    """h[p] = silu(a[p] w1[g]^T) * (a[p] w3[g]^T) for the rows of each group as
+    in :func:`fp8_matmul`, quantized: (h [R,F] e4m3, scale [R, ceil(F/128)])."""
+    R, K, F, G = _check_product(a, a_scale, (("w1", w1, w1_scale), ("w3", w3, w3_scale)), offsets, ws)
+    h = torch.empty(R, F, dtype=FP8, device=a.device)
+    scale = torch.empty(R, _fp8_blocks(F), dtype=torch.float32, device=a.device)
+    _ok(load().moe_fp8_gated(R, K, F, G, a.data_ptr(), a_scale.data_ptr(),
+                             None if offsets is None else offsets.data_ptr(), w1.data_ptr(), w1_scale.data_ptr(),
+                             w3.data_ptr(), w3_scale.data_ptr(), h.data_ptr(), scale.data_ptr(), ws.data_ptr(),
+                             ws.numel(), _stream(stream)), "moe_fp8_gated")
+    return h, scale
+
+
+@dataclass
+class Fp8Weights:
+    """One expert set's 8-bit weights, from bf16 W1, W3 [E,H,F] and W2 [E,F,H]."""
+    w1: torch.Tensor
+    w1_scale: torch.Tensor
+    w3: torch.Tensor
+    w3_scale: torch.Tensor
+    w2: torch.Tensor
+    w2_scale: torch.Tensor
+
+    @classmethod
+    def from_bf16(cls, W1, W3, W2, stream=None) -> "Fp8Weights":
+        return cls(*(t for w in (W1, W3, W2) for t in fp8_quantize_weight(w, stream=stream)))
+
+    def _struct(self, E, H, F, device) -> Fp8Ffn:
+        for n, (N, K) in {"w1": (F, H), "w3": (F, H), "w2": (H, F)}.items():
+            _expect(getattr(self, n), n, (E, N, K), FP8, device)
+            _expect(getattr(self, n + "_scale"), n + "_scale", (E, _fp8_blocks(N), _fp8_blocks(K)), torch.float32,
+                    device)
+        return Fp8Ffn(*(getattr(self, n).data_ptr() for n, _ in Fp8Ffn._fields_))
+
+
+def fp8_layer_forward(dims: Dims, x, xq, xq_scale, Wg, routed: Fp8Weights, ws, bias=None,
+                      shared: Fp8Weights | None = None, out=None, routing: Routing | None = None, renormalize=True,
+                      shared_gate=None, stream=None):
+    """The whole layer on 8-bit experts: the router reads x [T,H] (bf16), the
+    experts xq, xq_scale (the same rows quantized: y, q, scale of
+    :func:`add_rmsnorm_fp8`). ``ws`` from ``fp8_workspace(dims)``."""
+    T, H, dev = dims.T, dims.H, x.device
+    _expect(x, "x", (T, H), torch.bfloat16, dev)
+    _expect(xq, "xq", (T, H), FP8, dev)
+    _expect(xq_scale, "xq_scale", (T, _fp8_blocks(H)), torch.float32, dev)
+    _expect(Wg, "Wg", (H, dims.E), torch.bfloat16, dev)
+    if bias is not None:
+        _expect(bias, "bias", (dims.E,), torch.float32, dev)
+    if out is None:
+        out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    else:
+        _expect(out, "out", (T, H), torch.bfloat16, dev)
+    if dims.F_shared > 0 and shared is None:
+        raise ValueError("shared: the shared expert's weights are needed when F_shared > 0")
+    f = routed._struct(dims.E, H, dims.F, dev)
+    fs = shared._struct(1, H, dims.F_shared, dev) if dims.F_shared > 0 else None
+    r = None
+    if routing is not None:
+        r = RoutingOut(*(ctypes.c_void_p(getattr(routing, n).data_ptr()) for n in
+                         ("topk_idx", "topk_w", "counts", "offsets", "src_row", "inv_pos")))
+    g = _gating(renormalize, shared_gate)
+    _ok(load().moe_fp8_layer_forward(ctypes.byref(dims), _p(x), _p(xq), _p(xq_scale), _p(Wg), _p(bias),
+                                     ctypes.byref(g) if g is not None else None, ctypes.byref(f),
+                                     ctypes.byref(fs) if fs is not None else None, _p(out),
+                                     ctypes.byref(r) if r is not None else None, _p(ws), ws.numel(),
+                                     _stream(stream)), "moe_fp8_layer_forward")
+    return out
+
+
+class MoEFp8Layer:
+    """A pre-norm expert layer of a residual stream, served in 8 bits: the
+    residual's addition, the norm and its quantization, then the layer on
+    weights quantized once from bf16. ``forward(x, residual)`` returns (the
+    layer's output, the residual stream that the next layer adds it to)."""
+
+    def __init__(self, norm_weight, Wg, W1, W3, W2, k, bias=None, W1s=None, W3s=None, W2s=None, eps=1e-6):
+        self.norm_weight, self.Wg, self.bias, self.k, self.eps = norm_weight, Wg, bias, int(k), eps
+        self.H, self.E = Wg.shape
+        self.F = W1.shape[2]
+        self.Fs = 0 if W1s is None else W1s.shape[1]
+        self.routed = Fp8Weights.from_bf16(W1, W3, W2)
+        self.shared = None if W1s is None else Fp8Weights.from_bf16(W1s[None], W3s[None], W2s[None])
+        self._ws = None
+        self._T = None
+
+    def dims(self, T) -> Dims:
+        return make_dims(T, self.H, self.F, self.E, self.k, self.Fs)
+
+    def workspace(self, T):
+        if self._ws is None or self._T != T:
+            self._ws = fp8_workspace(self.dims(T), device=self.Wg.device)
+            self._T = T
+        return self._ws
+
+    def forward(self, x, residual=None, routing=None, stream=None):
+        T = x.shape[0]
+        r, y, q, scale = add_rmsnorm_fp8(x, self.norm_weight, residual=residual, eps=self.eps, stream=stream)
+        out = fp8_layer_forward(self.dims(T), y, q, scale, self.Wg, self.routed, self.workspace(T), bias=self.bias,
+                                shared=self.shared, routing=routing, stream=stream)
+        return out, x if residual is None else r
