@@ -1,5 +1,5 @@
-// fp8.cuh -- what the 8-bit kernels share: block scales, e4m3 conversion and
-// packed fp32 arithmetic (device), and the kernels' launchers (host). Internal.
+// fp8.cuh -- what the 8-bit kernels share: block scales, e4m3 conversion
+// (device), and the kernels' launchers (host). Internal.
 //
 // A value v of a block of 128 is held as e4m3 q with the block's fp32 scale:
 //   scale = max(largest |v| of the block, 2^-100) / 448,  q = e4m3(v / scale),
@@ -104,26 +104,6 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
     return (uint32_t)lo | ((uint32_t)hi << 16);
-}
-
-__device__ __forceinline__ uint64_t pack_f32x2(uint32_t lo, uint32_t hi)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-    return r;
-}
-
-__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-
-// two fp32 fused multiply-adds: a * b + c in each half
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
 }
 
 // x / (1 + e^-x); e^-x = inf for x below about -88 gives -0

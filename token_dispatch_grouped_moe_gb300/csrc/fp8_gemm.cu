@@ -21,7 +21,7 @@
 // of (expert, N tile, M tile, K split) items computed from the group offsets:
 //   warps 0..7  fold and epilogue: warp w reads TMEM lanes 32 (w mod 4) .. + 31
 //               (rows) and columns 128 (w / 4) .. + 127: 128 fp32 accumulators a
-//               thread, packed in pairs for fma.rn.f32x2;
+//               thread;
 //   warp 8      TMA producer: 4-stage ring of {A 128 x 128, B 256 x 128} bytes;
 //   warp 9      TMEM allocator and MMA issuer (warps 10, 11 only give registers).
 // When there are too few tiles for the SMs (few rows), K is split over several
@@ -124,12 +124,12 @@ __device__ __forceinline__ void fold_barrier()   // the fold warps only
     asm volatile("bar.sync 1, %0;" ::"n"(FOLD_THREADS) : "memory");
 }
 
-// acc[C .. C + 15] += v[0 .. 31] * f, in pairs
+// acc[C .. C + 31] += v[0 .. 31] * f
 template <int C>
-__device__ __forceinline__ void fold32(uint64_t (&acc)[64], const uint32_t (&v)[32], uint64_t f)
+__device__ __forceinline__ void fold32(float (&acc)[128], const uint32_t (&v)[32], float f)
 {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[C + i] = fma_f32x2(pack_f32x2(v[2 * i], v[2 * i + 1]), f, acc[C + i]);
+    for (int i = 0; i < 32; ++i) acc[C + i] = fmaf(__uint_as_float(v[i]), f, acc[C + i]);
 }
 
 template <bool GATED, typename OUT>
@@ -262,44 +262,46 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             __syncwarp();
         } else if (warp == 9) {
             // ============================ MMA issuer ==============================
-            if (lane == 0) {
-                int stage = 0;
-                uint32_t phase = 0;
-                int acc = 0;
-                uint32_t acc_phase = 0;
-                bool ok = true;
-                bool any = false;
-                for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
-                    const int split = w % S;
-                    const int n_kb = (split + 1) * k_blocks / S - split * k_blocks / S;
-                    for (int i = 0; i < n_kb; ++i) {
-                        if (!mbar_wait(smem_u32(&st->tempty[acc]), acc_phase ^ 1u, abort, args.err) ||
-                            !mbar_wait(smem_u32(&st->full[stage]), phase, abort, args.err)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t a_base = tiles_addr + stage * STAGE_BYTES;
-                        const uint32_t b_base = a_base + A_BYTES;
-    #pragma unroll
-                        for (int kk = 0; kk < BK / 32; ++kk) {
+            // the whole warp walks the items and waits (uniform control flow, so the
+            // descriptors stay in uniform registers); one elected lane issues
+            const uint32_t leader = elect_one_sync();
+            const uint64_t a_desc = smem_desc_sw128(tiles_addr, 16, 1024);
+            const uint64_t b_desc = smem_desc_sw128(tiles_addr + A_BYTES, 16, 1024);
+            int stage = 0;
+            uint32_t phase = 0;
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            bool ok = true;
+            bool any = false;
+            for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+                const int split = w % S;
+                const int n_kb = (split + 1) * k_blocks / S - split * k_blocks / S;
+                for (int i = 0; i < n_kb; ++i) {
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(smem_u32(&st->full[stage]), phase, abort, args.err) &&
+                                        mbar_wait(smem_u32(&st->tempty[acc]), acc_phase ^ 1u, abort, args.err));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (leader) {
+                        const uint32_t d = tmem_base + acc * BN;
+                        const uint64_t at = (uint64_t)(stage * (STAGE_BYTES >> 4));
+#pragma unroll
+                        for (int kk = 0; kk < BK / 32; ++kk)
                             // K-major A and B: each K step of 32 is 32 bytes further along the row
-                            const uint64_t ad = smem_desc_sw128(a_base + kk * 32, 16, 1024);
-                            const uint64_t bd = smem_desc_sw128(b_base + kk * 32, 16, 1024);
-                            tc_mma_f8(tmem_base + acc * BN, ad, bd, IDESC, kk != 0 ? 1u : 0u);
-                        }
-                        any = true;
-                        tc_commit(smem_u32(&st->empty[stage]));
+                            tc_mma_f8(d, a_desc + at + 2 * kk, b_desc + at + 2 * kk, IDESC, kk != 0 ? 1u : 0u);
+                        // one commit for the block: the fold warps give the stage back
                         tc_commit(smem_u32(&st->tfull[acc]));
-                        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
                     }
+                    __syncwarp();
+                    any = true;
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
                 }
-                if (!ok && any) {
-                    // drain: every MMA issued so far must finish before TMEM is freed
-                    tc_commit(smem_u32(&st->drain));
-                    mbar_wait_drain(smem_u32(&st->drain), 0);
-                }
+            }
+            if (!ok && any && leader) {
+                // drain: every MMA issued so far must finish before TMEM is freed
+                tc_commit(smem_u32(&st->drain));
+                mbar_wait_drain(smem_u32(&st->drain), 0);
             }
             __syncwarp();
         }
@@ -310,6 +312,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         const int r = (warp & 3) * 32 + lane;        // row of the tile = TMEM lane
         const uint32_t t_row = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + half * 128;
         const int n_blocks = (args.N + kFp8Block - 1) / kFp8Block;
+        int stage = 0;
         int buf = 0;
         uint32_t buf_phase = 0;
         uint32_t parity = 0;   // which amax buffer this tile uses
@@ -321,9 +324,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             const bool valid = r < it.rows;
             const int p = it.row0 + r;
             const int kb0 = it.split * k_blocks / S, kb1 = (it.split + 1) * k_blocks / S;
-            uint64_t acc[64];
+            float acc[128];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i] = 0;
+            for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
             const float* sa = args.a_scale + (int64_t)min(p, args.R - 1) * k_blocks;
             // gated: the slice's block of W1 and of W3; product: this half's block
             const int nb = GATED ? it.n_tile : min(2 * it.n_tile + half, n_blocks - 1);
@@ -341,25 +344,26 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t t = t_row + buf * BN;
-                const uint64_t p0 = pack_f32x2(__float_as_uint(c0), __float_as_uint(c0));
-                const uint64_t p1 = pack_f32x2(__float_as_uint(c1), __float_as_uint(c1));
+                // the block's MMAs are done, so its stage may be loaded again
+                if (threadIdx.x == 0) mbar_arrive(smem_u32(&st->empty[stage]));
+                if (++stage == STAGES) stage = 0;
                 uint32_t u[32], v[32];
                 tmem_ld_32x32b_x32(t, u);
-                tc_wait_ld_for(u);
                 tmem_ld_32x32b_x32(t + 32, v);
-                fold32<0>(acc, u, p0);
-                tc_wait_ld_for(v);
-                tmem_ld_32x32b_x32(t + 64, u);
-                fold32<16>(acc, v, p0);
                 tc_wait_ld_for(u);
+                tc_wait_ld_for(v);
+                fold32<0>(acc, u, c0);
+                tmem_ld_32x32b_x32(t + 64, u);
+                fold32<32>(acc, v, c0);
                 tmem_ld_32x32b_x32(t + 96, v);
-                fold32<32>(acc, u, p1);
+                tc_wait_ld_for(u);
                 tc_wait_ld_for(v);
                 // TMEM is read: the tensor cores may fill this buffer again
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&st->tempty[buf]));
-                fold32<48>(acc, v, p1);
+                fold32<64>(acc, u, c1);
+                fold32<96>(acc, v, c1);
                 if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
             }
 
@@ -370,10 +374,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 if (ok && valid) {
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
-                        float4 o;
-                        unpack_f32x2(acc[2 * c], o.x, o.y);
-                        unpack_f32x2(acc[2 * c + 1], o.z, o.w);
-                        __stcg(part + c * BM, o);
+                        __stcg(part + c * BM,
+                               make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]));
                     }
                 }
                 __threadfence();
@@ -401,8 +403,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                             sum.z += v.z;
                             sum.w += v.w;
                         }
-                        acc[2 * c] = pack_f32x2(__float_as_uint(sum.x), __float_as_uint(sum.y));
-                        acc[2 * c + 1] = pack_f32x2(__float_as_uint(sum.z), __float_as_uint(sum.w));
+                        acc[4 * c] = sum.x;
+                        acc[4 * c + 1] = sum.y;
+                        acc[4 * c + 2] = sum.z;
+                        acc[4 * c + 3] = sum.w;
                     }
                 }
             }
@@ -413,14 +417,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 float h[64];
                 float amax = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float g0, g1, u0, u1;
-                    unpack_f32x2(acc[i], g0, g1);
-                    unpack_f32x2(acc[32 + i], u0, u1);
-                    h[2 * i] = silu(g0) * u0;
-                    h[2 * i + 1] = silu(g1) * u1;
+                for (int i = 0; i < 64; ++i) {
+                    h[i] = silu(acc[i]) * acc[64 + i];
                     // columns past N are zero (zero weights): they do not count
-                    amax = max_nan(amax, max_nan(fabsf(h[2 * i]), fabsf(h[2 * i + 1])));
+                    amax = max_nan(amax, fabsf(h[i]));
                 }
                 // the block's maximum: this half's and the other's
                 st->amax[parity][half][r] = amax;
@@ -467,9 +467,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         if (n0 + 8 * i < args.N) {
                             float o[8];
 #pragma unroll
-                            for (int u = 0; u < 4; ++u) unpack_f32x2(acc[4 * i + u], o[2 * u], o[2 * u + 1]);
-#pragma unroll
-                            for (int u = 0; u < 8; ++u) o[u] *= wt;
+                            for (int u = 0; u < 8; ++u) o[u] = acc[8 * i + u] * wt;
                             store8(dst + 8 * i, o);
                         }
                     }
