@@ -58,15 +58,27 @@ Fp8GemmArgs product_args(int32_t R, int32_t K, int32_t N, int32_t G, const int32
     return a;
 }
 
+// Whether a product over R rows in G groups runs two CTAs per MMA (256-row
+// tiles, a third less read from L2), by rows per group on average. Measured,
+// one CTA -> pair, us: gated K = 2048, N = 1408, 64 groups: 384 rows 163 -> 170,
+// 768: 303 -> 284, 1536: 562 -> 516; gated K = 4096, N = 14336, 8 groups: 256:
+// 266 -> 277, 512: 458 -> 448, 1024: 850 -> 793; product K = 1408, N = 2048,
+// 64 groups: 768: 195 -> 207, 1536: 371 -> 365; product K = 14336, N = 4096,
+// 8 groups: 1024: 391 -> 402; one group 4096 x 4096: 4096: 72 -> 71, 8192:
+// 125 -> 122. Fewer rows pad more in 256-row tiles; and K is split only with
+// one CTA.
+bool pair_for(int64_t R, int32_t G, bool gated) { return R >= (int64_t)(gated ? 512 : 2048) * G; }
+
 moe_status run_product(Fp8GemmArgs a, const moe_e4m3* A, Operand w, bool f32, void* out, int sms, cudaStream_t s)
 {
     CUtensorMap ma, mw;
+    const bool pair = pair_for(a.R, a.G, false);
     if (!encode_map_e4m3(&ma, A, (uint64_t)a.K, (uint64_t)a.R, 0, kFp8Block, 128) ||
-        !encode_map_e4m3(&mw, w.v, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.G, kFp8Block, 256))
+        !encode_map_e4m3(&mw, w.v, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.G, kFp8Block, fp8_box_rows(false, pair)))
         return MOE_ERR_CUDA;
     a.w0_scale = w.scale;
     a.out = out;
-    MOE_TRY(launch_fp8_gemm(f32 ? kFp8ProductF32 : kFp8ProductBf16, ma, mw, mw, a, sms, s));
+    MOE_TRY(launch_fp8_gemm(f32 ? kFp8ProductF32 : kFp8ProductBf16, pair, ma, mw, mw, a, sms, s));
     return MOE_OK;
 }
 
@@ -74,15 +86,16 @@ moe_status run_gated(Fp8GemmArgs a, const moe_e4m3* A, Operand w1, Operand w3, m
                      cudaStream_t s)
 {
     CUtensorMap ma, m1, m3;
+    const bool pair = pair_for(a.R, a.G, true);
     if (!encode_map_e4m3(&ma, A, (uint64_t)a.K, (uint64_t)a.R, 0, kFp8Block, 128) ||
-        !encode_map_e4m3(&m1, w1.v, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.G, kFp8Block, 64) ||
-        !encode_map_e4m3(&m3, w3.v, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.G, kFp8Block, 64))
+        !encode_map_e4m3(&m1, w1.v, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.G, kFp8Block, fp8_box_rows(true, pair)) ||
+        !encode_map_e4m3(&m3, w3.v, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.G, kFp8Block, fp8_box_rows(true, pair)))
         return MOE_ERR_CUDA;
     a.w0_scale = w1.scale;
     a.w1_scale = w3.scale;
     a.out = h;
     a.out_scale = h_scale;
-    MOE_TRY(launch_fp8_gemm(kFp8Gated, ma, m1, m3, a, sms, s));
+    MOE_TRY(launch_fp8_gemm(kFp8Gated, pair, ma, m1, m3, a, sms, s));
     return MOE_OK;
 }
 

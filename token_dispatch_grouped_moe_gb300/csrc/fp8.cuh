@@ -59,8 +59,9 @@ struct Fp8GemmArgs {
 };
 
 // tmA: A [R, K] e4m3, box 128 x 128; tmB0 / tmB1: weights [G, N, K], box 128 x
-// 256 (gated: 128 x 64 of W1 and of W3); 128-byte swizzle.
-cudaError_t launch_fp8_gemm(Fp8GemmMode mode, const CUtensorMap& tmA, const CUtensorMap& tmB0,
+// fp8_box_rows rows; 128-byte swizzle. pair: two CTAs per MMA.
+inline uint32_t fp8_box_rows(bool gated, bool pair) { return gated ? 64 : pair ? 128 : 256; }
+cudaError_t launch_fp8_gemm(Fp8GemmMode mode, bool pair, const CUtensorMap& tmA, const CUtensorMap& tmB0,
                             const CUtensorMap& tmB1, const Fp8GemmArgs& a, int num_sms, cudaStream_t s);
 
 struct Fp8NormArgs {
