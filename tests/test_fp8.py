@@ -312,6 +312,7 @@ PRODUCTS = [   # K, N, rows of each group
     (256, 256, [129, 1]), (2048, 272, [0, 0, 7]), (1408, 2048, [1] * 6 + [0] * 10), (400, 400, [127, 128, 129, 0, 300]),
     (4096, 1024, [1]), (4096, 1024, [40]), (14336, 256, [1, 0, 1]), (14336, 256, [2, 128, 1]), (20480, 384, [333]),
     (2048, 1408, [90 + (7 * i) % 13 for i in range(64)]), (512, 128, [1] * 256), (256, 512, [3] * 255 + [1000]),
+    (256, 320, [2085]), (400, 272, [3000, 0, 5001, 100]), (4096, 14336, [1, 1]), (2048, 40960, [17]), (16384, 512, [1]),
 ]
 
 
@@ -403,7 +404,8 @@ def test_matmul_long_output(lib, ws):
 @pytest.mark.parametrize("K,F,counts", [(16, 16, [1]), (128, 64, [0, 3]), (144, 144, [3, 0, 130]), (256, 192, [129, 1]),
                                         (512, 128, [128]), (2048, 1408, [1] * 6 + [0] * 10), (4096, 272, [1, 1]),
                                         (4096, 1024, [40]), (8192, 128, [2, 128, 1]), (400, 400, [127, 128, 129, 0, 300]),
-                                        (2048, 1408, [90 + (7 * i) % 13 for i in range(64)]), (128, 256, [1] * 256)],
+                                        (2048, 1408, [90 + (7 * i) % 13 for i in range(64)]), (128, 256, [1] * 256),
+                                        (256, 272, [600]), (400, 144, [1000, 0, 257, 900]), (4096, 14336, [1, 0, 2])],
                          ids=lambda v: str(v) if isinstance(v, int) else f"{len(v)}g{sum(v)}r")
 def test_gated(lib, ws, K, F, counts):
     g = gen(K + F + sum(counts))

@@ -30,7 +30,7 @@ moe_status check_product(int64_t R, int32_t K, int32_t N, int32_t G, bool groupe
     if (!grouped && G != 1) return MOE_ERR_INVALID_ARG;
     if (K % 16 || N % 16 || G > 256 || R >= ((int64_t)1 << 31) - 256) return MOE_ERR_UNSUPPORTED;
     // tiles are counted in 32 bits
-    if ((R / 128 + G) * ((N + 127) / 128) >= ((int64_t)1 << 31) / kFp8MaxSplit) return MOE_ERR_UNSUPPORTED;
+    if ((R / 128 + G) * ((N + 127) / 128) >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
@@ -53,7 +53,7 @@ Fp8GemmArgs product_args(int32_t R, int32_t K, int32_t N, int32_t G, const int32
     a.k = 1;
     a.T = R;
     a.ticket = reinterpret_cast<int32_t*>(w + kFp8TicketOffset);
-    a.part = reinterpret_cast<float4*>(w + kFp8PartOffset);
+    a.part = reinterpret_cast<float*>(w + kFp8PartOffset);
     a.err = reinterpret_cast<uint32_t*>(ws);
     return a;
 }

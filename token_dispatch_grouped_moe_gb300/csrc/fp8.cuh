@@ -22,19 +22,20 @@ constexpr int kFp8Block = 128;        // values that share one scale
 constexpr float kE4m3Max = 448.0f;
 constexpr float kAmaxMin = 0x1p-100f;
 
-// K splits of the products (fp8_gemm.cu): at most kFp8MaxItems parts of one
-// 128 x 256 fp32 tile each in the workspace.
+// Cut tiles of the products (fp8_gemm.cu): their parts together hold at most
+// kFp8PartRows rows of 256 fp32 sums in the workspace; costs in K blocks.
 constexpr int kFp8MaxSplit = 16;
-constexpr int kFp8MaxItems = 320;
-constexpr int kFp8ItemCost = 3;       // fixed cost of an item, in K blocks
-constexpr int kFp8JoinCost = 4;       // and of joining the parts of a tile
-constexpr size_t kFp8PartBytes = (size_t)128 * 256 * 4;
+constexpr int kFp8MaxTickets = 512;
+constexpr int kFp8PartRows = 40960;
+constexpr float kFp8TileCost = 1.5f;
+constexpr float kFp8CutCost = 7.0f;
+constexpr float kFp8JoinCost = 1.4f;
 
 // The workspace of the 8-bit products: the error word, the tiles' tickets
 // (zero between calls), the parts.
 constexpr size_t kFp8TicketOffset = 256;
-constexpr size_t kFp8PartOffset = 256 + ((size_t)kFp8MaxItems * 4 + 255) / 256 * 256;
-constexpr size_t kFp8WorkspaceBytes = kFp8PartOffset + kFp8MaxItems * kFp8PartBytes;
+constexpr size_t kFp8PartOffset = 256 + (size_t)kFp8MaxTickets * 4;
+constexpr size_t kFp8WorkspaceBytes = kFp8PartOffset + (size_t)kFp8PartRows * 256 * 4;
 
 enum Fp8GemmMode { kFp8Gated = 0, kFp8ProductBf16 = 1, kFp8ProductF32 = 2 };
 
@@ -53,8 +54,8 @@ struct Fp8GemmArgs {
     const float* topk_w;        // product with src_row: the gate weights by assignment
     int32_t k;
     int64_t T;
-    int32_t* ticket;            // [kFp8MaxItems], zero
-    float4* part;               // [kFp8MaxItems] parts of kFp8PartBytes
+    int32_t* ticket;            // [kFp8MaxTickets], zero
+    float* part;                // [kFp8PartRows, 256]
     uint32_t* err;
 };
 
@@ -126,6 +127,16 @@ __device__ __forceinline__ void store8(__nv_bfloat16* dst, const float (&o)[8])
 {
     *reinterpret_cast<uint4*>(dst) =
         make_uint4(bf16x2(o[0], o[1]), bf16x2(o[2], o[3]), bf16x2(o[4], o[5]), bf16x2(o[6], o[7]));
+}
+
+__device__ __forceinline__ void store4(float* dst, float a, float b, float c, float d)
+{
+    *reinterpret_cast<float4*>(dst) = make_float4(a, b, c, d);
+}
+
+__device__ __forceinline__ void store4(__nv_bfloat16* dst, float a, float b, float c, float d)
+{
+    *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2(a, b), bf16x2(c, d));
 }
 
 __device__ __forceinline__ uint32_t f16x2(float a, float b)

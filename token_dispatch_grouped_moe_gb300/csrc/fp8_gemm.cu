@@ -18,7 +18,7 @@
 // other into their accumulators.
 //
 // Kernel shape: one CTA per SM (384 threads), persistent over a static schedule
-// of (expert, N tile, M tile, K split) items computed from the group offsets:
+// of (expert, N tile, M tile) tiles computed from the group offsets:
 //   warps 0..7  fold and epilogue: warp w reads TMEM lanes 32 (w mod 4) .. + 31
 //               (rows) and columns 128 (w / 4) .. + 127: 128 fp32 accumulators a
 //               thread;
@@ -28,11 +28,12 @@
 // CTA pairs (PAIR): a 2-CTA cluster shares one tcgen05.mma.cta_group::2 of M =
 // 256; both CTAs' boxes complete on rank 0's barrier, rank 0 issues, its commit
 // arrives in both CTAs, and both CTAs' fold warps release a buffer on rank 0.
-// When there are too few tiles for the SMs (few rows), K is split over several
-// items of one tile; each writes its fp32 partial sums to the workspace, takes
-// a ticket, and the last one adds the parts in split order (so the result does
-// not depend on which came last) and runs the epilogue. No CTA waits for
-// another. Every wait is bounded (ptx.cuh).
+// When the tiles do not fill the SMs evenly (few rows), K is cut: the blocks of
+// the tiles that are left over, end to end, go to the CTAs in equal runs; each
+// CTA writes the fp32 sums of a tile that it has only a part of to the
+// workspace and takes a ticket, and the last one adds the parts in the order of
+// their blocks (so the result does not depend on which came last) and runs the
+// epilogue. No CTA waits for another. Every wait is bounded (ptx.cuh).
 #include <atomic>
 #include <cstdint>
 #include <cuda.h>
@@ -84,7 +85,8 @@ struct SmemTail {
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
-    int last;                          // K split: this item took its tile's last ticket
+    int last;                          // cut tiles: this CTA took the tile's last ticket
+    int most_rows;                     // rows of the fullest tile
     int tile_start[MAX_GROUPS + 1];    // tiles before each group
     int offsets[MAX_GROUPS + 1];
     float2 factor[2][BM];              // sa * sw of each row: column halves (gated: W1 and W3)
@@ -97,48 +99,117 @@ constexpr size_t smem_bytes()
 }
 static_assert(smem_bytes<false>() <= 227 * 1024 && smem_bytes<true>() <= 227 * 1024, "shared memory");
 
-struct Item {
-    int g, row0, rows, n_tile, tile, split;
+struct Tile {
+    int g, row0, rows, n_tile;
 };
 
-// Item w: tile w / S, split w mod S; tiles expert-major, then N tile, then M
-// tile (neighbouring CTAs share the weights of an N tile in L2). This CTA's rows
-// start `sub` rows into the tile (a pair's rank 1: 128) and may be none (rows <= 0).
+// Tile w: tiles go expert-major, then N tile, then M tile (neighbouring CTAs
+// share the weights of an N tile in L2). This CTA's rows start `sub` rows into
+// the tile (a pair's rank 1: 128) and may be none (rows <= 0).
 template <int TILE_ROWS>
-__device__ __forceinline__ Item decode_item(int w, int S, int n_tiles, const int* ts, const int* offs, int G, int sub)
+__device__ __forceinline__ Tile decode_tile(int w, int n_tiles, const int* ts, const int* offs, int G, int sub)
 {
-    Item r;
-    r.tile = w / S;
-    r.split = w - r.tile * S;
+    Tile r;
     int lo = 0, hi = G;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (ts[mid] * n_tiles <= r.tile) lo = mid; else hi = mid;
+        if (ts[mid] * n_tiles <= w) lo = mid; else hi = mid;
     }
     r.g = lo;
     const int mt = ts[lo + 1] - ts[lo];
-    const int tl = r.tile - ts[lo] * n_tiles;
+    const int tl = w - ts[lo] * n_tiles;
     r.n_tile = tl / mt;
     r.row0 = offs[lo] + (tl - r.n_tile * mt) * TILE_ROWS + sub;
     r.rows = min(BM, offs[lo + 1] - r.row0);
     return r;
 }
 
-// How many ways to split K: the S that minimises (rounds of items over the
-// CTAs) x (K blocks per item + a fixed cost per item, larger when parts have
-// to be joined), with the parts of all items within the workspace.
-__device__ __forceinline__ int choose_split(int tiles, int k_blocks, int n_cta)
-{
-    int best = 1;
-    int best_cost = ((tiles + n_cta - 1) / n_cta) * (k_blocks + kFp8ItemCost);
-    for (int s = 2; s <= kFp8MaxSplit; ++s) {
-        if (tiles * s > kFp8MaxItems || k_blocks < 2 * s) break;
-        const int cost = ((tiles * s + n_cta - 1) / n_cta) * ((k_blocks + s - 1) / s + kFp8ItemCost + kFp8JoinCost);
-        if (cost < best_cost) {
-            best_cost = cost;
-            best = s;
+// The schedule: the first `full` tiles whole, round robin over the CTAs; the K
+// blocks of the rest, end to end, in `segments` equal runs, one a CTA. A run
+// that begins or ends inside a tile computes a part of its sums.
+struct Plan {
+    int tiles, full, segments;
+    int part_rows;   // rows a part has room for: those of the fullest tile
+};
+
+struct Piece {
+    int tile, kb0, kb1;
+};
+
+struct Walk {
+    int tile, step, full, k_blocks;
+    int64_t pos, end;
+
+    __device__ __forceinline__ Walk(const Plan& p, int unit, int n_units, int k_blocks_)
+        : tile(unit), step(n_units), full(p.full), k_blocks(k_blocks_), pos(0), end(0)
+    {
+        if (unit < p.segments) {
+            const int64_t total = (int64_t)(p.tiles - p.full) * k_blocks;
+            pos = total * unit / p.segments;
+            end = total * (unit + 1) / p.segments;
         }
     }
+
+    __device__ __forceinline__ bool next(Piece& p)
+    {
+        if (tile < full) {
+            p = {tile, 0, k_blocks};
+            tile += step;
+            return true;
+        }
+        if (pos >= end) return false;
+        const int q = (int)(pos / k_blocks);
+        p.tile = full + q;
+        p.kb0 = (int)(pos - (int64_t)q * k_blocks);
+        p.kb1 = (int)min((int64_t)k_blocks, p.kb0 + (end - pos));
+        pos += p.kb1 - p.kb0;
+        return true;
+    }
+};
+
+// The parts of tile q of the segments' tiles: the first segment that holds
+// blocks of it, and how many do. Segment c keeps a part that begins with its
+// tile in slot 2c + 1, one that begins inside it in slot 2c.
+__device__ __forceinline__ int first_part(const Plan& p, int q, int k_blocks, int& parts)
+{
+    const int64_t total = (int64_t)(p.tiles - p.full) * k_blocks;
+    auto segment_of = [&](int64_t block) { return (int)(((block + 1) * p.segments - 1) / total); };
+    const int first = segment_of((int64_t)q * k_blocks);
+    parts = segment_of((int64_t)(q + 1) * k_blocks - 1) - first + 1;
+    return first;
+}
+
+// The plan with the least estimated time, counted in K blocks of one CTA (0.42
+// us): whole tiles cost their blocks and kFp8TileCost; cutting tiles costs the
+// parts' publication and the join, a trip to L2 for every 8 rows and 4 parts.
+// Measured (us, whole tiles / best cut): one row, 16 tiles of 112 blocks for
+// each of 2 experts 55.6 / 27.8; 64 rows, 16 tiles of 32 blocks 17.2 / 15.7;
+// 128 rows, 16 tiles of 32 blocks 19.4 / 22.7; 333 rows, 42 tiles of 160 blocks
+// 74.7 / 45.7.
+__device__ __forceinline__ Plan make_plan(int tiles, int rows, int k_blocks, int n_cta)
+{
+    Plan best{tiles, tiles, 0, rows};
+    if (tiles == 0 || (int64_t)2 * n_cta * rows > kFp8PartRows || 2 * n_cta > kFp8MaxTickets) return best;
+    const int rounds = tiles / n_cta;
+    float best_cost = (float)((tiles + n_cta - 1) / n_cta) * ((float)k_blocks + kFp8TileCost);
+    // cut the tiles beyond the whole rounds but one (or all of them, when there
+    // is less than one round) into `segments` runs
+    const int full = rounds > 1 ? (rounds - 1) * n_cta : 0;
+    const int64_t total = (int64_t)(tiles - full) * k_blocks;
+    auto consider = [&](int segments, int parts, float cuts) {
+        if (total < (int64_t)2 * segments) return;
+        const float cost = (float)(full / n_cta) * ((float)k_blocks + kFp8TileCost) +
+                           (float)((total + segments - 1) / segments) + cuts * kFp8CutCost +
+                           kFp8JoinCost * (float)((rows + 7) / 8) * (float)((parts + 3) / 4);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best.full = full;
+            best.segments = segments;
+        }
+    };
+    for (int s = 2; s <= kFp8MaxSplit && tiles * s <= n_cta; ++s) consider(tiles * s, s, 1.0f);
+    // runs that do not line up with tiles leave most CTAs two parts
+    if (tiles % n_cta != 0) consider(n_cta, n_cta / (tiles - full) + 2, 2.0f);
     return best;
 }
 
@@ -153,6 +224,99 @@ __device__ __forceinline__ void fold32(float (&acc)[128], const uint32_t (&v)[32
 {
 #pragma unroll
     for (int i = 0; i < 32; ++i) acc[C + i] = fmaf(__uint_as_float(v[i]), f, acc[C + i]);
+}
+
+// Where row p of a product goes and what it is scaled by: false if nowhere.
+__device__ __forceinline__ bool row_target(const Fp8GemmArgs& args, int p, int64_t& row, float& wt)
+{
+    row = p;
+    wt = 1.0f;
+    if (args.src_row) {
+        // scattered: assignment f = src_row[p] goes to slot[f mod k][f / k]
+        const int f = args.src_row[p];
+        const int64_t t = f / args.k;
+        if (f < 0 || t >= args.T) {
+            report_error(args.err, MOE_DEV_ERR_BOUNDS);
+            return false;
+        }
+        row = (int64_t)(f - (int)t * args.k) * args.T + t;
+        wt = args.topk_w[f];
+    } else if (args.topk_w) {
+        wt = args.topk_w[p];
+    }
+    return true;
+}
+
+// The join of a tile's parts, `stride` floats each, added in the order of their
+// blocks, and its epilogue: a warp takes JOIN_ROWS rows at a time, a lane 4
+// columns of each half of a row, with JOIN_PARTS parts' loads in flight together
+// (the parts were just written, so a load is a trip to L2; what bounds the join
+// is the number of trips, not the bytes).
+constexpr int JOIN_ROWS = 1;
+constexpr int JOIN_PARTS = 4;
+
+template <bool GATED, typename OUT>
+__device__ __forceinline__ void join(const Fp8GemmArgs& args, const Tile& it, int first, int parts, int stride,
+                                     int n_blocks, int warp, int lane)
+{
+    // the first part begins with the tile, the others inside it (first_part)
+    const float* base = args.part + (int64_t)2 * first * stride;
+    auto slot = [&](int s) { return (int64_t)(s == 0 ? 1 : 2 * s) * stride; };
+    // gated: 4 columns of W1's sums and the same of W3's, 64 further on
+    const int c0 = GATED ? (lane >> 4) * 128 + (lane & 15) * 4 : lane * 4;
+    const int c1 = c0 + (GATED ? 64 : 128);
+    for (int r0 = warp * JOIN_ROWS; r0 < it.rows; r0 += FOLD_WARPS * JOIN_ROWS) {
+        float4 a[JOIN_ROWS], b[JOIN_ROWS];
+#pragma unroll
+        for (int q = 0; q < JOIN_ROWS; ++q) a[q] = b[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int s0 = 0; s0 < parts; s0 += JOIN_PARTS) {
+            float4 x[JOIN_PARTS][JOIN_ROWS], y[JOIN_PARTS][JOIN_ROWS];
+#pragma unroll
+            for (int s = 0; s < JOIN_PARTS; ++s)
+#pragma unroll
+                for (int q = 0; q < JOIN_ROWS; ++q)
+                    if (s0 + s < parts && r0 + q < it.rows) {
+                        const float* src = base + slot(s0 + s) + (r0 + q) * BN;
+                        x[s][q] = __ldcg(reinterpret_cast<const float4*>(src + c0));
+                        y[s][q] = __ldcg(reinterpret_cast<const float4*>(src + c1));
+                    }
+#pragma unroll
+            for (int s = 0; s < JOIN_PARTS; ++s)
+#pragma unroll
+                for (int q = 0; q < JOIN_ROWS; ++q)
+                    if (s0 + s < parts && r0 + q < it.rows) {
+                        a[q].x += x[s][q].x; a[q].y += x[s][q].y; a[q].z += x[s][q].z; a[q].w += x[s][q].w;
+                        b[q].x += y[s][q].x; b[q].y += y[s][q].y; b[q].z += y[s][q].z; b[q].w += y[s][q].w;
+                    }
+        }
+#pragma unroll
+        for (int q = 0; q < JOIN_ROWS; ++q) {
+            if (r0 + q >= it.rows) break;
+            const int p = it.row0 + r0 + q;
+            if constexpr (GATED) {
+                const float h[4] = {silu(a[q].x) * b[q].x, silu(a[q].y) * b[q].y, silu(a[q].z) * b[q].z,
+                                    silu(a[q].w) * b[q].w};
+                float amax = max_nan(max_nan(fabsf(h[0]), fabsf(h[1])), max_nan(fabsf(h[2]), fabsf(h[3])));
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+                const float scale = fp8_scale(amax);
+                const float inv = 1.0f / scale;
+                const int n = it.n_tile * 128 + lane * 4;
+                if (n < args.N)
+                    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(args.out) + (int64_t)p * args.N + n) =
+                        e4m3x4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
+                if (lane == 0) args.out_scale[(int64_t)p * n_blocks + it.n_tile] = scale;
+            } else {
+                int64_t row;
+                float wt;
+                if (!row_target(args, p, row, wt)) continue;
+                OUT* dst = static_cast<OUT*>(args.out) + row * args.N;
+                const int n = it.n_tile * BN + lane * 4;
+                if (n < args.N) store4(dst + n, a[q].x * wt, a[q].y * wt, a[q].z * wt, a[q].w * wt);
+                if (n + 128 < args.N) store4(dst + n + 128, b[q].x * wt, b[q].y * wt, b[q].z * wt, b[q].w * wt);
+            }
+        }
+    }
 }
 
 template <bool GATED, typename OUT, bool PAIR>
@@ -209,6 +373,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         // at all, so no row outside the operands is touched
         bool good = true;
         int tiles = 0;
+        int most = 0;   // rows of the fullest tile
         for (int g0 = 0; g0 < G; g0 += 32) {
             const int g = g0 + lane;
             int n = 0;
@@ -219,6 +384,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 st->offsets[g] = first;
                 if (g == G - 1) st->offsets[G] = end;
                 n = good ? (end - first + C::TILE_ROWS - 1) / C::TILE_ROWS : 0;
+                most = max(most, min(end - first, BM));
             }
             int incl = n;
 #pragma unroll
@@ -230,8 +396,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             tiles += __shfl_sync(0xffffffffu, incl, 31);
         }
         good = __all_sync(0xffffffffu, good);
+        most = __reduce_max_sync(0xffffffffu, most);
         if (lane == 0) {
             st->tile_start[G] = good ? tiles : 0;
+            st->most_rows = most;
             if (!good) report_error(args.err, MOE_DEV_ERR_BOUNDS);
         }
     }
@@ -245,8 +413,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const int n_tiles = (args.N + n_out - 1) / n_out;
     const int k_blocks = (args.K + BK - 1) / BK;
     const int tiles = st->tile_start[G] * n_tiles;
-    const int S = PAIR ? 1 : choose_split(tiles, k_blocks, n_units);
-    const int items = tiles * S;
+    const Plan plan = PAIR ? Plan{tiles, tiles, 0, 0} : make_plan(tiles, st->most_rows, k_blocks, n_units);
     volatile int* abort = &st->abort;
 
     if (warp >= 8) {
@@ -258,11 +425,11 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 uint32_t phase = 0;
                 int issued = 0;
                 bool ok = true;
-                for (int w = unit; w < items && ok; w += n_units) {
-                    const Item it = decode_item<C::TILE_ROWS>(w, S, n_tiles, st->tile_start, st->offsets, G, sub);
-                    const int kb1 = (it.split + 1) * k_blocks / S;
+                Walk walk(plan, unit, n_units, k_blocks);
+                for (Piece pc; ok && walk.next(pc);) {
+                    const Tile it = decode_tile<C::TILE_ROWS>(pc.tile, n_tiles, st->tile_start, st->offsets, G, sub);
                     const int n0 = it.n_tile * n_out;
-                    for (int kb = it.split * k_blocks / S; kb < kb1; ++kb) {
+                    for (int kb = pc.kb0; kb < pc.kb1; ++kb) {
                         if (!mbar_wait(smem_u32(&st->empty[stage]), phase ^ 1u, abort, args.err)) {
                             ok = false;
                             break;
@@ -314,7 +481,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             __syncwarp();
         } else if (warp == 9) {
             // ============================ MMA issuer ==============================
-            // the whole warp walks the items and waits (uniform control flow, so the
+            // the whole warp walks the pieces and waits (uniform control flow, so the
             // descriptors stay in uniform registers); one elected lane issues (a
             // pair: of the rank-0 CTA, for both)
             const uint32_t leader = elect_one_sync();
@@ -326,10 +493,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             uint32_t acc_phase = 0;
             bool ok = true;
             bool any = false;
-            for (int w = unit; w < items && ok && rank == 0; w += n_units) {
-                const int split = w % S;
-                const int n_kb = (split + 1) * k_blocks / S - split * k_blocks / S;
-                for (int i = 0; i < n_kb; ++i) {
+            Walk walk(plan, unit, n_units, k_blocks);
+            for (Piece pc; ok && rank == 0 && walk.next(pc);) {
+                for (int kb = pc.kb0; kb < pc.kb1; ++kb) {
                     ok = __all_sync(0xffffffffu,
                                     mbar_wait(smem_u32(&st->full[stage]), phase, abort, args.err) &&
                                         mbar_wait(smem_u32(&st->tempty[acc]), acc_phase ^ 1u, abort, args.err));
@@ -367,9 +533,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             int buf = 0;
             uint32_t buf_phase = 0;
             bool ok = true;
-            for (int w = unit; w < items && ok; w += n_units) {
-                const Item it = decode_item<C::TILE_ROWS>(w, S, n_tiles, st->tile_start, st->offsets, G, sub);
-                const int kb0 = it.split * k_blocks / S, kb1 = (it.split + 1) * k_blocks / S;
+            Walk walk(plan, unit, n_units, k_blocks);
+            for (Piece pc; ok && walk.next(pc);) {
+                const Tile it = decode_tile<C::TILE_ROWS>(pc.tile, n_tiles, st->tile_start, st->offsets, G, sub);
+                const int kb0 = pc.kb0, kb1 = pc.kb1;
                 const float* sa0 = args.a_scale + (int64_t)min(it.row0 + r0, args.R - 1) * k_blocks;
                 const float* sa1 = args.a_scale + (int64_t)min(it.row0 + r0 + 32, args.R - 1) * k_blocks;
                 // gated: the slice's block of W1 and of W3; product: each half's block
@@ -409,18 +576,18 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         uint32_t buf_phase = 0;
         bool ready = false;    // the next block is known to be there
         uint32_t parity = 0;   // which amax buffer this tile uses
-        // after an abort every fold warp still walks all items, without waiting
+        // after an abort every fold warp still walks all pieces, without waiting
         // for the tensor cores, so that the barriers below stay matched
         bool ok = true;
-        for (int w = unit; w < items; w += n_units) {
-            const Item it = decode_item<C::TILE_ROWS>(w, S, n_tiles, st->tile_start, st->offsets, G, sub);
+        Walk walk(plan, unit, n_units, k_blocks);
+        for (Piece pc; walk.next(pc);) {
+            const Tile it = decode_tile<C::TILE_ROWS>(pc.tile, n_tiles, st->tile_start, st->offsets, G, sub);
             const bool valid = r < it.rows;
             const int p = it.row0 + r;
-            const int kb0 = it.split * k_blocks / S, kb1 = (it.split + 1) * k_blocks / S;
             float acc[128];
 #pragma unroll
             for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-            for (int kb = kb0; kb < kb1 && ok; ++kb) {
+            for (int kb = pc.kb0; kb < pc.kb1 && ok; ++kb) {
                 ok = __all_sync(0xffffffffu, ready || mbar_wait(smem_u32(&st->tfull[buf]), buf_phase, abort, args.err));
                 if (!ok) break;
                 tc_fence_after();
@@ -457,48 +624,36 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 fold32<96>(acc, v, c1);
             }
 
-            if (S > 1) {
-                // publish this item's part (columns in fours, rows side by side), take
-                // a ticket; the last item of the tile adds the parts in split order
-                float4* part = args.part + (int64_t)w * (BM * BN / 4) + (half * 32) * BM + r;
+            if (pc.kb1 - pc.kb0 < k_blocks) {
+                // publish this piece's part (its rows side by side) and take a ticket;
+                // the last piece of the tile joins the parts
+                float* part = args.part + ((int64_t)(2 * unit + (pc.kb0 == 0)) * plan.part_rows + r) * BN + half * 128;
                 if (ok && valid) {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        __stcg(part + c * BM,
-                               make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]));
-                    }
+                    for (int c = 0; c < 128; c += 8)
+                        st_global_v8(part + c, __float_as_uint(acc[c]), __float_as_uint(acc[c + 1]),
+                                     __float_as_uint(acc[c + 2]), __float_as_uint(acc[c + 3]),
+                                     __float_as_uint(acc[c + 4]), __float_as_uint(acc[c + 5]),
+                                     __float_as_uint(acc[c + 6]), __float_as_uint(acc[c + 7]));
                 }
                 __threadfence();
                 fold_barrier();
+                const int q = pc.tile - plan.full;
+                int parts;
+                const int first = first_part(plan, q, k_blocks, parts);
                 if (threadIdx.x == 0) {
                     int last = 0;
                     if (!*abort) {
-                        last = atomicAdd(args.ticket + it.tile, 1) == S - 1;
-                        if (last) args.ticket[it.tile] = 0;   // as found, for the next call
+                        last = atomicAdd(args.ticket + q, 1) == parts - 1;
+                        if (last) args.ticket[q] = 0;   // as found, for the next call
                     }
                     __threadfence();
                     st->last = last;
                 }
                 fold_barrier();
-                if (!st->last) continue;
-                if (valid) {
-                    const float4* first = args.part + (int64_t)it.tile * S * (BM * BN / 4) + (half * 32) * BM + r;
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        float4 sum = __ldcg(first + c * BM);
-                        for (int s = 1; s < S; ++s) {
-                            const float4 v = __ldcg(first + (int64_t)s * (BM * BN / 4) + c * BM);
-                            sum.x += v.x;
-                            sum.y += v.y;
-                            sum.z += v.z;
-                            sum.w += v.w;
-                        }
-                        acc[4 * c] = sum.x;
-                        acc[4 * c + 1] = sum.y;
-                        acc[4 * c + 2] = sum.z;
-                        acc[4 * c + 3] = sum.w;
-                    }
-                }
+                if (st->last)
+                    join<GATED, OUT>(args, it, first, parts, plan.part_rows * BN, n_blocks, warp, lane);
+                continue;
             }
 
             if constexpr (GATED) {
@@ -536,20 +691,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 }
             } else if (valid && ok) {
                 const int n0 = it.n_tile * BN + half * 128;
-                int64_t row = p;
-                float wt = 1.0f;
-                bool in_bounds = true;
-                if (args.src_row) {
-                    // scattered: assignment f = src_row[p] goes to slot[f mod k][f / k]
-                    const int f = args.src_row[p];
-                    const int64_t t = f / args.k;
-                    in_bounds = f >= 0 && t < args.T;
-                    row = in_bounds ? (int64_t)(f - (int)t * args.k) * args.T + t : 0;
-                    if (in_bounds) wt = args.topk_w[f];
-                    else report_error(args.err, MOE_DEV_ERR_BOUNDS);
-                } else if (args.topk_w) {
-                    wt = args.topk_w[p];
-                }
+                int64_t row;
+                float wt;
+                const bool in_bounds = row_target(args, p, row, wt);
                 OUT* dst = static_cast<OUT*>(args.out) + row * args.N + n0;
                 if (in_bounds) {
 #pragma unroll
