@@ -726,17 +726,35 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     }
 }
 
+constexpr int kMaxDevices = 64;
+
+// Lets `kern` have `bytes` of dynamic shared memory on the current device, asked
+// of the runtime once per kernel (its bit set in `done`) and device.
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& done, int& dev)
+{
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    const uint64_t bit = (uint64_t)1 << dev;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
 // CTA-pair kernels: how many pairs can be resident at once (shared memory and
 // the GPCs' SM pairs decide), looked up once per kernel and device.
-constexpr int kMaxPairDevices = 64;
-std::atomic<int> g_pairs[3][kMaxPairDevices];
+std::atomic<int> g_pairs[3][kMaxDevices];
 
 template <bool GATED, typename OUT>
 cudaError_t launch_pair(int slot, const CUtensorMap& tmA, const CUtensorMap& tmB0, const CUtensorMap& tmB1,
                         const Fp8GemmArgs& a, int num_sms, cudaStream_t s)
 {
     auto kern = fp8_gemm_kernel<GATED, OUT, true>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<true>());
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = allow_smem(kern, smem_bytes<true>(), done, dev);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -751,10 +769,6 @@ cudaError_t launch_pair(int slot, const CUtensorMap& tmA, const CUtensorMap& tmB
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int dev = 0;
-    e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxPairDevices) return cudaErrorInvalidDevice;
     int pairs = g_pairs[slot][dev].load(std::memory_order_relaxed);
     if (pairs <= 0) {
         cfg.gridDim = dim3((unsigned)(num_sms & ~1));
@@ -778,7 +792,9 @@ cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB0, const CUtens
 {
     auto kern = fp8_gemm_kernel<GATED, OUT, false>;
     constexpr size_t smem = smem_bytes<false>();
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    const cudaError_t e = allow_smem(kern, smem, done, dev);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(num_sms), dim3(NUM_THREADS), smem, s, tmA, tmB0, tmB1, a);
 }

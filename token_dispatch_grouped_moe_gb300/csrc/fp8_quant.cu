@@ -21,7 +21,10 @@ namespace {
 //
 // One block per row; a thread holds VPT chunks of 8 consecutive columns in
 // registers, so a row is read once. 16 neighbouring lanes hold one 128-column
-// block, whose maximum is 4 shuffles away.
+// block, whose maximum is 4 shuffles away. Bound by memory from about a
+// thousand rows on: 8192 rows of 4096 bf16 with residual move 303 MB in 48.2 us
+// (6.3 TB/s, 0.93 of a plain copy's rate); one row is a launch and three trips
+// to memory (2.5 us).
 
 constexpr int kNormMaxThreads = 512;
 
@@ -150,7 +153,14 @@ cudaError_t launch_norm(const Fp8NormArgs& a, cudaStream_t s)
     const int n_vec = a.H / 8;
     const dim3 grid((unsigned)a.T);
     auto threads = [&](int vpt) { return dim3((unsigned)(((n_vec + vpt - 1) / vpt + 31) / 32 * 32)); };
-    if (n_vec <= kNormMaxThreads) return launch_pdl(fp8_norm_kernel<T, 1>, grid, threads(1), 0, s, a);
+    // one chunk a thread is the quickest for few rows; from 1024 rows on two
+    // chunks of a 16-bit type (32 bytes in flight a thread and tensor, half the
+    // threads to synchronise). Measured, one / two, us: H = 4096 with residual,
+    // 1 row 2.5 / 2.8, 512: 4.6 / 5.1, 1024: 7.8 / 7.6, 8192: 57.5 / 48.2; H = 2048
+    // without, 32768 rows 73.7 / 55.2; H = 512 (64 chunks) 34.2 / 35.1; fp32 (32
+    // bytes a chunk), H = 4096, 8192 rows 84.9 / 85.4.
+    const bool two = sizeof(T) == 2 && a.T >= 1024 && n_vec >= 128;
+    if (n_vec <= kNormMaxThreads && !two) return launch_pdl(fp8_norm_kernel<T, 1>, grid, threads(1), 0, s, a);
     if (n_vec <= 2 * kNormMaxThreads) return launch_pdl(fp8_norm_kernel<T, 2>, grid, threads(2), 0, s, a);
     if (n_vec <= 4 * kNormMaxThreads) return launch_pdl(fp8_norm_kernel<T, 4>, grid, threads(4), 0, s, a);
     if (n_vec <= 8 * kNormMaxThreads) return launch_pdl(fp8_norm_kernel<T, 8>, grid, threads(8), 0, s, a);
