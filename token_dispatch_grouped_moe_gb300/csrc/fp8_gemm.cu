@@ -252,8 +252,8 @@ __device__ __forceinline__ bool row_target(const Fp8GemmArgs& args, int p, int64
 // columns of each half of a row, with JOIN_PARTS parts' loads in flight together
 // (the parts were just written, so a load is a trip to L2; what bounds the join
 // is the number of trips, not the bytes).
-constexpr int JOIN_ROWS = 1;
-constexpr int JOIN_PARTS = 4;
+constexpr int JOIN_ROWS = 2;
+constexpr int JOIN_PARTS = 2;
 
 template <bool GATED, typename OUT>
 __device__ __forceinline__ void join(const Fp8GemmArgs& args, const Tile& it, int first, int parts, int stride,
@@ -659,13 +659,12 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             if constexpr (GATED) {
                 // h = silu(a W1^T) * (a W3^T) of this thread's row and 64 columns
                 const int n0 = it.n_tile * 128 + half * 64;
-                float h[64];
                 float amax = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 64; ++i) {
-                    h[i] = silu(acc[i]) * acc[64 + i];
+                    acc[i] = silu(acc[i]) * acc[64 + i];
                     // columns past N are zero (zero weights): they do not count
-                    amax = max_nan(amax, fabsf(h[i]));
+                    amax = max_nan(amax, fabsf(acc[i]));
                 }
                 // the block's maximum: this half's and the other's
                 st->amax[parity][half][r] = amax;
@@ -679,11 +678,12 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         if (n0 + 16 * i < args.N) {
+                            const float* h = acc + 16 * i;
                             uint4 o;
-                            o.x = e4m3x4(h[16 * i] * inv, h[16 * i + 1] * inv, h[16 * i + 2] * inv, h[16 * i + 3] * inv);
-                            o.y = e4m3x4(h[16 * i + 4] * inv, h[16 * i + 5] * inv, h[16 * i + 6] * inv, h[16 * i + 7] * inv);
-                            o.z = e4m3x4(h[16 * i + 8] * inv, h[16 * i + 9] * inv, h[16 * i + 10] * inv, h[16 * i + 11] * inv);
-                            o.w = e4m3x4(h[16 * i + 12] * inv, h[16 * i + 13] * inv, h[16 * i + 14] * inv, h[16 * i + 15] * inv);
+                            o.x = e4m3x4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
+                            o.y = e4m3x4(h[4] * inv, h[5] * inv, h[6] * inv, h[7] * inv);
+                            o.z = e4m3x4(h[8] * inv, h[9] * inv, h[10] * inv, h[11] * inv);
+                            o.w = e4m3x4(h[12] * inv, h[13] * inv, h[14] * inv, h[15] * inv);
                             *reinterpret_cast<uint4*>(dst + 16 * i) = o;
                         }
                     }
