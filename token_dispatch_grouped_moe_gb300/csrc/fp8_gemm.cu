@@ -91,6 +91,7 @@ struct SmemTail {
     int offsets[MAX_GROUPS + 1];
     float2 factor[2][BM];              // sa * sw of each row: column halves (gated: W1 and W3)
     float amax[2][2][BM];              // gated: [tile parity][column half][row]
+    uint4 stage_out[FOLD_WARPS][32 * 4];   // 64 bytes of a fold warp's 32 rows, on their way out
 };
 template <bool PAIR>
 constexpr size_t smem_bytes()
@@ -245,6 +246,26 @@ __device__ __forceinline__ bool row_target(const Fp8GemmArgs& args, int p, int64
         wt = args.topk_w[p];
     }
     return true;
+}
+
+// Writes 64 bytes of each of this warp's 32 rows (lane l holds row l's in v) to
+// out[i] + at, out[i] being row 8 i + l / 4 of lane l (null: not written). A lane's
+// own bytes would touch 32 lines with every store; through shared memory (16-byte
+// pieces swizzled by the row pair, so neither side has bank conflicts) a store
+// covers 8 rows' 64 contiguous bytes.
+__device__ __forceinline__ void store_rows(uint4* buf, int lane, const uint4 (&v)[4], unsigned char* const (&out)[4],
+                                           int64_t at, bool here)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) buf[lane * 4 + (j ^ ((lane >> 1) & 3))] = v[j];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = 8 * i + (lane >> 2);
+        const uint4 o = buf[row * 4 + ((lane & 3) ^ ((row >> 1) & 3))];
+        if (here && out[i]) *reinterpret_cast<uint4*>(out[i] + at) = o;
+    }
+    __syncwarp();
 }
 
 // The join of a tile's parts, `stride` floats each, added in the order of their
@@ -673,38 +694,57 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 parity ^= 1u;
                 const float scale = fp8_scale(amax);
                 const float inv = 1.0f / scale;
-                if (valid && ok) {
-                    uint8_t* dst = static_cast<uint8_t*>(args.out) + (int64_t)p * args.N + n0;
+                unsigned char* out[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (n0 + 16 * i < args.N) {
-                            const float* h = acc + 16 * i;
-                            uint4 o;
-                            o.x = e4m3x4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
-                            o.y = e4m3x4(h[4] * inv, h[5] * inv, h[6] * inv, h[7] * inv);
-                            o.z = e4m3x4(h[8] * inv, h[9] * inv, h[10] * inv, h[11] * inv);
-                            o.w = e4m3x4(h[12] * inv, h[13] * inv, h[14] * inv, h[15] * inv);
-                            *reinterpret_cast<uint4*>(dst + 16 * i) = o;
-                        }
-                    }
-                    if (half == 0) args.out_scale[(int64_t)p * n_blocks + it.n_tile] = scale;
+                for (int i = 0; i < 4; ++i) {
+                    const int row = (warp & 3) * 32 + 8 * i + (lane >> 2);
+                    out[i] = ok && row < it.rows
+                                 ? static_cast<unsigned char*>(args.out) + (int64_t)(it.row0 + row) * args.N + n0
+                                 : nullptr;
                 }
-            } else if (valid && ok) {
+                uint4 o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float* h = acc + 16 * i;
+                    o[i].x = e4m3x4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
+                    o[i].y = e4m3x4(h[4] * inv, h[5] * inv, h[6] * inv, h[7] * inv);
+                    o[i].z = e4m3x4(h[8] * inv, h[9] * inv, h[10] * inv, h[11] * inv);
+                    o[i].w = e4m3x4(h[12] * inv, h[13] * inv, h[14] * inv, h[15] * inv);
+                }
+                store_rows(st->stage_out[warp], lane, o, out, (lane & 3) * 16, n0 + (lane & 3) * 16 < args.N);
+                if (valid && ok && half == 0) args.out_scale[(int64_t)p * n_blocks + it.n_tile] = scale;
+            } else {
                 const int n0 = it.n_tile * BN + half * 128;
-                int64_t row;
-                float wt;
-                const bool in_bounds = row_target(args, p, row, wt);
-                OUT* dst = static_cast<OUT*>(args.out) + row * args.N + n0;
-                if (in_bounds) {
+                int64_t row = 0;
+                float wt = 1.0f;
+                const bool mine = ok && valid && row_target(args, p, row, wt);
+                const unsigned there = __ballot_sync(0xffffffffu, mine);
+                unsigned char* out[4];   // of the rows that this lane stores (store_rows)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (n0 + 8 * i < args.N) {
-                            float o[8];
+                for (int i = 0; i < 4; ++i) {
+                    const int l = 8 * i + (lane >> 2);
+                    const int64_t at = __shfl_sync(0xffffffffu, row, l);
+                    out[i] = (there >> l) & 1
+                                 ? reinterpret_cast<unsigned char*>(static_cast<OUT*>(args.out) + at * args.N + n0)
+                                 : nullptr;
+                }
+                constexpr int COLS = 64 / (int)sizeof(OUT);   // columns of a row at once
+                constexpr int PIECE = 16 / (int)sizeof(OUT);  // and of a 16-byte piece
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) o[u] = acc[8 * i + u] * wt;
-                            store8(dst + 8 * i, o);
-                        }
+                for (int c = 0; c < 128; c += COLS) {
+                    uint4 o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float* q = acc + c + PIECE * j;
+                        if constexpr (sizeof(OUT) == 2)
+                            o[j] = make_uint4(bf16x2(q[0] * wt, q[1] * wt), bf16x2(q[2] * wt, q[3] * wt),
+                                              bf16x2(q[4] * wt, q[5] * wt), bf16x2(q[6] * wt, q[7] * wt));
+                        else
+                            o[j] = make_uint4(__float_as_uint(q[0] * wt), __float_as_uint(q[1] * wt),
+                                              __float_as_uint(q[2] * wt), __float_as_uint(q[3] * wt));
                     }
+                    const int n = c + (lane & 3) * PIECE;
+                    store_rows(st->stage_out[warp], lane, o, out, (int64_t)n * (int)sizeof(OUT), n0 + n < args.N);
                 }
             }
         }
