@@ -182,6 +182,16 @@ def test_binding_checks_tensors(lib):
         lambda: lib.add_rmsnorm_fp8(torch.zeros(64, 4).t()),
         lambda: lib.fp8_quantize_weight(torch.zeros(2, 64, 64)),
     ]
+    bad += [
+        lambda: lib.fp8_matmul(a[0], s, w, wsc, ws, offsets=off),
+        lambda: lib.fp8_matmul(a, s, w[0], wsc, ws, offsets=off),
+        lambda: lib.fp8_matmul(a, None, w, wsc, ws, offsets=off),
+        lambda: lib.fp8_matmul(a, s, w, wsc, ws.int(), offsets=off),
+        lambda: lib.fp8_matmul(a, s, w, wsc, ws, offsets=off),           # right, but not on a GPU
+        lambda: lib.fp8_gated(a, s, w, wsc, w, wsc[:, :0], ws, offsets=off),
+        lambda: lib.add_rmsnorm_fp8(torch.zeros(64)),
+        lambda: lib.add_rmsnorm_fp8([1.0]),
+    ]
     for call in bad:
         with pytest.raises(ValueError):
             call()
@@ -455,10 +465,10 @@ def test_streams_and_graph(lib):
     w3, s3 = weight(g, 1, F, K)
     x = torch.randn(R, K, generator=g, device="cuda").bfloat16()
 
-    def both(p, p_scale):
-        h, hs = lib.fp8_gated(p, p_scale, w1, s1, w3, s3, own)
+    def both(p, p_scale, **kw):
+        h, hs = lib.fp8_gated(p, p_scale, w1, s1, w3, s3, own, **kw)
         return [t.view(torch.uint8) if t.dtype == FP8 else t
-                for t in (h, hs, lib.fp8_matmul(p, p_scale, w1, s1, own), *lib.add_rmsnorm_fp8(x)[1:])]
+                for t in (h, hs, lib.fp8_matmul(p, p_scale, w1, s1, own, **kw), *lib.add_rmsnorm_fp8(x, **kw)[1:])]
 
     want, want_b = both(a, a_scale), both(b, b_scale)
     torch.cuda.synchronize()
@@ -467,6 +477,13 @@ def test_streams_and_graph(lib):
         got = both(a, a_scale)
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(want, got))
+    # a stream given by argument: the outputs' memory is that stream's, so memory
+    # that the current stream frees and takes again cannot be the same
+    torch.cuda._sleep(1000000)
+    got = both(a, a_scale, stream=side)
+    busy = [torch.full_like(t, 3) for t in got]
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(want, got)) and len(busy) == len(got)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph, stream=side):
         got = both(a, a_scale)

@@ -450,38 +450,38 @@ class MoELayer:
 
 FP8 = torch.float8_e4m3fn
 FP8_BLOCK = 128   # values that share one scale
-_DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 def _fp8_blocks(n: int) -> int:
     return (n + FP8_BLOCK - 1) // FP8_BLOCK
 
 
-# Calls of a few microseconds are bound by the host, so the checks below are
-# plain comparisons, messages are built only on failure and the current stream's
-# handle is asked for directly (2.8 us less than torch.cuda.current_stream()).
-
-def _refuse(t, name, shape, dtype, device, what="a contiguous"):
-    raise ValueError(f"{name}: expected {what} {dtype} tensor of shape {tuple(shape)} on {device}, got "
-                     f"{t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
-
-
 def _expect(t, name, shape, dtype, device):
     """Argument check: a contiguous tensor of this shape and type on this device."""
     if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        _refuse(t, name, shape, dtype, device)
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
 
 
-def _rows(t, name, shape, dtype, device):
-    """Argument check: rows of contiguous elements, any row stride."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or (t.stride(1) != 1 and shape[1] > 1):
-        _refuse(t, name, shape, dtype, device, "rows of contiguous elements in a")
+# The calls below whose kernels take microseconds (the norm and the products)
+# check their arguments, allocate and launch in C++ (csrc/torch_binding.cpp).
+_binding = None
 
 
-def _raw_stream(stream, device) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index) if device.type == "cuda" else 0
+def _load_binding():
+    global _binding
+    load()
+    try:
+        from . import _binding as module
+    except ImportError as e:
+        raise RuntimeError(f"the Python binding is missing or was built for another PyTorch ({e}): run "
+                           "`python -m token_dispatch_grouped_moe_gb300.build --force`") from e
+    _binding = module
+    return module
+
+
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def fp8_workspace_size(dims: Dims | None = None) -> int:
@@ -503,30 +503,10 @@ def add_rmsnorm_fp8(x, weight=None, residual=None, eps=1e-6, want_y=True, sum_ou
     for each row's block of 128. Returns (r, y, q, scale): r is None without a
     residual (``sum_out`` gives its memory: x and residual are allowed), y None
     with ``want_y=False``."""
-    T, H = x.shape
-    dev = x.device
-    if x.dtype not in _DTYPE:
-        raise ValueError(f"x: bf16, fp16 or fp32 expected, got {x.dtype}")
-    _rows(x, "x", (T, H), x.dtype, dev)
-    if weight is not None:
-        _expect(weight, "weight", (H,), x.dtype, dev)
-    if residual is not None:
-        _rows(residual, "residual", (T, H), x.dtype, dev)
-        if sum_out is None:
-            sum_out = torch.empty(T, H, dtype=x.dtype, device=dev)
-    if sum_out is not None:
-        _rows(sum_out, "sum_out", (T, H), x.dtype, dev)
-    y = torch.empty(T, H, dtype=x.dtype, device=dev) if want_y else None
-    q = torch.empty(T, H, dtype=FP8, device=dev)
-    scale = torch.empty(T, _fp8_blocks(H), dtype=torch.float32, device=dev)
-    status = (_lib or load()).moe_add_rmsnorm_fp8(
-        T, H, _DTYPE[x.dtype], x.data_ptr(), x.stride(0), None if residual is None else residual.data_ptr(),
-        0 if residual is None else residual.stride(0), None if weight is None else weight.data_ptr(), eps,
-        None if sum_out is None else sum_out.data_ptr(), 0 if sum_out is None else sum_out.stride(0),
-        None if y is None else y.data_ptr(), q.data_ptr(), scale.data_ptr(), _raw_stream(stream, dev))
-    if status:
-        raise MoeError(status, "moe_add_rmsnorm_fp8")
-    return sum_out, y, q, scale
+    r = (_binding or _load_binding()).add_rmsnorm_fp8(x, weight, residual, eps, want_y, sum_out, _handle(stream))
+    if type(r) is int:
+        raise MoeError(r, "moe_add_rmsnorm_fp8")
+    return r
 
 
 def fp8_quantize_weight(w, stream=None):
@@ -537,26 +517,8 @@ def fp8_quantize_weight(w, stream=None):
     q = torch.empty(G, N, K, dtype=FP8, device=w.device)
     scale = torch.empty(G, _fp8_blocks(N), _fp8_blocks(K), dtype=torch.float32, device=w.device)
     _ok(load().moe_fp8_quantize_weight(G, K, N, w.data_ptr(), q.data_ptr(), scale.data_ptr(),
-                                       _raw_stream(stream, w.device)), "moe_fp8_quantize_weight")
+                                       _stream(stream)), "moe_fp8_quantize_weight")
     return q, scale
-
-
-def _check_product(a, a_scale, names, weights, scales, offsets, ws):
-    """The checks that the two products share; (R, K, N, G)."""
-    R, K = a.shape
-    shape = weights[0].shape
-    G, N, _ = shape
-    dev, kb = a.device, _fp8_blocks(K)
-    _expect(a, "a", (R, K), FP8, dev)
-    _expect(a_scale, "a_scale", (R, kb), torch.float32, dev)
-    for name, q, scale in zip(names, weights, scales):
-        _expect(q, name, (G, N, K), FP8, dev)
-        _expect(scale, name + "_scale", (G, _fp8_blocks(N), kb), torch.float32, dev)
-    if offsets is not None:
-        _expect(offsets, "offsets", (G + 1,), torch.int32, dev)
-    if ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
-        _refuse(ws, "ws", ws.shape, torch.uint8, dev)
-    return R, K, N, G
 
 
 def fp8_matmul(a, a_scale, w, w_scale, ws, offsets=None, out_dtype=torch.bfloat16, out=None, stream=None):
@@ -564,35 +526,22 @@ def fp8_matmul(a, a_scale, w, w_scale, ws, offsets=None, out_dtype=torch.bfloat1
     offsets[g+1] (one group without offsets): a [R,K] and w [G,N,K] in e4m3
     with their block scales, out [R,N] bf16 or fp32. Rows outside every group
     are not written."""
-    R, K, N, G = _check_product(a, a_scale, ("w",), (w,), (w_scale,), offsets, ws)
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"out_dtype: bf16 or fp32 expected, got {out_dtype}")
-    if out is None:
-        out = torch.empty(R, N, dtype=out_dtype, device=a.device)
-    else:
-        _expect(out, "out", (R, N), out_dtype, a.device)
-    status = (_lib or load()).moe_fp8_matmul(
-        R, K, N, G, a.data_ptr(), a_scale.data_ptr(), None if offsets is None else offsets.data_ptr(), w.data_ptr(),
-        w_scale.data_ptr(), _DTYPE[out_dtype], out.data_ptr(), ws.data_ptr(), ws.numel(),
-        _raw_stream(stream, a.device))
-    if status:
-        raise MoeError(status, "moe_fp8_matmul")
-    return out
+    r = (_binding or _load_binding()).fp8_matmul(a, a_scale, w, w_scale, ws, offsets, out_dtype is torch.bfloat16, out,
+                                                 _handle(stream))
+    if type(r) is int:
+        raise MoeError(r, "moe_fp8_matmul")
+    return r
 
 
 def fp8_gated(a, a_scale, w1, w1_scale, w3, w3_scale, ws, offsets=None, stream=None):
     """h[p] = silu(a[p] w1[g]^T) * (a[p] w3[g]^T) for the rows of each group as
     in :func:`fp8_matmul`, quantized: (h [R,F] e4m3, scale [R, ceil(F/128)])."""
-    R, K, F, G = _check_product(a, a_scale, ("w1", "w3"), (w1, w3), (w1_scale, w3_scale), offsets, ws)
-    h = torch.empty(R, F, dtype=FP8, device=a.device)
-    scale = torch.empty(R, _fp8_blocks(F), dtype=torch.float32, device=a.device)
-    status = (_lib or load()).moe_fp8_gated(
-        R, K, F, G, a.data_ptr(), a_scale.data_ptr(), None if offsets is None else offsets.data_ptr(), w1.data_ptr(),
-        w1_scale.data_ptr(), w3.data_ptr(), w3_scale.data_ptr(), h.data_ptr(), scale.data_ptr(), ws.data_ptr(),
-        ws.numel(), _raw_stream(stream, a.device))
-    if status:
-        raise MoeError(status, "moe_fp8_gated")
-    return h, scale
+    r = (_binding or _load_binding()).fp8_gated(a, a_scale, w1, w1_scale, w3, w3_scale, ws, offsets, _handle(stream))
+    if type(r) is int:
+        raise MoeError(r, "moe_fp8_gated")
+    return r
 
 
 @dataclass
@@ -647,7 +596,7 @@ def fp8_layer_forward(dims: Dims, x, xq, xq_scale, Wg, routed: Fp8Weights, ws, b
                                      ctypes.byref(g) if g is not None else None, ctypes.byref(f),
                                      ctypes.byref(fs) if fs is not None else None, _p(out),
                                      ctypes.byref(r) if r is not None else None, _p(ws), ws.numel(),
-                                     _raw_stream(stream, dev)), "moe_fp8_layer_forward")
+                                     _stream(stream)), "moe_fp8_layer_forward")
     return out
 
 
