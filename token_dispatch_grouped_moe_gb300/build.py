@@ -108,7 +108,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         tmp = BINDING + ".tmp"
         torch_lib = os.path.join(_torch_dir(), "lib")
         _run(["g++", "-shared", "-o", tmp, binding_obj, f"-L{PKG}", "-l:libmoe_gb300.so", "-Wl,-rpath,$ORIGIN",
-              f"-L{torch_lib}", f"-Wl,-rpath,{torch_lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"],
+              f"-L{torch_lib}", f"-Wl,-rpath,{torch_lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"],
              "link of the Python binding")
         os.replace(tmp, BINDING)
     if verbose:

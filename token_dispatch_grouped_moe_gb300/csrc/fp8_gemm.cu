@@ -54,6 +54,7 @@ constexpr int A_BYTES = BM * BK;   // 16 KB
 constexpr int FOLD_WARPS = 8;
 constexpr int FOLD_THREADS = 32 * FOLD_WARPS;
 constexpr int FACTOR_WARPS = 2;
+constexpr int TILE_SLOTS = 4;      // the factor warps are at most two blocks, so two pieces, ahead
 constexpr int NUM_THREADS = FOLD_THREADS + 128;
 // registers: 12 warps are launched with 168 each; the fold warps (128
 // accumulators, two 32-column loads in flight) take 216 once the other
@@ -75,6 +76,10 @@ struct Cfg {
     static constexpr uint32_t IDESC = idesc_e4m3_f32(TILE_ROWS, BN);
 };
 
+struct Tile {
+    int g, row0, rows, n_tile;
+};
+
 template <int STAGES>
 struct SmemTail {
     uint64_t full[STAGES];
@@ -89,6 +94,7 @@ struct SmemTail {
     int most_rows;                     // rows of the fullest tile
     int tile_start[MAX_GROUPS + 1];    // tiles before each group
     int offsets[MAX_GROUPS + 1];
+    Tile tile[TILE_SLOTS];             // the pieces' tiles, decoded by a factor warp
     float2 factor[2][BM];              // sa * sw of each row: column halves (gated: W1 and W3)
     float amax[2][2][BM];              // gated: [tile parity][column half][row]
     uint4 stage_out[FOLD_WARPS][32 * 4];   // 64 bytes of a fold warp's 32 rows, on their way out
@@ -99,10 +105,6 @@ constexpr size_t smem_bytes()
     return 1024 + (size_t)Cfg<PAIR>::STAGES * Cfg<PAIR>::STAGE_BYTES + sizeof(SmemTail<Cfg<PAIR>::STAGES>);
 }
 static_assert(smem_bytes<false>() <= 227 * 1024 && smem_bytes<true>() <= 227 * 1024, "shared memory");
-
-struct Tile {
-    int g, row0, rows, n_tile;
-};
 
 // Tile w: tiles go expert-major, then N tile, then M tile (neighbouring CTAs
 // share the weights of an N tile in L2). This CTA's rows start `sub` rows into
@@ -555,34 +557,54 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             uint32_t buf_phase = 0;
             bool ok = true;
             Walk walk(plan, unit, n_units, k_blocks);
-            for (Piece pc; ok && walk.next(pc);) {
-                const Tile it = decode_tile<C::TILE_ROWS>(pc.tile, n_tiles, st->tile_start, st->offsets, G, sub);
-                const int kb0 = pc.kb0, kb1 = pc.kb1;
-                const float* sa0 = args.a_scale + (int64_t)min(it.row0 + r0, args.R - 1) * k_blocks;
-                const float* sa1 = args.a_scale + (int64_t)min(it.row0 + r0 + 32, args.R - 1) * k_blocks;
+            Piece pc;
+            bool have = walk.next(pc);
+            int n = 0, kb = 0;
+            const float *sa0 = nullptr, *sa1 = nullptr, *sw0 = nullptr, *sw1 = nullptr;
+            Tile it;
+            auto enter = [&]() {   // the piece's scales
+                it = decode_tile<C::TILE_ROWS>(pc.tile, n_tiles, st->tile_start, st->offsets, G, sub);
+                kb = pc.kb0;
+                sa0 = args.a_scale + (int64_t)min(it.row0 + r0, args.R - 1) * k_blocks;
+                sa1 = args.a_scale + (int64_t)min(it.row0 + r0 + 32, args.R - 1) * k_blocks;
                 // gated: the slice's block of W1 and of W3; product: each half's block
                 const int64_t b0 = (int64_t)it.g * n_blocks + (GATED ? it.n_tile : 2 * it.n_tile);
                 const int64_t b1 = GATED || 2 * it.n_tile + 1 == n_blocks ? b0 : b0 + 1;
-                const float* sw0 = args.w0_scale + b0 * k_blocks;
-                const float* sw1 = (GATED ? args.w1_scale : args.w0_scale) + b1 * k_blocks;
-                float x0 = __ldg(sa0 + kb0), x1 = __ldg(sa1 + kb0), y0 = __ldg(sw0 + kb0), y1 = __ldg(sw1 + kb0);
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    const float2 f0 = make_float2(x0 * y0, x0 * y1), f1 = make_float2(x1 * y0, x1 * y1);
-                    if (kb + 1 < kb1) {   // the next block's scales, while the slot is waited for
-                        x0 = __ldg(sa0 + kb + 1);
-                        x1 = __ldg(sa1 + kb + 1);
-                        y0 = __ldg(sw0 + kb + 1);
-                        y1 = __ldg(sw1 + kb + 1);
-                    }
-                    ok = __all_sync(0xffffffffu,
-                                    mbar_wait(smem_u32(&st->ffree[buf]), buf_phase ^ 1u, abort, args.err));
-                    if (!ok) break;
-                    st->factor[buf][r0] = f0;
-                    st->factor[buf][r0 + 32] = f1;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&st->tfull[buf]));
-                    if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
+                sw0 = args.w0_scale + b0 * k_blocks;
+                sw1 = (GATED ? args.w1_scale : args.w0_scale) + b1 * k_blocks;
+            };
+            float x0 = 0.0f, x1 = 0.0f, y0 = 0.0f, y1 = 0.0f;
+            auto fetch = [&]() {
+                x0 = __ldg(sa0 + kb);
+                x1 = __ldg(sa1 + kb);
+                y0 = __ldg(sw0 + kb);
+                y1 = __ldg(sw1 + kb);
+            };
+            if (have) {
+                enter();
+                fetch();
+            }
+            while (have) {
+                const float2 f0 = make_float2(x0 * y0, x0 * y1), f1 = make_float2(x1 * y0, x1 * y1);
+                const bool opens = kb == pc.kb0;
+                const Tile now = it;
+                const int slot = n % TILE_SLOTS;
+                // the next block's scales, of the next piece after the last, while the
+                // slot is waited for
+                if (++kb == pc.kb1) {
+                    have = walk.next(pc);
+                    ++n;
+                    if (have) enter();
                 }
+                if (have) fetch();
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&st->ffree[buf]), buf_phase ^ 1u, abort, args.err));
+                if (!ok) break;
+                if (opens && warp == 10 && lane == 0) st->tile[slot] = now;
+                st->factor[buf][r0] = f0;
+                st->factor[buf][r0 + 32] = f1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&st->tfull[buf]));
+                if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
             }
         }
     } else {
@@ -601,10 +623,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         // for the tensor cores, so that the barriers below stay matched
         bool ok = true;
         Walk walk(plan, unit, n_units, k_blocks);
-        for (Piece pc; walk.next(pc);) {
-            const Tile it = decode_tile<C::TILE_ROWS>(pc.tile, n_tiles, st->tile_start, st->offsets, G, sub);
-            const bool valid = r < it.rows;
-            const int p = it.row0 + r;
+        int n = 0;
+        for (Piece pc; walk.next(pc); ++n) {
             float acc[128];
 #pragma unroll
             for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
@@ -645,6 +665,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 fold32<96>(acc, v, c1);
             }
 
+            const Tile it = ok ? st->tile[n % TILE_SLOTS] : Tile{0, 0, 0, 0};
+            const bool valid = r < it.rows;
+            const int p = it.row0 + r;
             if (pc.kb1 - pc.kb0 < k_blocks) {
                 // publish this piece's part (its rows side by side) and take a ticket;
                 // the last piece of the tile joins the parts

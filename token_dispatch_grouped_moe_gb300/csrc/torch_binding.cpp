@@ -11,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -115,7 +116,7 @@ struct Launch {
 
 Tensor empty(std::initializer_list<int64_t> size, at::ScalarType type, at::Device dev)
 {
-    return at::empty(at::IntArrayRef(size), at::TensorOptions().dtype(type).device(dev));
+    return Tensor(at::detail::empty_cuda(at::IntArrayRef(size), type, dev, std::nullopt));
 }
 
 // A status as the Python int that lib.py turns into MoeError.
