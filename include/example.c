@@ -26,6 +26,22 @@ int moe_forward(const moe_bf16* x, const moe_bf16* Wg, const moe_bf16* W1, const
     return st;
 }
 
+/* The same layer on 8-bit experts, in a residual stream: sum = x + residual and
+ * its norm, quantized, then the layer. `experts` holds weights made once with
+ * moe_fp8_quantize_weight; y, q and scale are [T, 4096] bf16, [T, 4096] e4m3
+ * and [T, 32] floats; ws is moe_fp8_workspace_size(&d) bytes, zeroed once. */
+int moe_forward_fp8(const moe_bf16* x, const moe_bf16* residual, const moe_bf16* norm_weight, const moe_bf16* Wg,
+                    const moe_fp8_ffn* experts, moe_bf16* sum, moe_bf16* y, moe_e4m3* q, float* scale,
+                    moe_bf16* out, int64_t T, void* ws, cudaStream_t stream)
+{
+    moe_dims d = {T, 4096, 14336, 8, 2, 0};
+    moe_status st = moe_add_rmsnorm_fp8(T, d.H, MOE_BF16, x, d.H, residual, d.H, norm_weight, 1e-6f, sum, d.H, y,
+                                        q, scale, (moe_stream_t)stream);
+    if (st != MOE_OK) return st;
+    return moe_fp8_layer_forward(&d, y, q, scale, Wg, NULL, NULL, experts, NULL, out, NULL, ws,
+                                 moe_fp8_workspace_size(&d), (moe_stream_t)stream);
+}
+
 #ifdef MOE_EXAMPLE_MAIN
 int main(void) { return 0; }
 #endif

@@ -34,6 +34,22 @@
 // workspace and takes a ticket, and the last one adds the parts in the order of
 // their blocks (so the result does not depend on which came last) and runs the
 // epilogue. No CTA waits for another. Every wait is bounded (ptx.cuh).
+//
+// What bounds it (one GB300):
+//   - many rows: the fold. A block's MMAs take 512 cycles; folding its 128 x 256
+//     sums takes 256 cycles of the FMA pipe in each SM quarter and, with the trips
+//     to TMEM and the barriers, 800-900 in all, of which the MMAs of the next block
+//     cover theirs. 8192 x 8192 x 8192: 400-420 us, 2.6-2.75 PFLOP/s (a library
+//     product without block scales: 3.6-3.8); back to back the GPU is at its power
+//     cap (1350 W, 1.5-1.6 GHz) and the rate that of the energy. Measured and not
+//     kept: pairs of sums in fma.rn.f32x2 (register moves: 2.0 PFLOP/s), factors
+//     four blocks at a time, N = 128 MMAs with four buffers, loads of the next block
+//     asked for before the last sums (spills), a release without memory order.
+//   - few rows: the weights' bytes: 1024 tokens, 64 experts 2048 -> 1408, top 6
+//     5.6 TB/s, 789 tokens 2560 -> 3584, top 8 6.2 TB/s (0.83, 0.92 of a copy).
+//   - one token: latency (11 us for 6 experts 1408 -> 2048: the first loads land
+//     5 us after the previous kernel's end) and, on wide experts, the last run's
+//     tail (8 experts 4096 -> 14336, top 2: 54 us for 235 MB).
 #include <atomic>
 #include <cstdint>
 #include <cuda.h>
