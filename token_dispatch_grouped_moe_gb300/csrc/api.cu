@@ -19,7 +19,7 @@
 namespace moe {
 namespace {
 
-constexpr int kVersion = 300;   // 0.3.0
+constexpr int kVersion = 400;   // 0.4.0
 constexpr int kMaxDevices = 64;
 
 // ------------------------------------------------------------ device info --
