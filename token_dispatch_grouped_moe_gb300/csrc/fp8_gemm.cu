@@ -96,6 +96,14 @@ struct Tile {
     int g, row0, rows, n_tile;
 };
 
+// The schedule: the first `full` tiles whole, round robin over the CTAs; the K
+// blocks of the rest, end to end, in `segments` equal runs, one a CTA. A run
+// that begins or ends inside a tile computes a part of its sums.
+struct Plan {
+    int tiles, full, segments;
+    int part_rows;   // rows a part has room for: those of the fullest tile
+};
+
 template <int STAGES>
 struct SmemTail {
     uint64_t full[STAGES];
@@ -112,7 +120,7 @@ struct SmemTail {
     int offsets[MAX_GROUPS + 1];
     Tile tile[TILE_SLOTS];             // the pieces' tiles, decoded by a factor warp
     float2 factor[2][BM];              // sa * sw of each row: column halves (gated: W1 and W3)
-    float amax[2][2][BM];              // gated: [tile parity][column half][row]
+    float amax[2][2][BM];              // gated: [piece parity][column half][row]
     uint4 stage_out[FOLD_WARPS][32 * 4];   // 64 bytes of a fold warp's 32 rows, on their way out
 };
 template <bool PAIR>
@@ -142,14 +150,6 @@ __device__ __forceinline__ Tile decode_tile(int w, int n_tiles, const int* ts, c
     r.rows = min(BM, offs[lo + 1] - r.row0);
     return r;
 }
-
-// The schedule: the first `full` tiles whole, round robin over the CTAs; the K
-// blocks of the rest, end to end, in `segments` equal runs, one a CTA. A run
-// that begins or ends inside a tile computes a part of its sums.
-struct Plan {
-    int tiles, full, segments;
-    int part_rows;   // rows a part has room for: those of the fullest tile
-};
 
 struct Piece {
     int tile, kb0, kb1;
@@ -198,38 +198,46 @@ __device__ __forceinline__ int first_part(const Plan& p, int q, int k_blocks, in
     return first;
 }
 
+// The join of a tile's parts (below): rows of a warp and parts whose loads are in
+// flight together. More of either spill the registers of the fold (measured:
+// a gated batch 72 -> 107 us).
+constexpr int JOIN_ROWS = 2;
+constexpr int JOIN_PARTS = 2;
+
 // The plan with the least estimated time, counted in K blocks of one CTA (0.42
-// us): whole tiles cost their blocks and kFp8TileCost; cutting tiles costs the
-// parts' publication and the join, a trip to L2 for every 8 rows and 4 parts.
-// Measured (us, whole tiles / best cut): one row, 16 tiles of 112 blocks for
-// each of 2 experts 55.6 / 27.8; 64 rows, 16 tiles of 32 blocks 17.2 / 15.7;
-// 128 rows, 16 tiles of 32 blocks 19.4 / 22.7; 333 rows, 42 tiles of 160 blocks
-// 74.7 / 45.7.
-__device__ __forceinline__ Plan make_plan(int tiles, int rows, int k_blocks, int n_cta)
+// us), one candidate a lane (the warp calls it together): lane 0 every tile
+// whole, which costs its blocks and kFp8TileCost; lane l the tiles, where they
+// fill less than one round, in l + 1 parts each; lane 31 the tiles beyond the
+// whole rounds but one (or all of them) in equal runs. Cutting costs the parts'
+// publication, twice where the runs do not line up with tiles, and the join's
+// trips to L2. Measured (us, whole tiles / best cut): one row, 16 tiles of 112
+// blocks for each of 2 experts 55.6 / 27.8; 64 rows, 16 tiles of 32 blocks 17.2
+// / 15.7; 128 rows, 16 tiles of 32 blocks 19.4 / 22.7; 333 rows, 42 tiles of 160
+// blocks 74.7 / 43.
+__device__ __forceinline__ Plan make_plan(int tiles, int rows, int k_blocks, int n_cta, int lane)
 {
-    Plan best{tiles, tiles, 0, rows};
-    if (tiles == 0 || (int64_t)2 * n_cta * rows > kFp8PartRows || 2 * n_cta > kFp8MaxTickets) return best;
+    const bool room = (int64_t)2 * n_cta * rows <= kFp8PartRows && 2 * n_cta <= kFp8MaxTickets;
     const int rounds = tiles / n_cta;
-    float best_cost = (float)((tiles + n_cta - 1) / n_cta) * ((float)k_blocks + kFp8TileCost);
-    // cut the tiles beyond the whole rounds but one (or all of them, when there
-    // is less than one round) into `segments` runs
-    const int full = rounds > 1 ? (rounds - 1) * n_cta : 0;
-    const int64_t total = (int64_t)(tiles - full) * k_blocks;
-    auto consider = [&](int segments, int parts, float cuts) {
-        if (total < (int64_t)2 * segments) return;
-        const float cost = (float)(full / n_cta) * ((float)k_blocks + kFp8TileCost) +
-                           (float)((total + segments - 1) / segments) + cuts * kFp8CutCost +
-                           kFp8JoinCost * (float)((rows + 7) / 8) * (float)((parts + 3) / 4);
-        if (cost < best_cost) {
-            best_cost = cost;
-            best.full = full;
-            best.segments = segments;
-        }
-    };
-    for (int s = 2; s <= kFp8MaxSplit && tiles * s <= n_cta; ++s) consider(tiles * s, s, 1.0f);
-    // runs that do not line up with tiles leave most CTAs two parts
-    if (tiles % n_cta != 0) consider(n_cta, n_cta / (tiles - full) + 2, 2.0f);
-    return best;
+    const float whole = (float)k_blocks + kFp8TileCost;
+    int full = tiles, segments = 0, parts = 0;
+    float cost = (float)((tiles + n_cta - 1) / n_cta) * whole;
+    bool fits = lane == 0;
+    if (lane > 0 && room && tiles > 0) {
+        full = rounds > 1 ? (rounds - 1) * n_cta : 0;
+        segments = lane == 31 ? n_cta : tiles * (lane + 1);
+        parts = lane == 31 ? n_cta / (tiles - full) + 2 : lane + 1;
+        const int64_t total = (int64_t)(tiles - full) * k_blocks;
+        fits = total >= (int64_t)2 * segments &&
+               (lane == 31 ? tiles % n_cta != 0 : lane < kFp8MaxSplit && segments <= n_cta);
+        cost = (float)(full / n_cta) * whole + (float)((total + segments - 1) / segments) +
+               (lane == 31 ? 2.0f : 1.0f) * kFp8CutCost +
+               kFp8JoinCost * (float)((rows + FOLD_WARPS * JOIN_ROWS - 1) / (FOLD_WARPS * JOIN_ROWS)) *
+                   (float)((parts + JOIN_PARTS - 1) / JOIN_PARTS);
+    }
+    // the least cost (its low bits give way to the lane)
+    const uint32_t key = fits ? (__float_as_uint(cost) & ~31u) | (uint32_t)lane : 0xffffffffu;
+    const int best = (int)(__reduce_min_sync(0xffffffffu, key) & 31u);
+    return Plan{tiles, __shfl_sync(0xffffffffu, full, best), __shfl_sync(0xffffffffu, segments, best), rows};
 }
 
 __device__ __forceinline__ void fold_barrier()   // the fold warps only
@@ -291,9 +299,6 @@ __device__ __forceinline__ void store_rows(uint4* buf, int lane, const uint4 (&v
 // columns of each half of a row, with JOIN_PARTS parts' loads in flight together
 // (the parts were just written, so a load is a trip to L2; what bounds the join
 // is the number of trips, not the bytes).
-constexpr int JOIN_ROWS = 2;
-constexpr int JOIN_PARTS = 2;
-
 template <bool GATED, typename OUT>
 __device__ __forceinline__ void join(const Fp8GemmArgs& args, const Tile& it, int first, int parts, int stride,
                                      int n_blocks, int warp, int lane)
@@ -451,8 +456,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const int n_out = GATED ? BN / 2 : BN;   // output columns of a tile
     const int n_tiles = (args.N + n_out - 1) / n_out;
     const int k_blocks = (args.K + BK - 1) / BK;
-    const int tiles = st->tile_start[G] * n_tiles;
-    const Plan plan = PAIR ? Plan{tiles, tiles, 0, 0} : make_plan(tiles, st->most_rows, k_blocks, n_units);
+    const int all_tiles = st->tile_start[G] * n_tiles;
+    const Plan plan = PAIR ? Plan{all_tiles, all_tiles, 0, 0}   // pairs cut nothing
+                           : make_plan(all_tiles, st->most_rows, k_blocks, n_units, lane);
     volatile int* abort = &st->abort;
 
     if (warp >= 8) {
@@ -629,12 +635,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         const int half = warp >> 2;                  // MMA columns 128 half .. + 127
         const int r = (warp & 3) * 32 + lane;        // row of the tile = TMEM lane
         const uint32_t t_row = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + half * 128;
-        const int n_blocks = (args.N + kFp8Block - 1) / kFp8Block;
         int stage = 0;
         int buf = 0;
         uint32_t buf_phase = 0;
         bool ready = false;    // the next block is known to be there
-        uint32_t parity = 0;   // which amax buffer this tile uses
         // after an abort every fold warp still walks all pieces, without waiting
         // for the tensor cores, so that the barriers below stay matched
         bool ok = true;
@@ -681,6 +685,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 fold32<96>(acc, v, c1);
             }
 
+            const int n_blocks = (args.N + kFp8Block - 1) / kFp8Block;
             const Tile it = ok ? st->tile[n % TILE_SLOTS] : Tile{0, 0, 0, 0};
             const bool valid = r < it.rows;
             const int p = it.row0 + r;
@@ -727,10 +732,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     amax = max_nan(amax, fabsf(acc[i]));
                 }
                 // the block's maximum: this half's and the other's
-                st->amax[parity][half][r] = amax;
+                st->amax[n & 1][half][r] = amax;
                 fold_barrier();
-                amax = max_nan(amax, st->amax[parity][half ^ 1][r]);
-                parity ^= 1u;
+                amax = max_nan(amax, st->amax[n & 1][half ^ 1][r]);
                 const float scale = fp8_scale(amax);
                 const float inv = 1.0f / scale;
                 unsigned char* out[4];
