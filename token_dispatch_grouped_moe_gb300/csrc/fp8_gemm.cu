@@ -40,11 +40,16 @@
 //     sums takes 256 cycles of the FMA pipe in each SM quarter and, with the trips
 //     to TMEM and the barriers, 800-900 in all, of which the MMAs of the next block
 //     cover theirs. 8192 x 8192 x 8192: 400-420 us, 2.6-2.75 PFLOP/s (a library
-//     product without block scales: 3.6-3.8); back to back the GPU is at its power
-//     cap (1350 W, 1.5-1.6 GHz) and the rate that of the energy. Measured and not
-//     kept: pairs of sums in fma.rn.f32x2 (register moves: 2.0 PFLOP/s), factors
-//     four blocks at a time, N = 128 MMAs with four buffers, loads of the next block
-//     asked for before the last sums (spills), a release without memory order.
+//     product without block scales: 3.6-3.8). A buffer's round trip is about 950
+//     cycles from its release to the next sums (the release seen, MMAs issued, 512
+//     of MMAs, the commit seen) and 700 to the next release, for two buffers. Back
+//     to back the product is at the GPU's power cap as well (1350 W, 1.6 GHz); the
+//     gated form, with about 4000 cycles of epilogue a tile (silu 1750, conversion
+//     and stores 1200), runs at 1.97 GHz. Measured and not kept: pairs of sums in
+//     fma.rn.f32x2 (register moves: 2.0 PFLOP/s), factors four blocks at a time, N =
+//     128 MMAs with four buffers, loads of the next block asked for before the last
+//     sums (spills), releases without memory order, one reciprocal for two silus,
+//     and warps without rows of a tile passing its blocks on unread.
 //   - few rows: the weights' bytes: 1024 tokens, 64 experts 2048 -> 1408, top 6
 //     5.6 TB/s, 789 tokens 2560 -> 3584, top 8 6.2 TB/s (0.83, 0.92 of a copy).
 //   - one token: latency (11 us for 6 experts 1408 -> 2048: the first loads land
