@@ -591,3 +591,10 @@ def test_layer_gating_variants(lib):
         # e4m3 activations, weights and h: three roundings of at most 2^-4, as independent errors
         assert float((a - b).norm() / b.norm()) <= 2 ** -4 * 3 ** 0.5
     assert float((run(renormalize=False) - run()).norm()) > 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = lib.fp8_layer_forward(dims, y, q, qs, Wg, layer.routed, ws, shared=layer.shared, stream=side)
+    side.synchronize()
+    assert torch.equal(got.double(), run())
+    with pytest.raises(ValueError):
+        run(shared_gate=wsg[:64])

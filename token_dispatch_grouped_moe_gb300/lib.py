@@ -579,8 +579,11 @@ def fp8_layer_forward(dims: Dims, x, xq, xq_scale, Wg, routed: Fp8Weights, ws, b
     _expect(Wg, "Wg", (H, dims.E), torch.bfloat16, dev)
     if bias is not None:
         _expect(bias, "bias", (dims.E,), torch.float32, dev)
+    if shared_gate is not None:
+        _expect(shared_gate, "shared_gate", (H,), torch.bfloat16, dev)
     if out is None:
-        out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+        with torch.cuda.stream(stream):   # the memory is the stream's that writes it
+            out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
     else:
         _expect(out, "out", (T, H), torch.bfloat16, dev)
     if dims.F_shared > 0 and shared is None:
