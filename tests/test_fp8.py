@@ -323,6 +323,7 @@ PRODUCTS = [   # K, N, rows of each group
     (4096, 1024, [1]), (4096, 1024, [40]), (14336, 256, [1, 0, 1]), (14336, 256, [2, 128, 1]), (20480, 384, [333]),
     (2048, 1408, [90 + (7 * i) % 13 for i in range(64)]), (512, 128, [1] * 256), (256, 512, [3] * 255 + [1000]),
     (256, 320, [2085]), (400, 272, [3000, 0, 5001, 100]), (4096, 14336, [1, 1]), (2048, 40960, [17]), (16384, 512, [1]),
+    (8192, 272, [130]), (8192, 144, [20, 40, 0, 33]), (1024, 2064, [1]), (1040, 2064, [1]),
 ]
 
 

@@ -69,16 +69,32 @@ Fp8GemmArgs product_args(int32_t R, int32_t K, int32_t N, int32_t G, const int32
 // one CTA.
 bool pair_for(int64_t R, int32_t G, bool gated) { return R >= (int64_t)(gated ? 512 : 2048) * G; }
 
+// The form of a product: a pair as above; tiles of 128 columns where all of them
+// find an SM (counted from above: every group may begin a tile) and the blocks
+// are few, or the rows too many for a cheap join of cut tiles; else of 256.
+// Measured, 256 / 128 columns, us, one group N = 4096: 8 rows K = 512 6.5 / 5.8,
+// 4096: 11.3 / 11.9; 16 rows K = 2048 9.8 / 9.4; 64 rows K = 4096 15.6 / 13.4;
+// 512 rows K = 4096 19.6 / 16.0, 8192: 29.3 / 26.4, 12288: 36.3 / 38.0; two of 8
+// experts 14336 -> 4096, one row each 29.7 / 40.9; 6 of 64 1408 -> 2048 10.5 /
+// 11.4; 160 tiles of 128 columns on 152 SMs 20.0 / 28.0.
+Fp8GemmForm product_form(int64_t R, int32_t K, int32_t N, int32_t G, int sms)
+{
+    if (pair_for(R, G, false)) return kFp8Pair;
+    const int64_t m_tiles = G == 1 ? (R + 127) / 128 : R / 128 + (R < G ? R : G);
+    const bool fit = m_tiles * ((N + 127) / 128) <= sms;
+    return fit && (K <= 1024 || (K <= 8192 && R >= (int64_t)16 * G)) ? kFp8Narrow : kFp8Wide;
+}
+
 moe_status run_product(Fp8GemmArgs a, const moe_e4m3* A, Operand w, bool f32, void* out, int sms, cudaStream_t s)
 {
     CUtensorMap ma, mw;
-    const bool pair = pair_for(a.R, a.G, false);
+    const Fp8GemmForm form = product_form(a.R, a.K, a.N, a.G, sms);
     if (!encode_map_e4m3(&ma, A, (uint64_t)a.K, (uint64_t)a.R, 0, kFp8Block, 128) ||
-        !encode_map_e4m3(&mw, w.v, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.G, kFp8Block, fp8_box_rows(false, pair)))
+        !encode_map_e4m3(&mw, w.v, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.G, kFp8Block, fp8_box_rows(false, form)))
         return MOE_ERR_CUDA;
     a.w0_scale = w.scale;
     a.out = out;
-    MOE_TRY(launch_fp8_gemm(f32 ? kFp8ProductF32 : kFp8ProductBf16, pair, ma, mw, mw, a, sms, s));
+    MOE_TRY(launch_fp8_gemm(f32 ? kFp8ProductF32 : kFp8ProductBf16, form, ma, mw, mw, a, sms, s));
     return MOE_OK;
 }
 
@@ -86,16 +102,16 @@ moe_status run_gated(Fp8GemmArgs a, const moe_e4m3* A, Operand w1, Operand w3, m
                      cudaStream_t s)
 {
     CUtensorMap ma, m1, m3;
-    const bool pair = pair_for(a.R, a.G, true);
+    const Fp8GemmForm form = pair_for(a.R, a.G, true) ? kFp8Pair : kFp8Wide;
     if (!encode_map_e4m3(&ma, A, (uint64_t)a.K, (uint64_t)a.R, 0, kFp8Block, 128) ||
-        !encode_map_e4m3(&m1, w1.v, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.G, kFp8Block, fp8_box_rows(true, pair)) ||
-        !encode_map_e4m3(&m3, w3.v, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.G, kFp8Block, fp8_box_rows(true, pair)))
+        !encode_map_e4m3(&m1, w1.v, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.G, kFp8Block, fp8_box_rows(true, form)) ||
+        !encode_map_e4m3(&m3, w3.v, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.G, kFp8Block, fp8_box_rows(true, form)))
         return MOE_ERR_CUDA;
     a.w0_scale = w1.scale;
     a.w1_scale = w3.scale;
     a.out = h;
     a.out_scale = h_scale;
-    MOE_TRY(launch_fp8_gemm(kFp8Gated, pair, ma, m1, m3, a, sms, s));
+    MOE_TRY(launch_fp8_gemm(kFp8Gated, form, ma, m1, m3, a, sms, s));
     return MOE_OK;
 }
 

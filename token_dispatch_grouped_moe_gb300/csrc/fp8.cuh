@@ -38,6 +38,8 @@ constexpr size_t kFp8PartOffset = 256 + (size_t)kFp8MaxTickets * 4;
 constexpr size_t kFp8WorkspaceBytes = kFp8PartOffset + (size_t)kFp8PartRows * 256 * 4;
 
 enum Fp8GemmMode { kFp8Gated = 0, kFp8ProductBf16 = 1, kFp8ProductF32 = 2 };
+// one CTA per MMA of 256 columns; of 128 (products only); a CTA pair per MMA
+enum Fp8GemmForm { kFp8Wide = 0, kFp8Narrow = 1, kFp8Pair = 2 };
 
 struct Fp8GemmArgs {
     int32_t R;                  // rows of A
@@ -59,10 +61,10 @@ struct Fp8GemmArgs {
     uint32_t* err;
 };
 
-// tmA: A [R, K] e4m3, box 128 x 128; tmB0 / tmB1: weights [G, N, K], box 128 x
-// fp8_box_rows rows; 128-byte swizzle. pair: two CTAs per MMA.
-inline uint32_t fp8_box_rows(bool gated, bool pair) { return gated ? 64 : pair ? 128 : 256; }
-cudaError_t launch_fp8_gemm(Fp8GemmMode mode, bool pair, const CUtensorMap& tmA, const CUtensorMap& tmB0,
+// tmA: A [R, K] e4m3, box 128 x 128; tmB0 / tmB1: weights [G, N, K] (gated: W1
+// and W3; product: tmB1 unused), box 128 x fp8_box_rows; 128-byte swizzle.
+inline uint32_t fp8_box_rows(bool gated, Fp8GemmForm form) { return gated ? 64 : form == kFp8Wide ? 256 : 128; }
+cudaError_t launch_fp8_gemm(Fp8GemmMode mode, Fp8GemmForm form, const CUtensorMap& tmA, const CUtensorMap& tmB0,
                             const CUtensorMap& tmB1, const Fp8GemmArgs& a, int num_sms, cudaStream_t s);
 
 struct Fp8NormArgs {

@@ -28,6 +28,8 @@
 // CTA pairs (PAIR): a 2-CTA cluster shares one tcgen05.mma.cta_group::2 of M =
 // 256; both CTAs' boxes complete on rank 0's barrier, rank 0 issues, its commit
 // arrives in both CTAs, and both CTAs' fold warps release a buffer on rank 0.
+// A product of few tiles takes tiles of 128 columns (BN; 64 accumulators a thread,
+// a buffer given back after one trip to TMEM: 0.28 us a block instead of 0.42).
 // When the tiles do not fill the SMs evenly (few rows), K is cut: the blocks of
 // the tiles that are left over, end to end, go to the CTAs in equal runs; each
 // CTA writes the fp32 sums of a tile that it has only a part of to the
@@ -69,7 +71,6 @@ namespace moe {
 namespace {
 
 constexpr int BM = 128;
-constexpr int BN = 256;            // MMA N (gated: 128 of W1 and 128 of W3, interleaved by 64)
 constexpr int BK = kFp8Block;      // one scale block of K = one 128-byte swizzle span
 constexpr int A_BYTES = BM * BK;   // 16 KB
 constexpr int FOLD_WARPS = 8;
@@ -83,16 +84,18 @@ constexpr int NUM_THREADS = FOLD_THREADS + 128;
 constexpr int FOLD_REGS = 216;
 constexpr int OTHER_REGS = 72;
 constexpr int MAX_GROUPS = 256;
-constexpr int TMEM_COLS = 512;
 
 // One CTA per MMA (PAIR false): a stage holds 128 rows of A and 256 of B. A CTA
 // pair (tcgen05 cta_group::2): one MMA of 256 x 256 over both CTAs, each staging
 // its 128 rows of A and half of B's, so a third less comes from L2 per block.
-template <bool PAIR>
+// BN is the MMA's N (gated: 128 columns of W1 and 128 of W3, interleaved by 64):
+// 256, or 128 for a product whose tiles of 256 fill less than half of the SMs.
+template <bool PAIR, int BN>
 struct Cfg {
     static constexpr int B_ROWS = PAIR ? BN / 2 : BN;
     static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * BK;   // 48 KB or 32 KB
-    static constexpr int STAGES = PAIR ? 6 : 4;
+    static constexpr int STAGES = STAGE_BYTES == 48 * 1024 ? 4 : 6;
+    static constexpr int TMEM_COLS = 2 * BN;                    // two buffers
     static constexpr int TILE_ROWS = PAIR ? 2 * BM : BM;        // rows of one work item
     static constexpr uint32_t IDESC = idesc_e4m3_f32(TILE_ROWS, BN);
 };
@@ -128,12 +131,14 @@ struct SmemTail {
     float amax[2][2][BM];              // gated: [piece parity][column half][row]
     uint4 stage_out[FOLD_WARPS][32 * 4];   // 64 bytes of a fold warp's 32 rows, on their way out
 };
-template <bool PAIR>
+template <bool PAIR, int BN>
 constexpr size_t smem_bytes()
 {
-    return 1024 + (size_t)Cfg<PAIR>::STAGES * Cfg<PAIR>::STAGE_BYTES + sizeof(SmemTail<Cfg<PAIR>::STAGES>);
+    using C = Cfg<PAIR, BN>;
+    return 1024 + (size_t)C::STAGES * C::STAGE_BYTES + sizeof(SmemTail<C::STAGES>);
 }
-static_assert(smem_bytes<false>() <= 227 * 1024 && smem_bytes<true>() <= 227 * 1024, "shared memory");
+static_assert(smem_bytes<false, 256>() <= 227 * 1024 && smem_bytes<true, 256>() <= 227 * 1024 &&
+                  smem_bytes<false, 128>() <= 227 * 1024, "shared memory");
 
 // Tile w: tiles go expert-major, then N tile, then M tile (neighbouring CTAs
 // share the weights of an N tile in L2). This CTA's rows start `sub` rows into
@@ -206,7 +211,8 @@ __device__ __forceinline__ int first_part(const Plan& p, int q, int k_blocks, in
 // The join of a tile's parts (below): rows of a warp and parts whose loads are in
 // flight together. More of either spill the registers of the fold (measured:
 // a gated batch 72 -> 107 us).
-constexpr int JOIN_ROWS = 2;
+template <int BN>
+constexpr int JOIN_ROWS = BN == 256 ? 2 : 4;
 constexpr int JOIN_PARTS = 2;
 
 // The plan with the least estimated time, counted in K blocks of one CTA (0.42
@@ -219,11 +225,15 @@ constexpr int JOIN_PARTS = 2;
 // blocks for each of 2 experts 55.6 / 27.8; 64 rows, 16 tiles of 32 blocks 17.2
 // / 15.7; 128 rows, 16 tiles of 32 blocks 19.4 / 22.7; 333 rows, 42 tiles of 160
 // blocks 74.7 / 43.
+template <int BN>
 __device__ __forceinline__ Plan make_plan(int tiles, int rows, int k_blocks, int n_cta, int lane)
 {
+    // a block of 128 columns takes 0.26 us, the rest as long as for 256
+    constexpr float unit = BN == 256 ? 1.0f : 1.6f;
+    constexpr int join_rows = FOLD_WARPS * JOIN_ROWS<BN>;
     const bool room = (int64_t)2 * n_cta * rows <= kFp8PartRows && 2 * n_cta <= kFp8MaxTickets;
     const int rounds = tiles / n_cta;
-    const float whole = (float)k_blocks + kFp8TileCost;
+    const float whole = (float)k_blocks + unit * kFp8TileCost;
     int full = tiles, segments = 0, parts = 0;
     float cost = (float)((tiles + n_cta - 1) / n_cta) * whole;
     bool fits = lane == 0;
@@ -235,9 +245,9 @@ __device__ __forceinline__ Plan make_plan(int tiles, int rows, int k_blocks, int
         fits = total >= (int64_t)2 * segments &&
                (lane == 31 ? tiles % n_cta != 0 : lane < kFp8MaxSplit && segments <= n_cta);
         cost = (float)(full / n_cta) * whole + (float)((total + segments - 1) / segments) +
-               (lane == 31 ? 2.0f : 1.0f) * kFp8CutCost +
-               kFp8JoinCost * (float)((rows + FOLD_WARPS * JOIN_ROWS - 1) / (FOLD_WARPS * JOIN_ROWS)) *
-                   (float)((parts + JOIN_PARTS - 1) / JOIN_PARTS);
+               unit * ((lane == 31 ? 2.0f : 1.0f) * kFp8CutCost +
+                       kFp8JoinCost * (float)((rows + join_rows - 1) / join_rows) *
+                           (float)((parts + JOIN_PARTS - 1) / JOIN_PARTS));
     }
     // the least cost (its low bits give way to the lane)
     const uint32_t key = fits ? (__float_as_uint(cost) & ~31u) | (uint32_t)lane : 0xffffffffu;
@@ -251,8 +261,8 @@ __device__ __forceinline__ void fold_barrier()   // the fold warps only
 }
 
 // acc[C .. C + 31] += v[0 .. 31] * f
-template <int C>
-__device__ __forceinline__ void fold32(float (&acc)[128], const uint32_t (&v)[32], float f)
+template <int C, int N>
+__device__ __forceinline__ void fold32(float (&acc)[N], const uint32_t (&v)[32], float f)
 {
 #pragma unroll
     for (int i = 0; i < 32; ++i) acc[C + i] = fmaf(__uint_as_float(v[i]), f, acc[C + i]);
@@ -304,42 +314,46 @@ __device__ __forceinline__ void store_rows(uint4* buf, int lane, const uint4 (&v
 // columns of each half of a row, with JOIN_PARTS parts' loads in flight together
 // (the parts were just written, so a load is a trip to L2; what bounds the join
 // is the number of trips, not the bytes).
-template <bool GATED, typename OUT>
+template <bool GATED, typename OUT, int BN>
 __device__ __forceinline__ void join(const Fp8GemmArgs& args, const Tile& it, int first, int parts, int stride,
                                      int n_blocks, int warp, int lane)
 {
+    constexpr int ROWS = JOIN_ROWS<BN>;
+    constexpr bool TWO = BN == 256;   // a second 4 columns: of W3, or 128 further on
     // the first part begins with the tile, the others inside it (first_part)
     const float* base = args.part + (int64_t)2 * first * stride;
     auto slot = [&](int s) { return (int64_t)(s == 0 ? 1 : 2 * s) * stride; };
     // gated: 4 columns of W1's sums and the same of W3's, 64 further on
     const int c0 = GATED ? (lane >> 4) * 128 + (lane & 15) * 4 : lane * 4;
     const int c1 = c0 + (GATED ? 64 : 128);
-    for (int r0 = warp * JOIN_ROWS; r0 < it.rows; r0 += FOLD_WARPS * JOIN_ROWS) {
-        float4 a[JOIN_ROWS], b[JOIN_ROWS];
+    for (int r0 = warp * ROWS; r0 < it.rows; r0 += FOLD_WARPS * ROWS) {
+        float4 a[ROWS], b[ROWS];
 #pragma unroll
-        for (int q = 0; q < JOIN_ROWS; ++q) a[q] = b[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int q = 0; q < ROWS; ++q) a[q] = b[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int s0 = 0; s0 < parts; s0 += JOIN_PARTS) {
-            float4 x[JOIN_PARTS][JOIN_ROWS], y[JOIN_PARTS][JOIN_ROWS];
+            float4 x[JOIN_PARTS][ROWS], y[JOIN_PARTS][ROWS];
 #pragma unroll
             for (int s = 0; s < JOIN_PARTS; ++s)
 #pragma unroll
-                for (int q = 0; q < JOIN_ROWS; ++q)
+                for (int q = 0; q < ROWS; ++q)
                     if (s0 + s < parts && r0 + q < it.rows) {
                         const float* src = base + slot(s0 + s) + (r0 + q) * BN;
                         x[s][q] = __ldcg(reinterpret_cast<const float4*>(src + c0));
-                        y[s][q] = __ldcg(reinterpret_cast<const float4*>(src + c1));
+                        if (TWO) y[s][q] = __ldcg(reinterpret_cast<const float4*>(src + c1));
                     }
 #pragma unroll
             for (int s = 0; s < JOIN_PARTS; ++s)
 #pragma unroll
-                for (int q = 0; q < JOIN_ROWS; ++q)
+                for (int q = 0; q < ROWS; ++q)
                     if (s0 + s < parts && r0 + q < it.rows) {
                         a[q].x += x[s][q].x; a[q].y += x[s][q].y; a[q].z += x[s][q].z; a[q].w += x[s][q].w;
-                        b[q].x += y[s][q].x; b[q].y += y[s][q].y; b[q].z += y[s][q].z; b[q].w += y[s][q].w;
+                        if (TWO) {
+                            b[q].x += y[s][q].x; b[q].y += y[s][q].y; b[q].z += y[s][q].z; b[q].w += y[s][q].w;
+                        }
                     }
         }
 #pragma unroll
-        for (int q = 0; q < JOIN_ROWS; ++q) {
+        for (int q = 0; q < ROWS; ++q) {
             if (r0 + q >= it.rows) break;
             const int p = it.row0 + r0 + q;
             if constexpr (GATED) {
@@ -362,13 +376,14 @@ __device__ __forceinline__ void join(const Fp8GemmArgs& args, const Tile& it, in
                 OUT* dst = static_cast<OUT*>(args.out) + row * args.N;
                 const int n = it.n_tile * BN + lane * 4;
                 if (n < args.N) store4(dst + n, a[q].x * wt, a[q].y * wt, a[q].z * wt, a[q].w * wt);
-                if (n + 128 < args.N) store4(dst + n + 128, b[q].x * wt, b[q].y * wt, b[q].z * wt, b[q].w * wt);
+                if (TWO && n + 128 < args.N)
+                    store4(dst + n + 128, b[q].x * wt, b[q].y * wt, b[q].z * wt, b[q].w * wt);
             }
         }
     }
 }
 
-template <bool GATED, typename OUT, bool PAIR>
+template <bool GATED, typename OUT, bool PAIR, int BN>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
                 const __grid_constant__ CUtensorMap tmB1, const Fp8GemmArgs args)
@@ -376,7 +391,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t tiles_addr = (raw_addr + 1023u) & ~1023u;
-    using C = Cfg<PAIR>;
+    static_assert(BN == 256 || (!GATED && !PAIR), "128 columns: a product, one CTA per MMA");
+    using C = Cfg<PAIR, BN>;
+    constexpr int HALF = BN / 2;       // columns of a fold thread
     constexpr int STAGES = C::STAGES;
     constexpr int STAGE_BYTES = C::STAGE_BYTES;
     constexpr int CG = PAIR ? 2 : 1;   // tcgen05 CTA group
@@ -411,7 +428,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         if (GATED) tma_prefetch_desc(&tmB1);
     }
     if (warp == 9) {
-        tmem_alloc<CG>(smem_u32(&st->tmem_base), TMEM_COLS);
+        tmem_alloc<CG>(smem_u32(&st->tmem_base), C::TMEM_COLS);
         tmem_relinquish<CG>();
     }
     pdl_wait();
@@ -463,7 +480,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const int k_blocks = (args.K + BK - 1) / BK;
     const int all_tiles = st->tile_start[G] * n_tiles;
     const Plan plan = PAIR ? Plan{all_tiles, all_tiles, 0, 0}   // pairs cut nothing
-                           : make_plan(all_tiles, st->most_rows, k_blocks, n_units, lane);
+                           : make_plan<BN>(all_tiles, st->most_rows, k_blocks, n_units, lane);
     volatile int* abort = &st->abort;
 
     if (warp >= 8) {
@@ -595,8 +612,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 sa0 = args.a_scale + (int64_t)min(it.row0 + r0, args.R - 1) * k_blocks;
                 sa1 = args.a_scale + (int64_t)min(it.row0 + r0 + 32, args.R - 1) * k_blocks;
                 // gated: the slice's block of W1 and of W3; product: each half's block
-                const int64_t b0 = (int64_t)it.g * n_blocks + (GATED ? it.n_tile : 2 * it.n_tile);
-                const int64_t b1 = GATED || 2 * it.n_tile + 1 == n_blocks ? b0 : b0 + 1;
+                const int64_t b0 = (int64_t)it.g * n_blocks + (GATED || BN == 128 ? it.n_tile : 2 * it.n_tile);
+                const int64_t b1 = GATED || BN == 128 || 2 * it.n_tile + 1 == n_blocks ? b0 : b0 + 1;
                 sw0 = args.w0_scale + b0 * k_blocks;
                 sw1 = (GATED ? args.w1_scale : args.w0_scale) + b1 * k_blocks;
             };
@@ -637,9 +654,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     } else {
         setmaxnreg_inc<FOLD_REGS>();
         // ========================= fold and epilogue ==========================
-        const int half = warp >> 2;                  // MMA columns 128 half .. + 127
+        const int half = warp >> 2;                  // MMA columns HALF half .. + HALF - 1
         const int r = (warp & 3) * 32 + lane;        // row of the tile = TMEM lane
-        const uint32_t t_row = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + half * 128;
+        const uint32_t t_row = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + half * HALF;
         int stage = 0;
         int buf = 0;
         uint32_t buf_phase = 0;
@@ -650,9 +667,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         Walk walk(plan, unit, n_units, k_blocks);
         int n = 0;
         for (Piece pc; walk.next(pc); ++n) {
-            float acc[128];
+            float acc[HALF];
 #pragma unroll
-            for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
+            for (int i = 0; i < HALF; ++i) acc[i] = 0.0f;
             for (int kb = pc.kb0; kb < pc.kb1 && ok; ++kb) {
                 ok = __all_sync(0xffffffffu, ready || mbar_wait(smem_u32(&st->tfull[buf]), buf_phase, abort, args.err));
                 if (!ok) break;
@@ -669,12 +686,14 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 tmem_ld_32x32b_x32(t + 32, v);
                 tc_wait_ld_for(u);
                 tc_wait_ld_for(v);
-                fold32<0>(acc, u, c0);
-                tmem_ld_32x32b_x32(t + 64, u);
-                fold32<32>(acc, v, c0);
-                tmem_ld_32x32b_x32(t + 96, v);
-                tc_wait_ld_for(u);
-                tc_wait_ld_for(v);
+                if constexpr (HALF == 128) {
+                    fold32<0>(acc, u, c0);
+                    tmem_ld_32x32b_x32(t + 64, u);
+                    fold32<32>(acc, v, c0);
+                    tmem_ld_32x32b_x32(t + 96, v);
+                    tc_wait_ld_for(u);
+                    tc_wait_ld_for(v);
+                }
                 // TMEM is read: the tensor cores may fill this buffer again
                 tc_fence_before();
                 __syncwarp();
@@ -686,8 +705,13 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
                 // whether the next block is there, asked before this one's last sums
                 ready = mbar_test(smem_u32(&st->tfull[buf]), buf_phase);
-                fold32<64>(acc, u, c1);
-                fold32<96>(acc, v, c1);
+                if constexpr (HALF == 128) {
+                    fold32<64>(acc, u, c1);
+                    fold32<96>(acc, v, c1);
+                } else {
+                    fold32<0>(acc, u, c0);
+                    fold32<32>(acc, v, c0);
+                }
             }
 
             const int n_blocks = (args.N + kFp8Block - 1) / kFp8Block;
@@ -697,10 +721,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             if (pc.kb1 - pc.kb0 < k_blocks) {
                 // publish this piece's part (its rows side by side) and take a ticket;
                 // the last piece of the tile joins the parts
-                float* part = args.part + ((int64_t)(2 * unit + (pc.kb0 == 0)) * plan.part_rows + r) * BN + half * 128;
+                float* part = args.part + ((int64_t)(2 * unit + (pc.kb0 == 0)) * plan.part_rows + r) * BN + half * HALF;
                 if (ok && valid) {
 #pragma unroll
-                    for (int c = 0; c < 128; c += 8)
+                    for (int c = 0; c < HALF; c += 8)
                         st_global_v8(part + c, __float_as_uint(acc[c]), __float_as_uint(acc[c + 1]),
                                      __float_as_uint(acc[c + 2]), __float_as_uint(acc[c + 3]),
                                      __float_as_uint(acc[c + 4]), __float_as_uint(acc[c + 5]),
@@ -722,7 +746,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 }
                 fold_barrier();
                 if (st->last)
-                    join<GATED, OUT>(args, it, first, parts, plan.part_rows * BN, n_blocks, warp, lane);
+                    join<GATED, OUT, BN>(args, it, first, parts, plan.part_rows * BN, n_blocks, warp, lane);
                 continue;
             }
 
@@ -762,7 +786,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 store_rows(st->stage_out[warp], lane, o, out, (lane & 3) * 16, n0 + (lane & 3) * 16 < args.N);
                 if (valid && ok && half == 0) args.out_scale[(int64_t)p * n_blocks + it.n_tile] = scale;
             } else {
-                const int n0 = it.n_tile * BN + half * 128;
+                const int n0 = it.n_tile * BN + half * HALF;
                 int64_t row = 0;
                 float wt = 1.0f;
                 const bool mine = ok && valid && row_target(args, p, row, wt);
@@ -779,7 +803,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 constexpr int COLS = 64 / (int)sizeof(OUT);   // columns of a row at once
                 constexpr int PIECE = 16 / (int)sizeof(OUT);  // and of a 16-byte piece
 #pragma unroll
-                for (int c = 0; c < 128; c += COLS) {
+                for (int c = 0; c < HALF; c += COLS) {
                     uint4 o[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -810,7 +834,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     }
     if (warp == 9) {
         tc_fence_after();
-        tmem_dealloc<CG>(tmem_base, TMEM_COLS);
+        tmem_dealloc<CG>(tmem_base, C::TMEM_COLS);
     }
 }
 
@@ -839,10 +863,10 @@ template <bool GATED, typename OUT>
 cudaError_t launch_pair(int slot, const CUtensorMap& tmA, const CUtensorMap& tmB0, const CUtensorMap& tmB1,
                         const Fp8GemmArgs& a, int num_sms, cudaStream_t s)
 {
-    auto kern = fp8_gemm_kernel<GATED, OUT, true>;
+    auto kern = fp8_gemm_kernel<GATED, OUT, true, 256>;
     static std::atomic<uint64_t> done{0};
     int dev = 0;
-    cudaError_t e = allow_smem(kern, smem_bytes<true>(), done, dev);
+    cudaError_t e = allow_smem(kern, smem_bytes<true, 256>(), done, dev);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -853,7 +877,7 @@ cudaError_t launch_pair(int slot, const CUtensorMap& tmA, const CUtensorMap& tmB
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(NUM_THREADS);
-    cfg.dynamicSmemBytes = smem_bytes<true>();
+    cfg.dynamicSmemBytes = smem_bytes<true, 256>();
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -874,12 +898,12 @@ cudaError_t launch_pair(int slot, const CUtensorMap& tmA, const CUtensorMap& tmB
     return e;
 }
 
-template <bool GATED, typename OUT>
+template <bool GATED, typename OUT, int BN>
 cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB0, const CUtensorMap& tmB1, const Fp8GemmArgs& a,
                    int num_sms, cudaStream_t s)
 {
-    auto kern = fp8_gemm_kernel<GATED, OUT, false>;
-    constexpr size_t smem = smem_bytes<false>();
+    auto kern = fp8_gemm_kernel<GATED, OUT, false, BN>;
+    constexpr size_t smem = smem_bytes<false, BN>();
     static std::atomic<uint64_t> done{0};
     int dev = 0;
     const cudaError_t e = allow_smem(kern, smem, done, dev);
@@ -887,23 +911,29 @@ cudaError_t launch(const CUtensorMap& tmA, const CUtensorMap& tmB0, const CUtens
     return launch_pdl(kern, dim3(num_sms), dim3(NUM_THREADS), smem, s, tmA, tmB0, tmB1, a);
 }
 
+template <typename OUT>
+cudaError_t launch_product(Fp8GemmForm form, int slot, const CUtensorMap& tmA, const CUtensorMap& tmB,
+                           const Fp8GemmArgs& a, int num_sms, cudaStream_t s)
+{
+    if (form == kFp8Pair) return launch_pair<false, OUT>(slot, tmA, tmB, tmB, a, num_sms, s);
+    if (form == kFp8Narrow) return launch<false, OUT, 128>(tmA, tmB, tmB, a, num_sms, s);
+    return launch<false, OUT, 256>(tmA, tmB, tmB, a, num_sms, s);
+}
+
 }  // namespace
 
-cudaError_t launch_fp8_gemm(Fp8GemmMode mode, bool pair, const CUtensorMap& tmA, const CUtensorMap& tmB0,
+cudaError_t launch_fp8_gemm(Fp8GemmMode mode, Fp8GemmForm form, const CUtensorMap& tmA, const CUtensorMap& tmB0,
                             const CUtensorMap& tmB1, const Fp8GemmArgs& a, int num_sms, cudaStream_t s)
 {
     if (a.R == 0) return cudaSuccess;
     if (a.R < 0 || a.G < 1 || a.G > MAX_GROUPS || (!a.offsets && a.G != 1)) return cudaErrorInvalidValue;
     switch (mode) {
     case kFp8Gated:
-        return pair ? launch_pair<true, uint8_t>(0, tmA, tmB0, tmB1, a, num_sms, s)
-                    : launch<true, uint8_t>(tmA, tmB0, tmB1, a, num_sms, s);
-    case kFp8ProductBf16:
-        return pair ? launch_pair<false, __nv_bfloat16>(1, tmA, tmB0, tmB1, a, num_sms, s)
-                    : launch<false, __nv_bfloat16>(tmA, tmB0, tmB1, a, num_sms, s);
-    case kFp8ProductF32:
-        return pair ? launch_pair<false, float>(2, tmA, tmB0, tmB1, a, num_sms, s)
-                    : launch<false, float>(tmA, tmB0, tmB1, a, num_sms, s);
+        if (form == kFp8Narrow) return cudaErrorInvalidValue;
+        return form == kFp8Pair ? launch_pair<true, uint8_t>(0, tmA, tmB0, tmB1, a, num_sms, s)
+                                : launch<true, uint8_t, 256>(tmA, tmB0, tmB1, a, num_sms, s);
+    case kFp8ProductBf16: return launch_product<__nv_bfloat16>(form, 1, tmA, tmB0, a, num_sms, s);
+    case kFp8ProductF32: return launch_product<float>(form, 2, tmA, tmB0, a, num_sms, s);
     }
     return cudaErrorInvalidValue;
 }
