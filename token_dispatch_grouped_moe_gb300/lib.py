@@ -616,21 +616,26 @@ class MoEFp8Layer:
         self.Fs = 0 if W1s is None else W1s.shape[1]
         self.routed = Fp8Weights.from_bf16(W1, W3, W2)
         self.shared = None if W1s is None else Fp8Weights.from_bf16(W1s[None], W3s[None], W2s[None])
-        self._ws = None
-        self._T = None
+        self._ws = {}
 
     def dims(self, T) -> Dims:
         return make_dims(T, self.H, self.F, self.E, self.k, self.Fs)
 
-    def workspace(self, T):
-        if self._ws is None or self._T != T:
-            self._ws = fp8_workspace(self.dims(T), device=self.Wg.device)
-            self._T = T
-        return self._ws
+    def workspace(self, T, stream=None):
+        """The workspace of calls of T rows on ``stream`` (the current one). It is
+        made and zeroed on that stream, before the work that uses it, and goes
+        back to that stream's memory behind it."""
+        s = torch.cuda.current_stream(self.Wg.device) if stream is None else stream
+        rows, ws = self._ws.get(s.cuda_stream, (None, None))
+        if rows != T:
+            with torch.cuda.stream(s):
+                ws = fp8_workspace(self.dims(T), device=self.Wg.device)
+            self._ws[s.cuda_stream] = (T, ws)
+        return ws
 
     def forward(self, x, residual=None, routing=None, stream=None):
         T = x.shape[0]
         r, y, q, scale = add_rmsnorm_fp8(x, self.norm_weight, residual=residual, eps=self.eps, stream=stream)
-        out = fp8_layer_forward(self.dims(T), y, q, scale, self.Wg, self.routed, self.workspace(T), bias=self.bias,
-                                shared=self.shared, routing=routing, stream=stream)
+        out = fp8_layer_forward(self.dims(T), y, q, scale, self.Wg, self.routed, self.workspace(T, stream),
+                                bias=self.bias, shared=self.shared, routing=routing, stream=stream)
         return out, x if residual is None else r
