@@ -1,4 +1,4 @@
-"""Whose memory the 8-bit calls use: the stream, the graph and the device that a
+"""Whose memory the layer objects and the 8-bit calls use: the stream, the graph and the device that a
 call runs on, checked on the host with stand-ins for PyTorch's streams, and on
 the GPU with a current stream that is busy."""
 import contextlib
@@ -91,6 +91,21 @@ def test_fp8_layer_workspace_is_made_on_the_calls_stream(lib, monkeypatch, strea
     assert made == [2, 1, 2]
 
 
+def test_bf16_layer_workspace_is_made_on_the_calls_stream(lib, monkeypatch, streams):
+    made = record_workspaces(lib, monkeypatch, streams, "workspace")
+    layer, w, k = host_layer(lib.MoELayer)
+    layer.__init__(w["Wg"], w["W1"], w["W3"], w["W2"], k)
+    used = []
+    monkeypatch.setattr(lib, "layer_forward", lambda dims, x, Wg, W1, W3, W2, ws, *a, **kw: used.append(ws))
+    x, side = torch.zeros(4, 64), fake_stream(2)
+    layer.forward(x, stream=side)
+    layer.forward(x)
+    layer.forward(x, stream=side)
+    assert made == [2, 1] and used[0] is used[2] and used[1] is not used[0]
+    layer.forward(torch.zeros(9, 64), stream=side)
+    assert made == [2, 1, 2]
+
+
 # ------------------------------------------------------------------ on the GPU
 
 def gen(seed):
@@ -135,4 +150,25 @@ def test_fp8_layer_on_a_side_stream_while_the_current_one_is_busy(lib):
             assert torch.equal(got, w)   # before the current stream's fills
         torch.cuda.synchronize()
         assert torch.equal(got, w)       # and behind them
+        assert lib.check(layer.workspace(x.shape[0], side)) == lib.MOE_OK
+
+
+@gpu
+def test_bf16_layer_on_a_side_stream_while_the_current_one_is_busy(lib):
+    g = gen(2)
+    H, F, E, k = 512, 256, 8, 2
+    Wg, W1, W3, W2 = weights(g, H, F, E)
+    calls = [torch.randn(T, H, generator=g, device="cuda").bfloat16() for T in (1, 37, 5, 300)]
+    want = [lib.MoELayer(Wg, W1, W3, W2, k).forward(x) for x in calls]
+    layer = lib.MoELayer(Wg, W1, W3, W2, k)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for x, w in zip(calls, want):
+        out = torch.empty_like(w)
+        late_fill([lib.workspace_size(layer.dims(x.shape[0]))], 0xFF)
+        layer.forward(x, out=out, stream=side)
+        with torch.cuda.stream(side):
+            assert torch.equal(out, w)
+        torch.cuda.synchronize()
+        assert torch.equal(out, w)
         assert lib.check(layer.workspace(x.shape[0], side)) == lib.MOE_OK

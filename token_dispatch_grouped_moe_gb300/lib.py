@@ -418,7 +418,26 @@ def host_chunks(dims: Dims) -> int:
     return int(load().moe_host_chunks(ctypes.byref(dims)))
 
 
-class MoELayer:
+class _Layer:
+    """What the layer objects share: their sizes and a workspace for each stream."""
+
+    def dims(self, T) -> Dims:
+        return make_dims(T, self.H, self.F, self.E, self.k, self.Fs)
+
+    def workspace(self, T, stream=None):
+        """The workspace of calls of T rows on ``stream`` (the current one). It is
+        made and zeroed on that stream, before the work that uses it, and goes
+        back to that stream's memory behind it."""
+        s = torch.cuda.current_stream(self.Wg.device) if stream is None else stream
+        rows, ws = self._ws.get(s.cuda_stream, (None, None))
+        if rows != T:
+            with torch.cuda.stream(s):
+                ws = self._new_workspace(self.dims(T))
+            self._ws[s.cuda_stream] = (T, ws)
+        return ws
+
+
+class MoELayer(_Layer):
     """Weights and a workspace on one device; ``forward(x)`` runs the layer."""
 
     def __init__(self, Wg, W1, W3, W2, k, bias=None, W1s=None, W3s=None, W2s=None):
@@ -427,21 +446,14 @@ class MoELayer:
         self.H, self.E = Wg.shape
         self.F = W1.shape[2]
         self.Fs = 0 if W1s is None else W1s.shape[1]
-        self._ws = None
-        self._T = None
+        self._ws = {}
 
-    def dims(self, T) -> Dims:
-        return make_dims(T, self.H, self.F, self.E, self.k, self.Fs)
-
-    def workspace(self, T):
-        if self._ws is None or self._T != T:
-            self._ws = workspace(self.dims(T), device=self.Wg.device)
-            self._T = T
-        return self._ws
+    def _new_workspace(self, dims):
+        return workspace(dims, device=self.Wg.device)
 
     def forward(self, x, out=None, routing=None, events=None, stream=None):
         T = x.shape[0]
-        return layer_forward(self.dims(T), x, self.Wg, self.W1, self.W3, self.W2, self.workspace(T),
+        return layer_forward(self.dims(T), x, self.Wg, self.W1, self.W3, self.W2, self.workspace(T, stream),
                              self.bias, self.W1s, self.W3s, self.W2s, out=out, routing=routing,
                              events=events, stream=stream)
 
@@ -603,7 +615,7 @@ def fp8_layer_forward(dims: Dims, x, xq, xq_scale, Wg, routed: Fp8Weights, ws, b
     return out
 
 
-class MoEFp8Layer:
+class MoEFp8Layer(_Layer):
     """A pre-norm expert layer of a residual stream, served in 8 bits: the
     residual's addition, the norm and its quantization, then the layer on
     weights quantized once from bf16. ``forward(x, residual)`` returns (the
@@ -618,20 +630,8 @@ class MoEFp8Layer:
         self.shared = None if W1s is None else Fp8Weights.from_bf16(W1s[None], W3s[None], W2s[None])
         self._ws = {}
 
-    def dims(self, T) -> Dims:
-        return make_dims(T, self.H, self.F, self.E, self.k, self.Fs)
-
-    def workspace(self, T, stream=None):
-        """The workspace of calls of T rows on ``stream`` (the current one). It is
-        made and zeroed on that stream, before the work that uses it, and goes
-        back to that stream's memory behind it."""
-        s = torch.cuda.current_stream(self.Wg.device) if stream is None else stream
-        rows, ws = self._ws.get(s.cuda_stream, (None, None))
-        if rows != T:
-            with torch.cuda.stream(s):
-                ws = fp8_workspace(self.dims(T), device=self.Wg.device)
-            self._ws[s.cuda_stream] = (T, ws)
-        return ws
+    def _new_workspace(self, dims):
+        return fp8_workspace(dims, device=self.Wg.device)
 
     def forward(self, x, residual=None, routing=None, stream=None):
         T = x.shape[0]
