@@ -456,10 +456,13 @@ int32_t moe_host_chunks(const moe_dims* dims);
  * Conventions are those of the other entry points. The workspace `ws` of the
  * products (moe_fp8_workspace_size(NULL) bytes, for any sizes) and of
  * moe_fp8_layer_forward (moe_fp8_workspace_size(dims)) must hold zeros in its
- * first moe_fp8_workspace_size(NULL) bytes before its first use, and again
- * after moe_check has returned MOE_ERR_TIMEOUT for it; the calls leave them as
- * the next call needs them. Two calls that share a workspace must not overlap.
+ * first MOE_FP8_WORKSPACE_ZEROS bytes (the error word and the tickets of cut
+ * tiles) before its first use, and again after moe_check has returned
+ * MOE_ERR_TIMEOUT for it; the calls leave them as the next call needs them, of
+ * these or any other sizes that the workspace is large enough for. The rest may
+ * hold anything. Two calls that share a workspace must not overlap.
  */
+#define MOE_FP8_WORKSPACE_ZEROS 2304
 
 /* Bytes of the 8-bit entry points' workspace: of the products for dims NULL,
  * else of moe_fp8_layer_forward (0 for invalid dims). */

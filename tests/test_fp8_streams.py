@@ -106,6 +106,47 @@ def test_bf16_layer_workspace_is_made_on_the_calls_stream(lib, monkeypatch, stre
     assert made == [2, 1, 2]
 
 
+@pytest.mark.parametrize("bits", [8, 16])
+def test_layer_workspace_grows_only(lib, monkeypatch, streams, bits):
+    """Batches of changing length keep one workspace, large enough for each."""
+    made = record_workspaces(lib, monkeypatch, streams, "fp8_workspace" if bits == 8 else "workspace")
+    if bits == 8:
+        layer = fp8_host_layer(lib, monkeypatch)
+    else:
+        layer, w, k = host_layer(lib.MoELayer)
+        layer.__init__(w["Wg"], w["W1"], w["W3"], w["W2"], k)
+    first = layer.workspace(100)
+    assert all(layer.workspace(T) is first for T in (1, 64, 100, 0, 7)) and len(made) == 1
+    # row by row: a few workspaces, not one for each length
+    for T in range(101, 1000):
+        layer.workspace(T)
+    assert len(made) <= 12
+
+
+@pytest.mark.parametrize("H,F,E,k,Fs", [(64, 64, 8, 2, 0), (2048, 1408, 64, 6, 2816), (4096, 14336, 8, 2, 0),
+                                        (512, 64, 256, 8, 0), (1024, 512, 128, 8, 64)])
+def test_workspace_sizes_grow_with_the_rows(lib, H, F, E, k, Fs):
+    """A workspace of more rows is large enough for fewer."""
+    rows = [0, 1, 2, 31, 127, 128, 129, 511, 512, 513, 1024, 4095, 4096, 4097, 8192, 32768, 100000]
+    for size in (lib.fp8_workspace_size, lib.workspace_size):
+        sizes = [size(lib.make_dims(T, H, F, E, k, Fs)) for T in rows]
+        assert sizes == sorted(sizes) and sizes[0] > 0
+
+
+def test_fp8_workspace_zeroes_its_head_only(lib, monkeypatch):
+    """The zeros that the calls ask for, not tens of megabytes or gigabytes of them."""
+    import re
+    header = open(__file__.replace("tests/test_fp8_streams.py", "include/moe.h")).read()
+    zeros = int(re.search(r"#define MOE_FP8_WORKSPACE_ZEROS (\d+)", header).group(1))
+    assert lib.FP8_WORKSPACE_ZEROS == zeros <= 4096
+    real = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: real(*a, **kw).fill_(0xA5))
+    for dims in (None, lib.make_dims(5, 64, 64, 8, 2)):
+        ws = lib.fp8_workspace(dims, device="cpu")
+        assert ws.numel() == lib.fp8_workspace_size(dims)
+        assert not ws[:zeros].any() and bool((ws[zeros:] == 0xA5).all())
+
+
 # ------------------------------------------------------------------ on the GPU
 
 def gen(seed):
@@ -172,3 +213,27 @@ def test_bf16_layer_on_a_side_stream_while_the_current_one_is_busy(lib):
         torch.cuda.synchronize()
         assert torch.equal(out, w)
         assert lib.check(layer.workspace(x.shape[0], side)) == lib.MOE_OK
+
+
+@gpu
+def test_fp8_workspace_needs_no_zeros_but_its_heads(lib):
+    """Products with cut tiles and the layer, on a workspace of NaN bits behind
+    its head, first for many rows and then for few."""
+    g = gen(3)
+    H, F, E, k = 1024, 512, 8, 2
+    Wg, W1, W3, W2 = weights(g, H, F, E)
+    layer = lib.MoEFp8Layer(None, Wg, W1, W3, W2, k)
+    ws = lib.fp8_workspace(layer.dims(700))
+    ws[lib.FP8_WORKSPACE_ZEROS:] = 0xFF
+    for T in (700, 1, 130):
+        x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+        _, y, q, s = lib.add_rmsnorm_fp8(x)
+        got = lib.fp8_layer_forward(layer.dims(T), y, q, s, Wg, layer.routed, ws)
+        clean = torch.zeros(lib.fp8_workspace_size(layer.dims(T)), dtype=torch.uint8, device="cuda")
+        want = lib.fp8_layer_forward(layer.dims(T), y, q, s, Wg, layer.routed, clean)
+        assert torch.equal(got, want) and bool(got.isfinite().all())
+        w, w_scale = layer.routed.w2[:1], layer.routed.w2_scale[:1]
+        a = q[:, :F].contiguous()
+        a_scale = s[:, : F // 128].contiguous()
+        assert torch.equal(lib.fp8_matmul(a, a_scale, w, w_scale, ws), lib.fp8_matmul(a, a_scale, w, w_scale, clean))
+        assert lib.check(ws) == lib.MOE_OK and lib.check(clean) == lib.MOE_OK

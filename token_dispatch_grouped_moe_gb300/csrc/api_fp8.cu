@@ -14,6 +14,7 @@ namespace moe {
 namespace {
 
 constexpr int32_t kNormMaxH = 32768;
+static_assert(kFp8PartOffset == MOE_FP8_WORKSPACE_ZEROS, "what has to be zero lies before the parts");
 
 size_t blocks_of(int32_t n) { return ((size_t)n + kFp8Block - 1) / kFp8Block; }
 

@@ -425,15 +425,17 @@ class _Layer:
         return make_dims(T, self.H, self.F, self.E, self.k, self.Fs)
 
     def workspace(self, T, stream=None):
-        """The workspace of calls of T rows on ``stream`` (the current one). It is
-        made and zeroed on that stream, before the work that uses it, and goes
-        back to that stream's memory behind it."""
+        """A workspace for calls of up to T rows, or more, on ``stream`` (the current
+        one). It is made on that stream, before the work that uses it, and goes
+        back to that stream's memory behind it. It grows by a quarter at least, so
+        a batch that gets longer row by row does not make a new one every time."""
         s = torch.cuda.current_stream(self.Wg.device) if stream is None else stream
-        rows, ws = self._ws.get(s.cuda_stream, (None, None))
-        if rows != T:
+        rows, ws = self._ws.get(s.cuda_stream, (-1, None))
+        if rows < T:
+            rows = max(T, rows + rows // 4)
             with torch.cuda.stream(s):
-                ws = self._new_workspace(self.dims(T))
-            self._ws[s.cuda_stream] = (T, ws)
+                ws = self._new_workspace(self.dims(rows))
+            self._ws[s.cuda_stream] = (rows, ws)
         return ws
 
 
@@ -462,6 +464,7 @@ class MoELayer(_Layer):
 
 FP8 = torch.float8_e4m3fn
 FP8_BLOCK = 128   # values that share one scale
+FP8_WORKSPACE_ZEROS = 2304   # bytes of a workspace that have to be zero before its first use
 
 
 def _fp8_blocks(n: int) -> int:
@@ -501,12 +504,15 @@ def fp8_workspace_size(dims: Dims | None = None) -> int:
 
 
 def fp8_workspace(dims: Dims | None = None, device=None) -> torch.Tensor:
-    """A zeroed workspace of :func:`fp8_matmul` and :func:`fp8_gated` (any
-    sizes), or of :func:`fp8_layer_forward` for ``dims``."""
+    """A workspace of :func:`fp8_matmul` and :func:`fp8_gated` (any sizes), or of
+    :func:`fp8_layer_forward` for ``dims`` (or fewer rows), zeros where the calls
+    need them."""
     n = fp8_workspace_size(dims)
     if n == 0:
         raise MoeError(1, "fp8_workspace_size")
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    ws[:FP8_WORKSPACE_ZEROS].zero_()
+    return ws
 
 
 def add_rmsnorm_fp8(x, weight=None, residual=None, eps=1e-6, want_y=True, sum_out=None, stream=None):
