@@ -38,6 +38,8 @@ def streams(monkeypatch):
         finally:
             state.stack.pop()
 
+    state.captured = set()   # handles of streams that are being captured
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state.now() in state.captured)
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: state.stack[-1])
     return state
@@ -121,6 +123,28 @@ def test_layer_workspace_grows_only(lib, monkeypatch, streams, bits):
     for T in range(101, 1000):
         layer.workspace(T)
     assert len(made) <= 12
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+def test_layer_workspace_of_a_graph_is_the_graphs(lib, monkeypatch, streams, bits):
+    """A captured call neither takes the workspace that is kept for eager calls
+    (which is given back once a longer batch has outgrown it, under the graph's
+    feet) nor leaves its own for them (whose zeroing runs with the graph only)."""
+    made = record_workspaces(lib, monkeypatch, streams, "fp8_workspace" if bits == 8 else "workspace")
+    if bits == 8:
+        layer = fp8_host_layer(lib, monkeypatch)
+    else:
+        layer, w, k = host_layer(lib.MoELayer)
+        layer.__init__(w["Wg"], w["W1"], w["W3"], w["W2"], k)
+    side = fake_stream(2)
+    eager = layer.workspace(8, side)
+    streams.captured.add(2)
+    first, second = layer.workspace(8, side), layer.workspace(8, side)
+    assert first is not eager and second is not eager and first is not second and made == [2, 2, 2]
+    longer = layer.workspace(16, side)
+    streams.captured.clear()
+    assert layer.workspace(8, side) is eager
+    assert layer.workspace(16, side) is not longer
 
 
 @pytest.mark.parametrize("H,F,E,k,Fs", [(64, 64, 8, 2, 0), (2048, 1408, 64, 6, 2816), (4096, 14336, 8, 2, 0),
@@ -237,3 +261,53 @@ def test_fp8_workspace_needs_no_zeros_but_its_heads(lib):
         a_scale = s[:, : F // 128].contiguous()
         assert torch.equal(lib.fp8_matmul(a, a_scale, w, w_scale, ws), lib.fp8_matmul(a, a_scale, w, w_scale, clean))
         assert lib.check(ws) == lib.MOE_OK and lib.check(clean) == lib.MOE_OK
+
+
+@gpu
+@pytest.mark.parametrize("bits", [8, 16])
+def test_layer_graph_outlives_the_workspaces_of_eager_calls(lib, bits):
+    """Captured after a warm-up, as usual; then eager calls of longer batches
+    outgrow the warm-up's workspace and its memory goes elsewhere; replayed."""
+    g = gen(4)
+    H, F, E, k = 512, 256, 8, 2
+    Wg, W1, W3, W2 = weights(g, H, F, E)
+    x = torch.randn(4, H, generator=g, device="cuda").bfloat16()
+    long = torch.randn(900, H, generator=g, device="cuda").bfloat16()
+    layer = lib.MoEFp8Layer(None, Wg, W1, W3, W2, k) if bits == 8 else lib.MoELayer(Wg, W1, W3, W2, k)
+    call = (lambda v: layer.forward(v)[0]) if bits == 8 else layer.forward
+    want, want_long = call(x), call(long)
+    layer._ws.clear()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = call(x)
+    with torch.cuda.stream(side):
+        assert torch.equal(call(long), want_long)   # before any replay
+        busy = [torch.full((1 << 22,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(32)]
+    torch.cuda.synchronize()
+    for _ in range(2):
+        got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    assert len(busy) == 32
+
+
+@gpu
+@pytest.mark.parametrize("T,H,F,E,k,Fs", [(1, 512, 256, 8, 2, 0), (300, 512, 256, 8, 2, 128), (5000, 512, 128, 64, 6, 0),
+                                          (700, 512, 4096, 8, 2, 0), (4500, 1024, 256, 16, 4, 0)])
+def test_bf16_workspace_needs_no_zeros_but_its_error_word(lib, T, H, F, E, k, Fs):
+    g = gen(5)
+    Wg, W1, W3, W2 = weights(g, H, F, E)
+    shared = [None] * 3 if not Fs else [t[0] for t in weights(g, H, Fs, 1)[1:]]
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    dims = lib.make_dims(T, H, F, E, k, Fs)
+    clean = torch.zeros(lib.workspace_size(dims), dtype=torch.uint8, device="cuda")
+    dirty = clean.clone()
+    dirty[256:] = 0xFF
+    want, got = (lib.layer_forward(dims, x, Wg, W1, W3, W2, ws, None, *shared) for ws in (clean, dirty))
+    assert torch.equal(got, want) and lib.check(clean) == lib.MOE_OK and lib.check(dirty) == lib.MOE_OK

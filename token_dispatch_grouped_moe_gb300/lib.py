@@ -277,11 +277,17 @@ def workspace_size(dims: Dims) -> int:
 
 
 def workspace(dims: Dims, device=None) -> torch.Tensor:
-    """A zeroed workspace (uint8) for ``dims``; the zeroed head is the error word."""
+    """A workspace (uint8) for ``dims``; its head, the error word, is zero."""
     n = workspace_size(dims)
     if n == 0:
         raise MoeError(1, "workspace_size")
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    return _zero_headed(n, 256, device)
+
+
+def _zero_headed(n: int, head: int, device) -> torch.Tensor:
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    ws[:head].zero_()
+    return ws
 
 
 def check(ws: torch.Tensor, stream=None) -> int:
@@ -428,14 +434,19 @@ class _Layer:
         """A workspace for calls of up to T rows, or more, on ``stream`` (the current
         one). It is made on that stream, before the work that uses it, and goes
         back to that stream's memory behind it. It grows by a quarter at least, so
-        a batch that gets longer row by row does not make a new one every time."""
+        a batch that gets longer row by row does not make a new one every time.
+        A stream that is captured gets a new one with each call, which belongs to
+        the graph: zeroed at every replay, and never given to anyone else while
+        the graph lives, as a workspace kept here is once it has been outgrown."""
         s = torch.cuda.current_stream(self.Wg.device) if stream is None else stream
         rows, ws = self._ws.get(s.cuda_stream, (-1, None))
-        if rows < T:
-            rows = max(T, rows + rows // 4)
-            with torch.cuda.stream(s):
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return self._new_workspace(self.dims(T))
+            if rows < T:
+                rows = max(T, rows + rows // 4)
                 ws = self._new_workspace(self.dims(rows))
-            self._ws[s.cuda_stream] = (rows, ws)
+                self._ws[s.cuda_stream] = (rows, ws)
         return ws
 
 
@@ -510,9 +521,7 @@ def fp8_workspace(dims: Dims | None = None, device=None) -> torch.Tensor:
     n = fp8_workspace_size(dims)
     if n == 0:
         raise MoeError(1, "fp8_workspace_size")
-    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
-    ws[:FP8_WORKSPACE_ZEROS].zero_()
-    return ws
+    return _zero_headed(n, FP8_WORKSPACE_ZEROS, device)
 
 
 def add_rmsnorm_fp8(x, weight=None, residual=None, eps=1e-6, want_y=True, sum_out=None, stream=None):
