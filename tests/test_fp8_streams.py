@@ -171,6 +171,45 @@ def test_fp8_workspace_zeroes_its_head_only(lib, monkeypatch):
         assert not ws[:zeros].any() and bool((ws[zeros:] == 0xA5).all())
 
 
+class FakeLibrary:
+    """Answers every call with MOE_OK and computes nothing."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+def record_allocations(monkeypatch, streams):
+    """The stream that each torch.empty was called on."""
+    taken, real = [], torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: (taken.append(streams.now()), real(*a, **kw))[1])
+    return taken
+
+
+def as_cuda(monkeypatch, lib):
+    """Lets host tensors pass for the device's in calls of the fake library."""
+    fake = FakeLibrary()
+    monkeypatch.setattr(lib, "load", lambda: fake)
+    return fake
+
+
+def test_quantized_weights_are_the_calls_streams_memory(lib, monkeypatch, streams):
+    as_cuda(monkeypatch, lib)
+    taken = record_allocations(monkeypatch, streams)
+    w = torch.zeros(2, 64, 64, dtype=torch.bfloat16)
+    lib.fp8_quantize_weight(w, stream=fake_stream(2))
+    assert taken == [2, 2]
+    lib.Fp8Weights.from_bf16(w, w, w, stream=fake_stream(3))
+    assert taken[2:] == [3] * 6
+    lib.fp8_quantize_weight(w)
+    assert taken[8:] == [1, 1]
+
+
 # ------------------------------------------------------------------ on the GPU
 
 def gen(seed):
@@ -311,3 +350,17 @@ def test_bf16_workspace_needs_no_zeros_but_its_error_word(lib, T, H, F, E, k, Fs
     dirty[256:] = 0xFF
     want, got = (lib.layer_forward(dims, x, Wg, W1, W3, W2, ws, None, *shared) for ws in (clean, dirty))
     assert torch.equal(got, want) and lib.check(clean) == lib.MOE_OK and lib.check(dirty) == lib.MOE_OK
+
+
+@gpu
+def test_quantized_weights_on_a_side_stream_while_the_current_one_is_busy(lib):
+    w = (torch.randn(3, 512, 256, generator=gen(6), device="cuda") * 0.02).bfloat16()
+    want, want_scale = lib.fp8_quantize_weight(w)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    late_fill([want.numel(), 4 * want_scale.numel()], 0xFF)
+    q, scale = lib.fp8_quantize_weight(w, stream=side)
+    with torch.cuda.stream(side):
+        assert torch.equal(q.view(torch.uint8), want.view(torch.uint8)) and torch.equal(scale, want_scale)
+    torch.cuda.synchronize()
+    assert torch.equal(q.view(torch.uint8), want.view(torch.uint8)) and torch.equal(scale, want_scale)

@@ -541,8 +541,9 @@ def fp8_quantize_weight(w, stream=None):
     a weight's layout for the 8-bit products, made once."""
     G, K, N = w.shape
     _expect(w, "w", (G, K, N), torch.bfloat16, w.device)
-    q = torch.empty(G, N, K, dtype=FP8, device=w.device)
-    scale = torch.empty(G, _fp8_blocks(N), _fp8_blocks(K), dtype=torch.float32, device=w.device)
+    with torch.cuda.stream(stream):   # the memory is the stream's that writes it
+        q = torch.empty(G, N, K, dtype=FP8, device=w.device)
+        scale = torch.empty(G, _fp8_blocks(N), _fp8_blocks(K), dtype=torch.float32, device=w.device)
     _ok(load().moe_fp8_quantize_weight(G, K, N, w.data_ptr(), q.data_ptr(), scale.data_ptr(),
                                        _stream(stream)), "moe_fp8_quantize_weight")
     return q, scale
