@@ -2,12 +2,15 @@
 call runs on, checked on the host with stand-ins for PyTorch's streams, and on
 the GPU with a current stream that is busy."""
 import contextlib
+import functools
 from types import SimpleNamespace
 
 import pytest
 import torch
+from torch._subclasses import FakeTensorMode
 
 gpu = pytest.mark.gpu
+pytestmark = pytest.mark.filterwarnings("ignore:Accessing the data pointer of FakeTensor")
 FP8 = torch.float8_e4m3fn
 
 
@@ -19,16 +22,18 @@ def lib():
     return L
 
 
-def fake_stream(handle):
-    return SimpleNamespace(cuda_stream=handle, device=torch.device("cpu"))
+def fake_stream(handle, device=0):
+    return SimpleNamespace(cuda_stream=handle, device=torch.device("cuda", device))
 
 
 @pytest.fixture
 def streams(monkeypatch):
-    """Stand-ins for PyTorch's current stream: ``now()`` is the handle of the
-    stream whose memory an allocation takes."""
+    """Stand-ins for PyTorch's streams and devices: ``now()`` is the handle of the
+    stream whose memory an allocation takes, and whose device a launch runs on.
+    Tensors are FakeTensors: they have a device and no memory."""
     state = SimpleNamespace(stack=[fake_stream(1)])
     state.now = lambda: state.stack[-1].cuda_stream
+    state.device = lambda: state.stack[-1].device.index
 
     @contextlib.contextmanager
     def on(s):
@@ -38,17 +43,25 @@ def streams(monkeypatch):
         finally:
             state.stack.pop()
 
+    def device_stream(device=None):
+        """The current stream of a device: 1 of device 0, 101 of device 1."""
+        index = state.device() if device is None else torch.device(device).index
+        return state.stack[-1] if index == state.device() else fake_stream(1 + 100 * index, index)
+
+    monkeypatch.setattr(torch.cuda, "device", lambda d: on(device_stream(d)))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: state.device())
     state.captured = set()   # handles of streams that are being captured
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state.now() in state.captured)
     monkeypatch.setattr(torch.cuda, "stream", on)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: state.stack[-1])
-    return state
+    monkeypatch.setattr(torch.cuda, "current_stream", device_stream)
+    with FakeTensorMode(allow_non_fake_inputs=True):
+        yield state
 
 
 def host_layer(cls, H=64, F=64, E=8, k=2):
     """A layer object without its weights' memory: its host logic alone."""
     layer = object.__new__(cls)
-    t = torch.zeros
+    t = functools.partial(torch.empty, device="cuda:0", dtype=torch.bfloat16)
     with_init = {"Wg": t(H, E), "W1": t(E, H, F), "W3": t(E, H, F), "W2": t(E, F, H)}
     return layer, with_init, k
 
@@ -172,14 +185,15 @@ def test_fp8_workspace_zeroes_its_head_only(lib, monkeypatch):
 
 
 class FakeLibrary:
-    """Answers every call with MOE_OK and computes nothing."""
+    """Answers every call with MOE_OK and computes nothing; keeps each call's
+    device and stream (its last argument)."""
 
-    def __init__(self):
-        self.calls = []
+    def __init__(self, streams):
+        self.streams, self.calls = streams, []
 
     def __getattr__(self, name):
         def call(*args):
-            self.calls.append((name, args))
+            self.calls.append((name, self.streams.device(), args[-1].value))
             return 0
         return call
 
@@ -191,23 +205,50 @@ def record_allocations(monkeypatch, streams):
     return taken
 
 
-def as_cuda(monkeypatch, lib):
-    """Lets host tensors pass for the device's in calls of the fake library."""
-    fake = FakeLibrary()
-    monkeypatch.setattr(lib, "load", lambda: fake)
-    return fake
-
-
 def test_quantized_weights_are_the_calls_streams_memory(lib, monkeypatch, streams):
-    as_cuda(monkeypatch, lib)
+    monkeypatch.setattr(lib, "load", lambda: FakeLibrary(streams))
+    w = torch.empty(2, 64, 64, dtype=torch.bfloat16, device="cuda:0")
     taken = record_allocations(monkeypatch, streams)
-    w = torch.zeros(2, 64, 64, dtype=torch.bfloat16)
     lib.fp8_quantize_weight(w, stream=fake_stream(2))
     assert taken == [2, 2]
     lib.Fp8Weights.from_bf16(w, w, w, stream=fake_stream(3))
     assert taken[2:] == [3] * 6
     lib.fp8_quantize_weight(w)
     assert taken[8:] == [1, 1]
+
+
+def fake_fp8_layer_call(lib, device, T=4, H=64, F=64, E=8, **kw):
+    t = functools.partial(torch.empty, device=device)
+    f = torch.float32
+    w = lib.Fp8Weights(t(E, F, H, dtype=FP8), t(E, 1, 1, dtype=f), t(E, F, H, dtype=FP8), t(E, 1, 1, dtype=f),
+                       t(E, H, F, dtype=FP8), t(E, 1, 1, dtype=f))
+    args = dict(x=t(T, H, dtype=torch.bfloat16), xq=t(T, H, dtype=FP8), xq_scale=t(T, 1, dtype=f),
+                Wg=t(H, E, dtype=torch.bfloat16), routed=w, ws=t(1 << 20, dtype=torch.uint8))
+    return lib.fp8_layer_forward(lib.make_dims(T, H, F, E, 2), **{**args, **kw})
+
+
+def test_calls_run_on_their_tensors_device(lib, monkeypatch, streams):
+    """Tensors of device 1 while device 0 is the current one."""
+    fake = FakeLibrary(streams)
+    monkeypatch.setattr(lib, "load", lambda: fake)
+    w = torch.empty(2, 64, 64, dtype=torch.bfloat16, device="cuda:1")
+    lib.fp8_quantize_weight(w)
+    lib.fp8_quantize_weight(w, stream=fake_stream(7, 1))
+    fake_fp8_layer_call(lib, "cuda:1")
+    fake_fp8_layer_call(lib, "cuda:1", stream=fake_stream(7, 1))
+    assert [c[1:] for c in fake.calls] == [(1, 101), (1, 7), (1, 101), (1, 7)]
+    fake_fp8_layer_call(lib, "cuda:0")
+    assert fake.calls[-1][1:] == (0, 1) and streams.device() == 0
+    # the memory that lib.check looks at
+    lib.check(torch.empty(256, dtype=torch.uint8, device="cuda:1"))
+    assert fake.calls[-1][1:] == (1, 101)
+    # a stream of one device cannot order work on another's tensors
+    q, scale = torch.empty(4, 64, dtype=FP8, device="cuda:1"), torch.empty(4, 1, device="cuda:1")
+    for call in (lambda **kw: lib.fp8_quantize_weight(w, **kw), lambda **kw: fake_fp8_layer_call(lib, "cuda:1", **kw),
+                 lambda **kw: lib.add_rmsnorm_fp8(w[0], **kw), lambda **kw: lib.fp8_matmul(q, scale, q, scale, q, **kw),
+                 lambda **kw: lib.fp8_gated(q, scale, q, scale, q, scale, q, **kw)):
+        with pytest.raises(ValueError, match="stream"):
+            call(stream=fake_stream(7, 0))
 
 
 # ------------------------------------------------------------------ on the GPU

@@ -7,6 +7,7 @@ library has not been built, :func:`load` raises: there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -177,6 +178,20 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on(device, stream):
+    """The context of a call: its tensors' device, and the stream given or that
+    device's current one. What is allocated within is memory of that stream."""
+    if device.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got tensors on {device}")
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream: of {stream.device}, but the tensors are on {device}")
+        return torch.cuda.stream(stream)
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
 def _ok(status: int, what: str):
     if status != MOE_OK:
         raise MoeError(status, what)
@@ -292,7 +307,8 @@ def _zero_headed(n: int, head: int, device) -> torch.Tensor:
 
 def check(ws: torch.Tensor, stream=None) -> int:
     """Synchronise and return (and clear) the device error status in ``ws``."""
-    return int(load().moe_check(_p(ws), _stream(stream)))
+    with _on(ws.device, stream):
+        return int(load().moe_check(_p(ws), _stream()))
 
 
 def _gating(renormalize=True, shared_gate=None):
@@ -438,15 +454,15 @@ class _Layer:
         A stream that is captured gets a new one with each call, which belongs to
         the graph: zeroed at every replay, and never given to anyone else while
         the graph lives, as a workspace kept here is once it has been outgrown."""
-        s = torch.cuda.current_stream(self.Wg.device) if stream is None else stream
-        rows, ws = self._ws.get(s.cuda_stream, (-1, None))
-        with torch.cuda.stream(stream):
+        with _on(self.Wg.device, stream):
             if torch.cuda.is_current_stream_capturing():
                 return self._new_workspace(self.dims(T))
+            key = torch.cuda.current_stream().cuda_stream
+            rows, ws = self._ws.get(key, (-1, None))
             if rows < T:
                 rows = max(T, rows + rows // 4)
                 ws = self._new_workspace(self.dims(rows))
-                self._ws[s.cuda_stream] = (rows, ws)
+                self._ws[key] = (rows, ws)
         return ws
 
 
@@ -506,8 +522,12 @@ def _load_binding():
     return module
 
 
-def _handle(stream):
-    return None if stream is None else stream.cuda_stream
+def _handle(stream, t):
+    """The handle of a stream given to a call on the tensor t."""
+    if stream is None:
+        return None
+    _on(t.device, stream)
+    return stream.cuda_stream
 
 
 def fp8_workspace_size(dims: Dims | None = None) -> int:
@@ -530,7 +550,7 @@ def add_rmsnorm_fp8(x, weight=None, residual=None, eps=1e-6, want_y=True, sum_ou
     for each row's block of 128. Returns (r, y, q, scale): r is None without a
     residual (``sum_out`` gives its memory: x and residual are allowed), y None
     with ``want_y=False``."""
-    r = (_binding or _load_binding()).add_rmsnorm_fp8(x, weight, residual, eps, want_y, sum_out, _handle(stream))
+    r = (_binding or _load_binding()).add_rmsnorm_fp8(x, weight, residual, eps, want_y, sum_out, _handle(stream, x))
     if type(r) is int:
         raise MoeError(r, "moe_add_rmsnorm_fp8")
     return r
@@ -541,11 +561,11 @@ def fp8_quantize_weight(w, stream=None):
     a weight's layout for the 8-bit products, made once."""
     G, K, N = w.shape
     _expect(w, "w", (G, K, N), torch.bfloat16, w.device)
-    with torch.cuda.stream(stream):   # the memory is the stream's that writes it
+    with _on(w.device, stream):
         q = torch.empty(G, N, K, dtype=FP8, device=w.device)
         scale = torch.empty(G, _fp8_blocks(N), _fp8_blocks(K), dtype=torch.float32, device=w.device)
-    _ok(load().moe_fp8_quantize_weight(G, K, N, w.data_ptr(), q.data_ptr(), scale.data_ptr(),
-                                       _stream(stream)), "moe_fp8_quantize_weight")
+        _ok(load().moe_fp8_quantize_weight(G, K, N, w.data_ptr(), q.data_ptr(), scale.data_ptr(), _stream()),
+            "moe_fp8_quantize_weight")
     return q, scale
 
 
@@ -557,7 +577,7 @@ def fp8_matmul(a, a_scale, w, w_scale, ws, offsets=None, out_dtype=torch.bfloat1
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"out_dtype: bf16 or fp32 expected, got {out_dtype}")
     r = (_binding or _load_binding()).fp8_matmul(a, a_scale, w, w_scale, ws, offsets, out_dtype is torch.bfloat16, out,
-                                                 _handle(stream))
+                                                 _handle(stream, a))
     if type(r) is int:
         raise MoeError(r, "moe_fp8_matmul")
     return r
@@ -566,7 +586,7 @@ def fp8_matmul(a, a_scale, w, w_scale, ws, offsets=None, out_dtype=torch.bfloat1
 def fp8_gated(a, a_scale, w1, w1_scale, w3, w3_scale, ws, offsets=None, stream=None):
     """h[p] = silu(a[p] w1[g]^T) * (a[p] w3[g]^T) for the rows of each group as
     in :func:`fp8_matmul`, quantized: (h [R,F] e4m3, scale [R, ceil(F/128)])."""
-    r = (_binding or _load_binding()).fp8_gated(a, a_scale, w1, w1_scale, w3, w3_scale, ws, offsets, _handle(stream))
+    r = (_binding or _load_binding()).fp8_gated(a, a_scale, w1, w1_scale, w3, w3_scale, ws, offsets, _handle(stream, a))
     if type(r) is int:
         raise MoeError(r, "moe_fp8_gated")
     return r
@@ -609,10 +629,7 @@ def fp8_layer_forward(dims: Dims, x, xq, xq_scale, Wg, routed: Fp8Weights, ws, b
         _expect(bias, "bias", (dims.E,), torch.float32, dev)
     if shared_gate is not None:
         _expect(shared_gate, "shared_gate", (H,), torch.bfloat16, dev)
-    if out is None:
-        with torch.cuda.stream(stream):   # the memory is the stream's that writes it
-            out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
-    else:
+    if out is not None:
         _expect(out, "out", (T, H), torch.bfloat16, dev)
     if dims.F_shared > 0 and shared is None:
         raise ValueError("shared: the shared expert's weights are needed when F_shared > 0")
@@ -623,11 +640,14 @@ def fp8_layer_forward(dims: Dims, x, xq, xq_scale, Wg, routed: Fp8Weights, ws, b
         r = RoutingOut(*(ctypes.c_void_p(getattr(routing, n).data_ptr()) for n in
                          ("topk_idx", "topk_w", "counts", "offsets", "src_row", "inv_pos")))
     g = _gating(renormalize, shared_gate)
-    _ok(load().moe_fp8_layer_forward(ctypes.byref(dims), _p(x), _p(xq), _p(xq_scale), _p(Wg), _p(bias),
-                                     ctypes.byref(g) if g is not None else None, ctypes.byref(f),
-                                     ctypes.byref(fs) if fs is not None else None, _p(out),
-                                     ctypes.byref(r) if r is not None else None, _p(ws), ws.numel(),
-                                     _stream(stream)), "moe_fp8_layer_forward")
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+        _ok(load().moe_fp8_layer_forward(ctypes.byref(dims), _p(x), _p(xq), _p(xq_scale), _p(Wg), _p(bias),
+                                         ctypes.byref(g) if g is not None else None, ctypes.byref(f),
+                                         ctypes.byref(fs) if fs is not None else None, _p(out),
+                                         ctypes.byref(r) if r is not None else None, _p(ws), ws.numel(),
+                                         _stream()), "moe_fp8_layer_forward")
     return out
 
 
