@@ -251,6 +251,39 @@ def test_calls_run_on_their_tensors_device(lib, monkeypatch, streams):
             call(stream=fake_stream(7, 0))
 
 
+def test_layer_call_refuses_what_its_kernels_cannot_take(lib, monkeypatch, streams):
+    """The workspace and the routing outputs: type, size, layout and device, and
+    tensors in host memory, before the library is called."""
+    fake = FakeLibrary(streams)
+    monkeypatch.setattr(lib, "load", lambda: fake)
+    t = functools.partial(torch.empty, device="cuda:0")
+    T, E, k = 4, 8, 2
+
+    def routing(**kw):
+        good = dict(topk_idx=t(T, k, dtype=torch.int32), topk_w=t(T, k), counts=t(E, dtype=torch.int32),
+                    offsets=t(E + 1, dtype=torch.int32), src_row=t(T * k, dtype=torch.int32),
+                    inv_pos=t(T * k, dtype=torch.int32))
+        return lib.Routing(**{**good, **kw})
+
+    fake_fp8_layer_call(lib, "cuda:0", routing=routing())
+    assert len(fake.calls) == 1
+    i32 = dict(dtype=torch.int32)
+    bad = [dict(ws=t(1 << 18, **i32)), dict(ws=t(1 << 21, dtype=torch.uint8)[::2]),
+           dict(ws=torch.empty(1 << 20, dtype=torch.uint8)), dict(ws=t(1 << 20, dtype=torch.uint8).to("cuda:1"))]
+    bad += [dict(routing=routing(**kw)) for kw in (
+        dict(topk_idx=t(T, k, dtype=torch.int64)), dict(topk_idx=t(T, k + 1, **i32)), dict(topk_w=t(T, k, dtype=torch.bfloat16)),
+        dict(counts=t(E - 1, **i32)), dict(offsets=t(E, **i32)), dict(src_row=t(T, **i32)),
+        dict(inv_pos=t(2 * T * k, **i32)[::2]), dict(inv_pos=torch.empty(T * k, **i32)))]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            fake_fp8_layer_call(lib, "cuda:0", **kw)
+    with pytest.raises(ValueError):
+        fake_fp8_layer_call(lib, "cpu")
+    with pytest.raises(ValueError):
+        lib.fp8_quantize_weight(torch.empty(2, 64, 64, dtype=torch.bfloat16))
+    assert len(fake.calls) == 1
+
+
 # ------------------------------------------------------------------ on the GPU
 
 def gen(seed):

@@ -635,10 +635,17 @@ def fp8_layer_forward(dims: Dims, x, xq, xq_scale, Wg, routed: Fp8Weights, ws, b
         raise ValueError("shared: the shared expert's weights are needed when F_shared > 0")
     f = routed._struct(dims.E, H, dims.F, dev)
     fs = shared._struct(1, H, dims.F_shared, dev) if dims.F_shared > 0 else None
+    if ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous uint8 tensor on {dev}, got {ws.dtype} (strides {ws.stride()}) on "
+                         f"{ws.device}")
     r = None
     if routing is not None:
-        r = RoutingOut(*(ctypes.c_void_p(getattr(routing, n).data_ptr()) for n in
-                         ("topk_idx", "topk_w", "counts", "offsets", "src_row", "inv_pos")))
+        R, E = T * dims.k, dims.E
+        sizes = {"topk_idx": (T, dims.k), "topk_w": (T, dims.k), "counts": (E,), "offsets": (E + 1,), "src_row": (R,),
+                 "inv_pos": (R,)}
+        for n, size in sizes.items():
+            _expect(getattr(routing, n), n, size, torch.float32 if n == "topk_w" else torch.int32, dev)
+        r = RoutingOut(*(ctypes.c_void_p(getattr(routing, n).data_ptr()) for n in sizes))
     g = _gating(renormalize, shared_gate)
     with _on(dev, stream):
         if out is None:
