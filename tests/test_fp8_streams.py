@@ -284,6 +284,40 @@ def test_layer_call_refuses_what_its_kernels_cannot_take(lib, monkeypatch, strea
     assert len(fake.calls) == 1
 
 
+def bf16_calls(lib, device, T=4, H=64, F=64, E=8, k=2):
+    """Every bf16 call that makes its outputs, on tensors of one device."""
+    t = functools.partial(torch.empty, device=device)
+    bf, i32 = dict(dtype=torch.bfloat16), dict(dtype=torch.int32)
+    d = lib.make_dims(T, H, F, E, k)
+    x, Wg, W1, W2 = t(T, H, **bf), t(H, E, **bf), t(E, H, F, **bf), t(E, F, H, **bf)
+    idx, ws, slot = t(T, k, **i32), t(1 << 20, dtype=torch.uint8), t(k, T, H)
+    return [lambda **kw: lib.route(d, x, Wg, **kw), lambda **kw: lib.permute(d, idx, ws, **kw),
+            lambda **kw: lib.permute_static(d, idx, **kw), lambda **kw: lib.combine(d, slot, **kw),
+            lambda **kw: lib.expert_ffn(d, x, t(T * k, **i32), t(E + 1, **i32), W1, W1, W2, t(T, k), ws, **kw),
+            lambda **kw: lib.layer_forward(d, x, Wg, W1, W1, W2, ws, **kw),
+            lambda **kw: lib.route_tc_selftest(d, x, Wg, ws, **kw),
+            lambda **kw: lib.layer_forward_host(d, torch.empty(T, H, **bf), Wg, W1, W1, W2, ws, x, x,
+                                                torch.empty(T, H, **bf), **kw)]
+
+
+def test_bf16_calls_run_on_their_tensors_device_and_stream(lib, monkeypatch, streams):
+    fake = FakeLibrary(streams)
+    monkeypatch.setattr(lib, "load", lambda: fake)
+    for call in bf16_calls(lib, "cuda:1"):
+        call()
+        assert fake.calls[-1][1:] == (1, 101), fake.calls[-1]
+        call(stream=fake_stream(7, 1))
+        assert fake.calls[-1][1:] == (1, 7), fake.calls[-1]
+        with pytest.raises(ValueError, match="stream"):
+            call(stream=fake_stream(7, 0))
+    for call in bf16_calls(lib, "cuda:0")[:-1]:
+        with monkeypatch.context() as m:
+            taken = record_allocations(m, streams)
+            call(stream=fake_stream(2))
+        # the last: what the call makes (expert_ffn's arguments above come first)
+        assert taken[-1] == 2, fake.calls[-1]
+
+
 # ------------------------------------------------------------------ on the GPU
 
 def gen(seed):
@@ -438,3 +472,22 @@ def test_quantized_weights_on_a_side_stream_while_the_current_one_is_busy(lib):
         assert torch.equal(q.view(torch.uint8), want.view(torch.uint8)) and torch.equal(scale, want_scale)
     torch.cuda.synchronize()
     assert torch.equal(q.view(torch.uint8), want.view(torch.uint8)) and torch.equal(scale, want_scale)
+
+
+@gpu
+def test_bf16_layer_output_on_a_side_stream_while_the_current_one_is_busy(lib):
+    g = gen(7)
+    T, H, F, E, k = 300, 512, 256, 8, 2
+    Wg, W1, W3, W2 = weights(g, H, F, E)
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    layer = lib.MoELayer(Wg, W1, W3, W2, k)
+    want = layer.forward(x)
+    side = torch.cuda.Stream()
+    layer.workspace(T, side)
+    torch.cuda.synchronize()
+    late_fill([want.numel() * 2] * 4, 0xFF)
+    got = layer.forward(x, stream=side)
+    with torch.cuda.stream(side):
+        assert torch.equal(got, want)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)

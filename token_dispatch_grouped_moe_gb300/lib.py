@@ -254,16 +254,17 @@ def route_tc_selftest(dims: Dims, x, Wg, ws, bias=None, renormalize=True, force_
     number of tokens recomputed in the canonical order)."""
     T, k, E = dims.T, dims.k, dims.E
     dev = x.device
-    idx = torch.empty(T, k, dtype=torch.int32, device=dev)
-    w = torch.empty(T, k, dtype=torch.float32, device=dev)
-    fast = torch.empty(T, E, dtype=torch.float32, device=dev) if want_fast else None
-    bound = torch.empty(T, dtype=torch.float32, device=dev) if want_fast else None
-    n = ctypes.c_int64(0)
-    _ok(load().moe_selftest_route_tc(ctypes.byref(dims), _p(x), _p(Wg), _p(bias), int(renormalize),
-                                     int(force_exact), _p(idx), _p(w), _p(fast), _p(bound),
-                                     ctypes.byref(n), _p(ws), ws.numel(), _stream(stream)),
-        "moe_selftest_route_tc")
-    return idx, w, fast, bound, int(n.value)
+    with _on(dev, stream):
+        idx = torch.empty(T, k, dtype=torch.int32, device=dev)
+        w = torch.empty(T, k, dtype=torch.float32, device=dev)
+        fast = torch.empty(T, E, dtype=torch.float32, device=dev) if want_fast else None
+        bound = torch.empty(T, dtype=torch.float32, device=dev) if want_fast else None
+        n = ctypes.c_int64(0)
+        _ok(load().moe_selftest_route_tc(ctypes.byref(dims), _p(x), _p(Wg), _p(bias), int(renormalize),
+                                         int(force_exact), _p(idx), _p(w), _p(fast), _p(bound),
+                                         ctypes.byref(n), _p(ws), ws.numel(), _stream(stream)),
+            "moe_selftest_route_tc")
+        return idx, w, fast, bound, int(n.value)
 
 
 def launch_count() -> int:
@@ -320,27 +321,29 @@ def _gating(renormalize=True, shared_gate=None):
 def route(dims: Dims, x, Wg, bias=None, topk_idx=None, topk_w=None, stream=None, renormalize=True):
     T, k = dims.T, dims.k
     dev = x.device
-    topk_idx = topk_idx if topk_idx is not None else torch.empty(T, k, dtype=torch.int32, device=dev)
-    topk_w = topk_w if topk_w is not None else torch.empty(T, k, dtype=torch.float32, device=dev)
-    g = _gating(renormalize)
-    _ok(load().moe_route_ex(ctypes.byref(dims), _p(x), _p(Wg), _p(bias),
-                            ctypes.byref(g) if g is not None else None, _p(topk_idx), _p(topk_w),
-                            _stream(stream)), "moe_route_ex")
-    return topk_idx, topk_w
+    with _on(dev, stream):
+        topk_idx = topk_idx if topk_idx is not None else torch.empty(T, k, dtype=torch.int32, device=dev)
+        topk_w = topk_w if topk_w is not None else torch.empty(T, k, dtype=torch.float32, device=dev)
+        g = _gating(renormalize)
+        _ok(load().moe_route_ex(ctypes.byref(dims), _p(x), _p(Wg), _p(bias),
+                                ctypes.byref(g) if g is not None else None, _p(topk_idx), _p(topk_w),
+                                _stream(stream)), "moe_route_ex")
+        return topk_idx, topk_w
 
 
 def permute(dims: Dims, topk_idx, ws, x=None, want_x_perm=False, stream=None):
     R, E = dims.T * dims.k, dims.E
     dev = topk_idx.device
-    counts = torch.empty(E, dtype=torch.int32, device=dev)
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    src_row = torch.empty(R, dtype=torch.int32, device=dev)
-    inv_pos = torch.empty(R, dtype=torch.int32, device=dev)
-    x_perm = torch.empty(R, dims.H, dtype=torch.bfloat16, device=dev) if want_x_perm else None
-    _ok(load().moe_permute(ctypes.byref(dims), _p(topk_idx), _p(counts), _p(offsets), _p(src_row),
-                           _p(inv_pos), _p(x), _p(x_perm), _p(ws), ws.numel(), _stream(stream)),
-        "moe_permute")
-    return counts, offsets, src_row, inv_pos, x_perm
+    with _on(dev, stream):
+        counts = torch.empty(E, dtype=torch.int32, device=dev)
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        src_row = torch.empty(R, dtype=torch.int32, device=dev)
+        inv_pos = torch.empty(R, dtype=torch.int32, device=dev)
+        x_perm = torch.empty(R, dims.H, dtype=torch.bfloat16, device=dev) if want_x_perm else None
+        _ok(load().moe_permute(ctypes.byref(dims), _p(topk_idx), _p(counts), _p(offsets), _p(src_row),
+                               _p(inv_pos), _p(x), _p(x_perm), _p(ws), ws.numel(), _stream(stream)),
+            "moe_permute")
+        return counts, offsets, src_row, inv_pos, x_perm
 
 
 def permute_static(dims: Dims, topk_idx, x=None, want_x_perm=False, stream=None):
@@ -348,33 +351,36 @@ def permute_static(dims: Dims, topk_idx, x=None, want_x_perm=False, stream=None)
     library; calls on one device must not overlap on the GPU)."""
     R, E = dims.T * dims.k, dims.E
     dev = topk_idx.device
-    counts = torch.empty(E, dtype=torch.int32, device=dev)
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    src_row = torch.empty(R, dtype=torch.int32, device=dev)
-    inv_pos = torch.empty(R, dtype=torch.int32, device=dev)
-    x_perm = torch.empty(R, dims.H, dtype=torch.bfloat16, device=dev) if want_x_perm else None
-    _ok(load().moe_permute_static(ctypes.byref(dims), _p(topk_idx), _p(counts), _p(offsets),
-                                  _p(src_row), _p(inv_pos), _p(x), _p(x_perm), _stream(stream)),
-        "moe_permute_static")
-    return counts, offsets, src_row, inv_pos, x_perm
+    with _on(dev, stream):
+        counts = torch.empty(E, dtype=torch.int32, device=dev)
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        src_row = torch.empty(R, dtype=torch.int32, device=dev)
+        inv_pos = torch.empty(R, dtype=torch.int32, device=dev)
+        x_perm = torch.empty(R, dims.H, dtype=torch.bfloat16, device=dev) if want_x_perm else None
+        _ok(load().moe_permute_static(ctypes.byref(dims), _p(topk_idx), _p(counts), _p(offsets),
+                                      _p(src_row), _p(inv_pos), _p(x), _p(x_perm), _stream(stream)),
+            "moe_permute_static")
+        return counts, offsets, src_row, inv_pos, x_perm
 
 
 def expert_ffn(dims: Dims, x, src_row, offsets, W1, W3, W2, topk_w, ws, slot=None, stream=None):
-    if slot is None:
-        slot = torch.empty(dims.k, dims.T, dims.H, dtype=torch.float32, device=x.device)
-    _ok(load().moe_expert_ffn(ctypes.byref(dims), _p(x), _p(src_row), _p(offsets), _p(W1), _p(W3),
-                              _p(W2), _p(topk_w), _p(slot), _p(ws), ws.numel(), _stream(stream)),
-        "moe_expert_ffn")
-    return slot
+    with _on(x.device, stream):
+        if slot is None:
+            slot = torch.empty(dims.k, dims.T, dims.H, dtype=torch.float32, device=x.device)
+        _ok(load().moe_expert_ffn(ctypes.byref(dims), _p(x), _p(src_row), _p(offsets), _p(W1), _p(W3),
+                                  _p(W2), _p(topk_w), _p(slot), _p(ws), ws.numel(), _stream(stream)),
+            "moe_expert_ffn")
+        return slot
 
 
 def combine(dims: Dims, slot, n_slots=None, out=None, stream=None):
-    n_slots = n_slots if n_slots is not None else slot.shape[0]
-    if out is None:
-        out = torch.empty(dims.T, dims.H, dtype=torch.bfloat16, device=slot.device)
-    _ok(load().moe_combine(ctypes.byref(dims), _p(slot), int(n_slots), _p(out), _stream(stream)),
-        "moe_combine")
-    return out
+    with _on(slot.device, stream):
+        n_slots = n_slots if n_slots is not None else slot.shape[0]
+        if out is None:
+            out = torch.empty(dims.T, dims.H, dtype=torch.bfloat16, device=slot.device)
+        _ok(load().moe_combine(ctypes.byref(dims), _p(slot), int(n_slots), _p(out), _stream(stream)),
+            "moe_combine")
+        return out
 
 
 @dataclass
@@ -399,26 +405,27 @@ def routing_buffers(dims: Dims, device) -> Routing:
 def layer_forward(dims: Dims, x, Wg, W1, W3, W2, ws, bias=None, W1s=None, W3s=None, W2s=None,
                   out=None, routing: Routing | None = None, events: StageEvents | None = None,
                   stream=None, renormalize=True, shared_gate=None):
-    if out is None:
-        out = torch.empty(dims.T, dims.H, dtype=torch.bfloat16, device=x.device)
-    r = None
-    if routing is not None:
-        r = RoutingOut(*(ctypes.c_void_p(getattr(routing, n).data_ptr()) for n in
-                         ("topk_idx", "topk_w", "counts", "offsets", "src_row", "inv_pos")))
-    g = _gating(renormalize, shared_gate)
-    if g is None:
-        _ok(load().moe_layer_forward(ctypes.byref(dims), _p(x), _p(Wg), _p(bias), _p(W1), _p(W3), _p(W2),
-                                     _p(W1s), _p(W3s), _p(W2s), _p(out),
-                                     ctypes.byref(r) if r is not None else None, _p(ws), ws.numel(),
-                                     ctypes.byref(events) if events is not None else None,
-                                     _stream(stream)), "moe_layer_forward")
-    else:
-        _ok(load().moe_layer_forward_ex(ctypes.byref(dims), _p(x), _p(Wg), _p(bias), ctypes.byref(g),
-                                        _p(W1), _p(W3), _p(W2), _p(W1s), _p(W3s), _p(W2s), _p(out),
-                                        ctypes.byref(r) if r is not None else None, _p(ws), ws.numel(),
-                                        ctypes.byref(events) if events is not None else None,
-                                        _stream(stream)), "moe_layer_forward_ex")
-    return out
+    with _on(x.device, stream):
+        if out is None:
+            out = torch.empty(dims.T, dims.H, dtype=torch.bfloat16, device=x.device)
+        r = None
+        if routing is not None:
+            r = RoutingOut(*(ctypes.c_void_p(getattr(routing, n).data_ptr()) for n in
+                             ("topk_idx", "topk_w", "counts", "offsets", "src_row", "inv_pos")))
+        g = _gating(renormalize, shared_gate)
+        if g is None:
+            _ok(load().moe_layer_forward(ctypes.byref(dims), _p(x), _p(Wg), _p(bias), _p(W1), _p(W3), _p(W2),
+                                         _p(W1s), _p(W3s), _p(W2s), _p(out),
+                                         ctypes.byref(r) if r is not None else None, _p(ws), ws.numel(),
+                                         ctypes.byref(events) if events is not None else None,
+                                         _stream(stream)), "moe_layer_forward")
+        else:
+            _ok(load().moe_layer_forward_ex(ctypes.byref(dims), _p(x), _p(Wg), _p(bias), ctypes.byref(g),
+                                            _p(W1), _p(W3), _p(W2), _p(W1s), _p(W3s), _p(W2s), _p(out),
+                                            ctypes.byref(r) if r is not None else None, _p(ws), ws.numel(),
+                                            ctypes.byref(events) if events is not None else None,
+                                            _stream(stream)), "moe_layer_forward_ex")
+        return out
 
 
 def layer_forward_host(dims: Dims, x_host, Wg, W1, W3, W2, ws, x_dev, out_dev, out_host=None, bias=None,
@@ -427,13 +434,14 @@ def layer_forward_host(dims: Dims, x_host, Wg, W1, W3, W2, ws, x_dev, out_dev, o
     x_dev/out_dev device staging buffers of [T, H] bf16; the chunks' copies
     overlap the layer's kernels. Returns out_host (valid once the stream has
     been synchronized)."""
-    if out_host is None:
-        out_host = torch.empty(dims.T, dims.H, dtype=torch.bfloat16).pin_memory()
-    _ok(load().moe_layer_forward_host(ctypes.byref(dims), _p(x_host), _p(Wg), _p(bias), _p(W1), _p(W3), _p(W2),
-                                      _p(W1s), _p(W3s), _p(W2s), _p(out_host), _p(x_dev), _p(out_dev),
-                                      int(n_chunks), _p(ws), ws.numel(), _stream(stream)),
-        "moe_layer_forward_host")
-    return out_host
+    with _on(x_dev.device, stream):
+        if out_host is None:
+            out_host = torch.empty(dims.T, dims.H, dtype=torch.bfloat16).pin_memory()
+        _ok(load().moe_layer_forward_host(ctypes.byref(dims), _p(x_host), _p(Wg), _p(bias), _p(W1), _p(W3), _p(W2),
+                                          _p(W1s), _p(W3s), _p(W2s), _p(out_host), _p(x_dev), _p(out_dev),
+                                          int(n_chunks), _p(ws), ws.numel(), _stream(stream)),
+            "moe_layer_forward_host")
+        return out_host
 
 
 def host_chunks(dims: Dims) -> int:
