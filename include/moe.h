@@ -517,6 +517,12 @@ moe_status moe_fp8_gated(int64_t R, int32_t K, int32_t F, int32_t G, const moe_e
                          const float* w3_scale, moe_e4m3* h, float* h_scale, void* ws, size_t ws_bytes,
                          moe_stream_t stream);
 
+/* Test hook (host only): which kernel a product of these sizes (gated != 0: a
+ * gated one) runs on a device of num_sms SMs: 0 one CTA per MMA, 1 the same with
+ * tiles of 128 columns, 2 a CTA pair; -1 for sizes that the calls refuse. The
+ * result does not depend on it but for the order of its sums. */
+int32_t moe_selftest_fp8_form(int64_t R, int32_t K, int32_t N, int32_t G, int32_t gated, int32_t num_sms);
+
 /* One expert set's 8-bit weights: w1, w3 [E,F,H], w2 [E,H,F] and their scales
  * (moe_fp8_quantize_weight of W1, W3, W2). */
 typedef struct {

@@ -66,24 +66,48 @@ Fp8GemmArgs product_args(int32_t R, int32_t K, int32_t N, int32_t G, const int32
 // 266 -> 277, 512: 458 -> 448, 1024: 850 -> 793; product K = 1408, N = 2048,
 // 64 groups: 768: 195 -> 207, 1536: 371 -> 365; product K = 14336, N = 4096,
 // 8 groups: 1024: 391 -> 402; one group 4096 x 4096: 4096: 72 -> 71, 8192:
-// 125 -> 122. Fewer rows pad more in 256-row tiles; and K is split only with
-// one CTA.
-bool pair_for(int64_t R, int32_t G, bool gated) { return R >= (int64_t)(gated ? 512 : 2048) * G; }
+// 125 -> 122. Fewer rows pad more in 256-row tiles. And K is split only with one
+// CTA, which pays from about 64 blocks of K on where the pairs' tiles (counted
+// for equal groups) leave most of a round idle: the only round more than half, or
+// the last of two or three more than 7/8. Gated, one group, K = 14336: 512 rows,
+// N = 256 31 -> 48, 2048 rows, N = 256 35 -> 50, 4096 rows, N = 256 (0.42 rounds)
+// 44 -> 51, 2048 rows, N = 640 (0.53) 62 -> 51, 4096 rows, N = 640 (1.05) 83 ->
+// 99, 2048 rows, N = 1408, 4 groups (1.16) 137 -> 100, 8192 rows, N = 640 (2.11)
+// 139 -> 151; K = 10240: 0.21 rounds 31 -> 37, 0.42 36 -> 38; K = 8192: 0.21 29 ->
+// 31, 0.42 33 -> 32, 1.05 58 -> 58; K = 6144: 0.21 27 -> 25.
+bool pair_for(int64_t R, int32_t K, int32_t N, int32_t G, bool gated, int sms)
+{
+    if (R < (int64_t)(gated ? 512 : 2048) * G) return false;
+    if (K <= 64 * kFp8Block) return true;
+    const int n_out = gated ? 128 : 256;
+    const int64_t tiles = G * (((R + G - 1) / G + 255) / 256) * ((N + n_out - 1) / n_out);
+    const int64_t pairs = sms > 1 ? sms / 2 : 1, rounds = tiles / pairs, last = tiles % pairs;
+    if (rounds == 0) return 2 * last >= pairs;
+    return rounds > 2 || last == 0 || 8 * last >= pairs;
+}
 
-// The form of a product: a pair as above; tiles of 128 columns where all of them
-// find an SM (counted from above: every group may begin a tile) and the blocks
-// are few, or the rows too many for a cheap join of cut tiles; else of 256.
-// Measured, 256 / 128 columns, us, one group N = 4096: 8 rows K = 512 6.5 / 5.8,
-// 4096: 11.3 / 11.9; 16 rows K = 2048 9.8 / 9.4; 64 rows K = 4096 15.6 / 13.4;
-// 512 rows K = 4096 19.6 / 16.0, 8192: 29.3 / 26.4, 12288: 36.3 / 38.0; two of 8
-// experts 14336 -> 4096, one row each 29.7 / 40.9; 6 of 64 1408 -> 2048 10.5 /
-// 11.4; 160 tiles of 128 columns on 152 SMs 20.0 / 28.0.
+// The form of a product: tiles of 128 columns where all of them find an SM
+// (counted from above: every group may begin a tile) and the blocks are few, or
+// the rows too many for a cheap join of cut tiles; else a pair as above, or one
+// CTA with tiles of 256 columns. Measured, 256 / 128 columns, us, one group N =
+// 4096: 8 rows K = 512 6.5 / 5.8, 4096: 11.3 / 11.9; 16 rows K = 2048 9.8 / 9.4; 64
+// rows K = 4096 15.6 / 13.4; 512 rows K = 4096 19.6 / 16.0, 8192: 29.3 / 26.4,
+// 12288: 36.3 / 38.0; two of 8 experts 14336 -> 4096, one row each 29.7 / 40.9; 6
+// of 64 1408 -> 2048 10.5 / 11.4; 160 tiles of 128 columns on 152 SMs 20.0 / 28.0.
+// A pair / 128 columns, one group N = 256: 2048 rows K = 1024 9.5 / 7.7, 8192 rows
+// K = 1024 9.9 / 8.3, 4096: 19.3 / 16.9, 8192: 32.6 / 27.8; 8 groups of 2048 rows,
+// N = 128, K = 2048 13.1 / 11.2.
 Fp8GemmForm product_form(int64_t R, int32_t K, int32_t N, int32_t G, int sms)
 {
-    if (pair_for(R, G, false)) return kFp8Pair;
     const int64_t m_tiles = G == 1 ? (R + 127) / 128 : R / 128 + (R < G ? R : G);
     const bool fit = m_tiles * ((N + 127) / 128) <= sms;
-    return fit && (K <= 1024 || (K <= 8192 && R >= (int64_t)16 * G)) ? kFp8Narrow : kFp8Wide;
+    if (fit && (K <= 1024 || (K <= 8192 && R >= (int64_t)16 * G))) return kFp8Narrow;
+    return pair_for(R, K, N, G, false, sms) ? kFp8Pair : kFp8Wide;
+}
+
+Fp8GemmForm gated_form(int64_t R, int32_t K, int32_t F, int32_t G, int sms)
+{
+    return pair_for(R, K, F, G, true, sms) ? kFp8Pair : kFp8Wide;
 }
 
 moe_status run_product(Fp8GemmArgs a, const moe_e4m3* A, Operand w, bool f32, void* out, int sms, cudaStream_t s)
@@ -103,7 +127,7 @@ moe_status run_gated(Fp8GemmArgs a, const moe_e4m3* A, Operand w1, Operand w3, m
                      cudaStream_t s)
 {
     CUtensorMap ma, m1, m3;
-    const Fp8GemmForm form = pair_for(a.R, a.G, true) ? kFp8Pair : kFp8Wide;
+    const Fp8GemmForm form = gated_form(a.R, a.K, a.N, a.G, sms);
     if (!encode_map_e4m3(&ma, A, (uint64_t)a.K, (uint64_t)a.R, 0, kFp8Block, 128) ||
         !encode_map_e4m3(&m1, w1.v, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.G, kFp8Block, fp8_box_rows(true, form)) ||
         !encode_map_e4m3(&m3, w3.v, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.G, kFp8Block, fp8_box_rows(true, form)))
@@ -239,6 +263,12 @@ moe_status moe_fp8_gated(int64_t R, int32_t K, int32_t F, int32_t G, const moe_e
     MOE_TRY_STATUS(run_gated(product_args((int32_t)R, K, F, G, offsets, a_scale, ws), a, {w1, w1_scale},
                              {w3, w3_scale}, h, h_scale, sms, (cudaStream_t)stream));
     return finish(cudaSuccess, ws, (cudaStream_t)stream);
+}
+
+int32_t moe_selftest_fp8_form(int64_t R, int32_t K, int32_t N, int32_t G, int32_t gated, int32_t num_sms)
+{
+    if (check_product(R, K, N, G, /*grouped=*/true) != MOE_OK || num_sms <= 0) return -1;
+    return gated ? gated_form(R, K, N, G, num_sms) : product_form(R, K, N, G, num_sms);
 }
 
 moe_status moe_fp8_layer_forward(const moe_dims* dims, const moe_bf16* x, const moe_e4m3* xq, const float* xq_scale,

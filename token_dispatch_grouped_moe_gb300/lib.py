@@ -27,7 +27,8 @@ EXPORTS = ["moe_version", "moe_status_string", "moe_workspace_size", "moe_check"
            "moe_get_option", "moe_permute_static", "moe_route_ex", "moe_layer_forward_ex",
            "moe_layer_plan", "moe_selftest_wait_timeout", "moe_launch_count", "moe_selftest_route_tc",
            "moe_layer_forward_host", "moe_host_chunks", "moe_fp8_workspace_size", "moe_add_rmsnorm_fp8",
-           "moe_fp8_quantize_weight", "moe_fp8_matmul", "moe_fp8_gated", "moe_fp8_layer_forward"]
+           "moe_fp8_quantize_weight", "moe_fp8_matmul", "moe_fp8_gated", "moe_fp8_layer_forward",
+           "moe_selftest_fp8_form"]
 
 OPT_GEMM0_A = 0
 GEMM0_A_PERMUTED = 0      # dispatch copies token rows to x_perm; GEMM0 loads dense tiles
@@ -162,6 +163,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_fp8_matmul.argtypes = [i64, i32, i32, i32, P, P, P, P, P, i32, P, P, sz, P]
     lib.moe_fp8_gated.restype = ctypes.c_int
     lib.moe_fp8_gated.argtypes = [i64, i32, i32, i32, P, P, P, P, P, P, P, P, P, P, sz, P]
+    lib.moe_selftest_fp8_form.restype = i32
+    lib.moe_selftest_fp8_form.argtypes = [i64, i32, i32, i32, i32, i32]
     lib.moe_fp8_layer_forward.restype = ctypes.c_int
     lib.moe_fp8_layer_forward.argtypes = [D, P, P, P, P, P, ctypes.POINTER(Gating), ctypes.POINTER(Fp8Ffn),
                                           ctypes.POINTER(Fp8Ffn), P, ctypes.POINTER(RoutingOut), P, sz, P]
@@ -598,6 +601,14 @@ def fp8_gated(a, a_scale, w1, w1_scale, w3, w3_scale, ws, offsets=None, stream=N
     if type(r) is int:
         raise MoeError(r, "moe_fp8_gated")
     return r
+
+
+FP8_FORM_WIDE, FP8_FORM_NARROW, FP8_FORM_PAIR = 0, 1, 2
+
+
+def fp8_form_selftest(R, K, N, G=1, gated=False, num_sms=152) -> int:
+    """Which kernel a product of these sizes runs (test hook moe_selftest_fp8_form)."""
+    return int(load().moe_selftest_fp8_form(R, K, N, G, int(gated), num_sms))
 
 
 @dataclass
