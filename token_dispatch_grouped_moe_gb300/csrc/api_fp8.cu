@@ -16,8 +16,6 @@ namespace {
 constexpr int32_t kNormMaxH = 32768;
 static_assert(kFp8PartOffset == MOE_FP8_WORKSPACE_ZEROS, "what has to be zero lies before the parts");
 
-size_t blocks_of(int32_t n) { return ((size_t)n + kFp8Block - 1) / kFp8Block; }
-
 moe_status check_ws(const void* ws, size_t ws_bytes, size_t need)
 {
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < need) return MOE_ERR_WORKSPACE;
@@ -147,6 +145,10 @@ moe_status check_ffn(const moe_fp8_ffn* f)
     return MOE_OK;
 }
 
+// The scales behind R quantized rows of n values: 4 bytes for each block of 128
+// fit into the other half of their buffer (n is a multiple of 64).
+float* scales_behind(moe_e4m3* rows, size_t R, int32_t n) { return reinterpret_cast<float*>(rows + R * (size_t)n); }
+
 // One expert set's gated product and second product; rows of the second are
 // scattered to slots (src_row) or written in order to slot.
 moe_status run_ffn(int32_t R, int32_t H, int32_t F, int32_t G, const int32_t* offsets, Operand x,
@@ -154,7 +156,7 @@ moe_status run_ffn(int32_t R, int32_t H, int32_t F, int32_t G, const int32_t* of
                    unsigned char* h, void* ws, int sms, cudaStream_t s)
 {
     moe_e4m3* hq = h;
-    float* hs = reinterpret_cast<float*>(h + al256((size_t)R * F));
+    float* hs = scales_behind(h, (size_t)R, F);
     MOE_TRY_STATUS(run_gated(product_args(R, H, F, G, offsets, x.scale, ws), x.v, {f.w1, f.w1_scale},
                              {f.w3, f.w3_scale}, hq, hs, sms, s));
     Fp8GemmArgs a = product_args(R, F, H, G, offsets, hs, ws);
@@ -165,23 +167,18 @@ moe_status run_ffn(int32_t R, int32_t H, int32_t F, int32_t G, const int32_t* of
     return run_product(a, hq, {f.w2, f.w2_scale}, /*f32=*/true, slot, sms, s);
 }
 
-// The layer's workspace: the products' part, the layer's own layout, the
-// quantized dispatch rows and h of the routed and of the shared experts.
+// The layer's workspace: the products' part, then that of the bf16 layer, whose
+// buffers for dispatched rows and h (2 bytes an element) hold the quantized rows
+// and, behind them, their scales.
 struct LayerLayout {
-    size_t base, x_perm, x_scale, h, h_shared, total;
+    size_t base, total;
 };
 
 LayerLayout layer_layout(const moe_dims& d)
 {
-    const size_t T = (size_t)d.T, R = T * d.k;
     LayerLayout L;
-    size_t o = al256(kFp8WorkspaceBytes);
-    L.base = o; o += al256(moe_workspace_size(&d));
-    L.x_perm = o; o += al256(R * (size_t)d.H);
-    L.x_scale = o; o += al256(R * blocks_of(d.H) * 4);
-    L.h = o; o += al256(R * (size_t)d.F) + al256(R * blocks_of(d.F) * 4);
-    L.h_shared = o; o += al256(T * (size_t)d.F_shared) + al256(T * blocks_of(d.F_shared) * 4);
-    L.total = o;
+    L.base = al256(kFp8WorkspaceBytes);
+    L.total = L.base + al256(moe_workspace_size(&d));
     return L;
 }
 
@@ -302,20 +299,20 @@ moe_status moe_fp8_layer_forward(const moe_dims* dims, const moe_bf16* x, const 
     Range layer_range("moe/fp8_layer_forward");
     Range stage("moe/route");
     MOE_TRY_STATUS(route_and_sort(d, plan.router, x, Wg, bias, gating, rt, w + L.base, err, sms, nullptr, stage, s));
-    moe_e4m3* xp = w + L.x_perm;
-    float* xs = reinterpret_cast<float*>(w + L.x_scale);
+    moe_e4m3* xp = rt.x_perm;
+    float* xs = scales_behind(xp, (size_t)R, d.H);
     MOE_TRY(launch_fp8_dispatch(xq, xq_scale, rt.topk_idx, rt.inv_pos, rt.offsets + d.E, xp, xs, d.T, d.H, d.k, d.E, err,
                                 sms, s));
     stage.next("moe/experts");
     MOE_TRY_STATUS(run_ffn((int32_t)R, d.H, d.F, d.E, rt.offsets, {xp, xs}, *routed, rt.src_row, rt.topk_w, d.k, d.T,
-                           rt.slot, w + L.h, ws, sms, s));
+                           rt.slot, rt.h, ws, sms, s));
     if (d.F_shared > 0) {
         stage.next("moe/shared_expert");
         // every token, in token order, with weight 1 or the sigmoid gate's
         if (shared_gate) MOE_TRY(launch_shared_gate(x, shared_gate, rt.shared_gate, d.T, d.H, sms, s));
         MOE_TRY_STATUS(run_ffn((int32_t)d.T, d.H, d.F_shared, 1, nullptr, {xq, xq_scale}, *shared, nullptr,
                                shared_gate ? rt.shared_gate : nullptr, 1, d.T, rt.slot + (size_t)R * d.H,
-                               w + L.h_shared, ws, sms, s));
+                               rt.h_shared, ws, sms, s));
     }
     stage.next("moe/combine");
     MOE_TRY(launch_combine(rt.slot, d.k + (d.F_shared > 0 ? 1 : 0), out, d.T, d.H, sms, s));
