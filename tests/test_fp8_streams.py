@@ -339,6 +339,7 @@ def late_fill(sizes, value):
     blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
     for b in blocks:
         b.fill_(value)
+    return {b.data_ptr() for b in blocks}
 
 
 @gpu
@@ -491,3 +492,36 @@ def test_bf16_layer_output_on_a_side_stream_while_the_current_one_is_busy(lib):
         assert torch.equal(got, want)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+@gpu
+@pytest.mark.parametrize("call", ["norm", "matmul", "gated", "quantize_weight", "layer"])
+def test_outputs_of_a_call_on_a_side_stream_are_that_streams_memory(lib, call):
+    """While the current stream still has to write blocks of the outputs' sizes
+    that the host has freed: outputs out of its pool would be those blocks."""
+    g = gen(8)
+    T, H, F, E, k = 128, 512, 256, 8, 2
+    Wg, W1, W3, W2 = weights(g, H, F, E)
+    layer = lib.MoEFp8Layer(None, Wg, W1, W3, W2, k)
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    _, y, q, s = lib.add_rmsnorm_fp8(x)
+    f, ws = layer.routed, lib.fp8_workspace(layer.dims(T))
+    one = (f.w1[:1], f.w1_scale[:1])
+    calls = {"norm": lambda **kw: lib.add_rmsnorm_fp8(x, residual=x, **kw),
+             "matmul": lambda **kw: (lib.fp8_matmul(q, s, *one, ws, **kw),),
+             "gated": lambda **kw: lib.fp8_gated(q, s, *one, *one, ws, **kw),
+             "quantize_weight": lambda **kw: lib.fp8_quantize_weight(W1, **kw),
+             "layer": lambda **kw: (lib.fp8_layer_forward(layer.dims(T), y, q, s, Wg, f, ws, **kw),)}
+    bits = lambda ts: [t.contiguous().view(torch.uint8) for t in ts]  # noqa: E731
+    want = bits(calls[call]())
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    freed = late_fill([t.numel() for t in want] * 2, 0xFF)
+    got = calls[call](stream=side)
+    assert not freed & {t.data_ptr() for t in got}
+    with torch.cuda.stream(side):
+        assert all(torch.equal(a, b) for a, b in zip(bits(got), want))
+    # what the current stream's pool gives now is among them
+    assert torch.empty(want[0].numel(), dtype=torch.uint8, device="cuda").data_ptr() in freed
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(bits(got), want))
