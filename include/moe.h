@@ -448,9 +448,10 @@ int32_t moe_host_chunks(const moe_dims* dims);
  *   weights [G, N, K]:  a scale for each 128 x 128 block, scale[G, ceil(N/128),
  *                       ceil(K/128)]. K is contiguous (the transpose of the
  *                       bf16 weights above).
- * Quantizing a block: scale = max(largest |v|, 2^-100) / 448, q = v / scale to
- * nearest (ties to even); a NaN or infinity in a block makes all of it NaN or
- * is carried as NaN. Sizes are multiples of 16, the last block may be shorter.
+ * Quantizing a block: scale = max(largest |v|, 2^-100) / 448, and q the nearest
+ * e4m3 (ties to even) to v / scale for weights, to v * (1 / scale) for
+ * activations, each operation rounded to fp32; a NaN or infinity in a block makes
+ * all of it NaN or is carried as NaN. Sizes are multiples of 16, the last block may be shorter.
  * The products accumulate in fp32 and apply the scales in fp32.
  *
  * Conventions are those of the other entry points. The workspace `ws` of the

@@ -2,10 +2,17 @@
 // (device), and the kernels' launchers (host). Internal.
 //
 // A value v of a block of 128 is held as e4m3 q with the block's fp32 scale:
-//   scale = max(largest |v| of the block, 2^-100) / 448,  q = e4m3(v / scale),
-// rounded to nearest, ties to even (448 is the largest e4m3 value; the floor
-// keeps the scale and its reciprocal finite for a block of zeros). A NaN in a
-// block makes its scale and so the whole block NaN.
+//   scale = max(largest |v| of the block, 2^-100) / 448,
+// q the nearest e4m3 (ties to even) to v / scale for weights and to v * (1 /
+// scale) for activations, in fp32 (448 is the largest e4m3 value; the floor keeps
+// the scale and its reciprocal finite for a block of zeros). A NaN in a block
+// makes its scale and so the whole block NaN.
+//
+// The product with the reciprocal is within 2^-23 of the quotient, so q is another
+// one for 2 of 10^7 values, whose quotients lie that near to the border between
+// two: either is as near to v. The quotient costs activations a division, or two
+// more FMAs a value: measured, us, 32768 x 2048 bf16 norm 54.7 -> 56.3, gated
+// prefill of 64 experts 2048 -> 1408 1050 -> 1064.
 #pragma once
 
 #include <cstdint>

@@ -170,8 +170,10 @@ cudaError_t launch_norm(const Fp8NormArgs& a, cudaStream_t s)
 // ---------------------------------------------------------------- weight --
 //
 // One block per 128 x 128 block of one expert's weight [K, N]: read along N,
-// kept in shared memory, written along K. The odd row pitch lets a warp read a
-// column of K values for 16 consecutive n without bank conflicts.
+// kept in shared memory, written along K: 128 bytes of 4 rows a warp. Its reads
+// of shared memory, 16 words of 4 columns and 8 places of K, lie in 4 banks (4-way
+// conflicts); 32 rows of 16 bytes would have none and write half sectors. Made
+// once for a weight: 64 experts 2048 x 1408 148 us, 3.7 TB/s, 0.56 of a copy.
 
 constexpr int kWPitch = 130;   // 16-bit values per staged row of 128
 
@@ -205,7 +207,6 @@ __global__ void __launch_bounds__(256) fp8_quantize_weight_kernel(const uint16_t
 #pragma unroll
     for (int i = 0; i < 8; ++i) amax = max_nan(amax, part[i]);
     const float sc = fp8_scale(amax);
-    const float inv = 1.0f / sc;
     if (threadIdx.x == 0)
         scale[(e * gridDim.x + blockIdx.x) * gridDim.y + blockIdx.y] = sc;
     for (int c = threadIdx.x; c < kFp8Block * 8; c += 256) {   // chunks of 16 k of one column
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(256) fp8_quantize_weight_kernel(const uint16_t
         if (n0 + nn >= N || k0 + kk >= K) continue;
         float f[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = __uint_as_float((uint32_t)tile[(kk + i) * kWPitch + nn] << 16) * inv;
+        for (int i = 0; i < 16; ++i) f[i] = __uint_as_float((uint32_t)tile[(kk + i) * kWPitch + nn] << 16) / sc;
         *reinterpret_cast<uint4*>(q + (e * N + n0 + nn) * K + k0 + kk) =
             make_uint4(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]),
                        e4m3x4(f[8], f[9], f[10], f[11]), e4m3x4(f[12], f[13], f[14], f[15]));
