@@ -565,7 +565,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 for (int kb = pc.kb0; kb < pc.kb1; ++kb) {
                     ok = __all_sync(0xffffffffu,
                                     mbar_wait(smem_u32(&st->full[stage]), phase, abort, args.err) &&
-                                        mbar_wait(smem_u32(&st->tempty[acc]), acc_phase ^ 1u, abort, args.err));
+                                        mbar_wait<PAIR, PAIR>(smem_u32(&st->tempty[acc]), acc_phase ^ 1u, abort, args.err));
                     if (!ok) break;
                     tc_fence_after();
                     if (leader) {

@@ -151,20 +151,33 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar)
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// The same arrival at CTA scope: it orders this thread's tcgen05 reads (after
-// tcgen05.fence::before_thread_sync) but publishes no memory to the other CTA.
+// The same arrival for a barrier that hands back TMEM: seen by the other CTA, but
+// releasing no memory. What it must come after, this thread's loads from TMEM, has
+// been waited for (tcgen05.wait::ld) and is ordered before it by
+// tcgen05.fence::before_thread_sync; a release would wait for everything else that
+// the thread has in flight.
 __device__ __forceinline__ void mbar_arrive_remote_tmem(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // CLUSTER: acquire at cluster scope (the phase was completed by arrivals from
-// another CTA of the cluster).
-template <bool CLUSTER = false>
+// another CTA of the cluster). TMEM: the same without an acquire, for a barrier
+// that hands back TMEM (mbar_arrive_remote_tmem); tcgen05.fence::after_thread_sync
+// orders what follows.
+template <bool CLUSTER = false, bool TMEM = false>
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
-    if constexpr (CLUSTER)
+    if constexpr (CLUSTER && TMEM)
+        asm volatile(
+            "{\n\t.reg .pred P;\n\t"
+            "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 P, [%1], %2;\n\t"
+            "selp.b32 %0, 1, 0, P;\n\t}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else if constexpr (CLUSTER)
         asm volatile(
             "{\n\t.reg .pred P;\n\t"
             "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 P, [%1], %2;\n\t"
@@ -200,14 +213,14 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
 // Waits for the phase of `bar` with parity `parity`. Returns false (after
 // recording a timeout and raising *abort) if it does not complete within
 // kWaitLimitNs, or if another role of the CTA has already raised *abort.
-template <bool CLUSTER = false>
+template <bool CLUSTER = false, bool TMEM = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort,
                                           uint32_t* err)
 {
-    if (mbar_try_wait<CLUSTER>(bar, parity)) return true;
+    if (mbar_try_wait<CLUSTER, TMEM>(bar, parity)) return true;
     unsigned long long t0 = globaltimer_ns();
     for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait<CLUSTER>(bar, parity)) return true;
+        if (mbar_try_wait<CLUSTER, TMEM>(bar, parity)) return true;
         if ((i & 255u) == 0) {
             if (*abort) return false;
             if (globaltimer_ns() - t0 > kWaitLimitNs) {
