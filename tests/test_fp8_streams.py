@@ -50,6 +50,7 @@ def streams(monkeypatch):
 
     monkeypatch.setattr(torch.cuda, "device", lambda d: on(device_stream(d)))
     monkeypatch.setattr(torch.cuda, "current_device", lambda: state.device())
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: device_stream(f"cuda:{index}").cuda_stream)
     state.captured = set()   # handles of streams that are being captured
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state.now() in state.captured)
     monkeypatch.setattr(torch.cuda, "stream", on)

@@ -176,9 +176,14 @@ def _p(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _raw_stream() -> int:
+    """The current stream's handle (torch.cuda.current_stream() makes an object
+    around it: 2.8 us a call)."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return ctypes.c_void_p(_raw_stream() if stream is None else stream.cuda_stream)
 
 
 def _on(device, stream):
@@ -468,7 +473,7 @@ class _Layer:
         with _on(self.Wg.device, stream):
             if torch.cuda.is_current_stream_capturing():
                 return self._new_workspace(self.dims(T))
-            key = torch.cuda.current_stream().cuda_stream
+            key = _raw_stream()
             rows, ws = self._ws.get(key, (-1, None))
             if rows < T:
                 rows = max(T, rows + rows // 4)
