@@ -29,7 +29,8 @@ int moe_forward(const moe_bf16* x, const moe_bf16* Wg, const moe_bf16* W1, const
 /* The same layer on 8-bit experts, in a residual stream: sum = x + residual and
  * its norm, quantized, then the layer. `experts` holds weights made once with
  * moe_fp8_quantize_weight; y, q and scale are [T, 4096] bf16, [T, 4096] e4m3
- * and [T, 32] floats; ws is moe_fp8_workspace_size(&d) bytes, zeroed once. */
+ * and [T, 32] floats; ws is moe_fp8_workspace_size(&d) bytes, the first
+ * MOE_FP8_WORKSPACE_ZEROS of them zeroed once. */
 int moe_forward_fp8(const moe_bf16* x, const moe_bf16* residual, const moe_bf16* norm_weight, const moe_bf16* Wg,
                     const moe_fp8_ffn* experts, moe_bf16* sum, moe_bf16* y, moe_e4m3* q, float* scale,
                     moe_bf16* out, int64_t T, void* ws, cudaStream_t stream)

@@ -480,7 +480,8 @@ size_t moe_fp8_workspace_size(const moe_dims* dims);
  *      (nullable, contiguous); q[T,H] and scale[T,ceil(H/128)]: y quantized
  *      (from fp32, not from its rounding).
  * H a multiple of 16 up to 32768; pointers but scale 16-byte aligned and row
- * strides multiples of 16 bytes.
+ * strides multiples of 16 bytes, at least H elements. The squares are summed in
+ * fp32: a row whose sum passes the largest fp32 (values of 2^64) has y = 0.
  */
 moe_status moe_add_rmsnorm_fp8(int64_t T, int32_t H, moe_dtype dtype, const void* x, int64_t x_stride,
                                const void* residual, int64_t residual_stride, const void* weight, float eps, void* sum,

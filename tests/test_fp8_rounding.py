@@ -74,6 +74,16 @@ def test_norm_quantization_is_the_product_with_the_reciprocal(lib, T, H):
 
 
 @gpu
+def test_norm_of_a_row_whose_squares_overflow(lib):
+    """As include/moe.h says: y = 0 for it, and nothing for its neighbours."""
+    x = torch.ones(3, 256, device="cuda")
+    x[1] = 2.0 ** 70
+    _, y, q, scale = lib.add_rmsnorm_fp8(x, eps=0.0)
+    assert bool((y[1] == 0).all()) and bool((q[1].float() == 0).all()) and bool((scale[1] == 2.0 ** -100 / 448).all())
+    assert bool((y[0] == 1).all()) and bool((y[2] == 1).all()) and bool((q[0].float() == 448).all())
+
+
+@gpu
 def test_norm_quantization_at_the_borders(lib):
     """Rows that the norm leaves as they are: mean square 1, two values of 8192 carry it.
     Either neighbour of a value at a border is as near to it."""

@@ -19,7 +19,7 @@
 namespace moe {
 namespace {
 
-constexpr int kVersion = 400;   // 0.4.0
+constexpr int kVersion = 401;   // 0.4.1
 constexpr int kMaxDevices = 64;
 
 // ------------------------------------------------------------ device info --

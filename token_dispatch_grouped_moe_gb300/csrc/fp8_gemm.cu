@@ -29,7 +29,8 @@
 // 256; both CTAs' boxes complete on rank 0's barrier, rank 0 issues, its commit
 // arrives in both CTAs, and both CTAs' fold warps release a buffer on rank 0.
 // A product of few tiles takes tiles of 128 columns (BN; 64 accumulators a thread,
-// a buffer given back after one trip to TMEM: 0.28 us a block instead of 0.42).
+// a buffer given back after one trip to TMEM: 0.31-0.33 us a block, of 256 columns
+// 0.39-0.43).
 // When the tiles do not fill the SMs evenly (few rows), K is cut: the blocks of
 // the tiles that are left over, end to end, go to the CTAs in equal runs; each
 // CTA writes the fp32 sums of a tile that it has only a part of to the
@@ -47,7 +48,9 @@
 //     of MMAs, the commit seen) and 700 to the next release, for two buffers. Back
 //     to back the product is at the GPU's power cap as well (1350 W, 1.6 GHz); the
 //     gated form, with about 4000 cycles of epilogue a tile (silu 1750, conversion
-//     and stores 1200), runs at 1.97 GHz. Measured and not kept: pairs of sums in
+//     and stores 1200), runs at 1.97 GHz. 32768 tokens, 64 experts 2048 -> 1408, top
+//     6, pass after pass: gated 1050 us; 8192 tokens, 8 experts 14336 -> 4096, top 2,
+//     Zipf: product 840-850 us. Measured and not kept: pairs of sums in
 //     fma.rn.f32x2 (register moves: 2.0 PFLOP/s), factors four blocks at a time, N =
 //     128 MMAs with four buffers, loads of the next block asked for before the last
 //     sums (spills), releases without memory order, one reciprocal for two silus,
@@ -89,7 +92,8 @@ constexpr int MAX_GROUPS = 256;
 // pair (tcgen05 cta_group::2): one MMA of 256 x 256 over both CTAs, each staging
 // its 128 rows of A and half of B's, so a third less comes from L2 per block.
 // BN is the MMA's N (gated: 128 columns of W1 and 128 of W3, interleaved by 64):
-// 256, or 128 for a product whose tiles of 256 fill less than half of the SMs.
+// 256, or 128 for a product whose tiles of 128 all find an SM (product_form in
+// api_fp8.cu).
 template <bool PAIR, int BN>
 struct Cfg {
     static constexpr int B_ROWS = PAIR ? BN / 2 : BN;
@@ -228,7 +232,10 @@ constexpr int JOIN_PARTS = 2;
 template <int BN>
 __device__ __forceinline__ Plan make_plan(int tiles, int rows, int k_blocks, int n_cta, int lane)
 {
-    // a block of 128 columns takes 0.26 us, the rest as long as for 256
+    // what a tile, a cut and a join cost beside the blocks, in blocks: more of the
+    // shorter ones of 128 columns (with 1.3, the blocks' own ratio, 16 rows of K =
+    // 2048, N = 4096 take 10.5 us instead of 9.4, 2048 rows of K = 4096, N = 256 17.7
+    // instead of 14.9, and 15 other shapes the same)
     constexpr float unit = BN == 256 ? 1.0f : 1.6f;
     constexpr int join_rows = FOLD_WARPS * JOIN_ROWS<BN>;
     const bool room = (int64_t)2 * n_cta * rows <= kFp8PartRows && 2 * n_cta <= kFp8MaxTickets;

@@ -562,7 +562,7 @@ def fp8_workspace(dims: Dims | None = None, device=None) -> torch.Tensor:
 
 def add_rmsnorm_fp8(x, weight=None, residual=None, eps=1e-6, want_y=True, sum_out=None, stream=None):
     """r = x + residual, y = r / sqrt(mean(r^2) + eps) * weight for the rows of
-    x [T,H] (bf16, fp16 or fp32; any row stride), and y in e4m3 with a scale
+    x [T,H] (bf16, fp16 or fp32; any row stride from H on), and y in e4m3 with a scale
     for each row's block of 128. Returns (r, y, q, scale): r is None without a
     residual (``sum_out`` gives its memory: x and residual are allowed), y None
     with ``want_y=False``."""
@@ -685,8 +685,10 @@ def fp8_layer_forward(dims: Dims, x, xq, xq_scale, Wg, routed: Fp8Weights, ws, b
 class MoEFp8Layer(_Layer):
     """A pre-norm expert layer of a residual stream, served in 8 bits: the
     residual's addition, the norm and its quantization, then the layer on
-    weights quantized once from bf16. ``forward(x, residual)`` returns (the
-    layer's output, the residual stream that the next layer adds it to)."""
+    weights quantized once from bf16 (on the stream current at that time).
+    ``forward(x, residual)`` returns (the layer's output, the residual stream
+    that the next layer adds it to); with ``stream`` it runs, and takes its
+    memory, there, behind what the caller has that stream wait for."""
 
     def __init__(self, norm_weight, Wg, W1, W3, W2, k, bias=None, W1s=None, W3s=None, W2s=None, eps=1e-6):
         self.norm_weight, self.Wg, self.bias, self.k, self.eps = norm_weight, Wg, bias, int(k), eps
