@@ -476,7 +476,8 @@ class _Layer:
             key = _raw_stream()
             rows, ws = self._ws.get(key, (-1, None))
             if rows < T:
-                rows = max(T, rows + rows // 4)
+                rows, ws = max(T, rows + rows // 4), None
+                self._ws.pop(key, None)   # its memory first, then the longer one's
                 ws = self._new_workspace(self.dims(rows))
                 self._ws[key] = (rows, ws)
         return ws
