@@ -551,6 +551,107 @@ moe_status moe_fp8_layer_forward(const moe_dims* dims, const moe_bf16* x, const 
                                  const moe_fp8_ffn* routed, const moe_fp8_ffn* shared, moe_bf16* out,
                                  const moe_routing_out* routing, void* ws, size_t ws_bytes, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Expert layers of another form: routing from given logits (moe_route_logits),
+ * a grouped product with bias, activation and residual (moe_linear), and the
+ * weighted sum of the experts' rows (moe_combine_rows). With moe_permute between
+ * the first two they are a layer whose router or experts moe_layer_forward does
+ * not have. Conventions are those of the other entry points.
+ */
+
+/* A router's scores of the logits l[E] of a token: softmax over all E, or 1 / (1 + e^-l). */
+typedef enum { MOE_SCORES_SOFTMAX = 0, MOE_SCORES_SIGMOID = 1 } moe_scores;
+
+typedef struct {
+    moe_scores scores;
+    const float* bias;     /* [E], added to the scores for the selection only; or null */
+    int32_t groups;        /* groups of E / groups neighbouring experts; 1 = none */
+    int32_t top_groups;    /* groups whose experts may be selected */
+    int32_t group_top;     /* a group's value: 1 its largest key, 2 the sum of its two largest score + bias */
+    int32_t renormalize;   /* 1: weights divided by their sum over the k selected */
+    float scale;           /* the weights' factor */
+} moe_scoring;
+
+/*
+ * Each token's k experts and weights from its logits:
+ *   s = scores(l); key = l without a bias (s is in the order of l), else s + bias;
+ *   the top_groups groups of the largest values keep their experts;
+ *   the k experts of the largest keys, descending;
+ *   w = s of the selected, / their sum if renormalize, * scale.
+ * Ties (of groups and of experts) go to the lower index. The order is that of real
+ * arithmetic up to fp64's rounding, whatever the logits' type.
+ * A logit of -inf is an expert with score 0 (selected, with weight 0, where no
+ * other is left; a softmax of nothing but -inf is all 0, and so is the
+ * renormalization of a sum of 0). A NaN logit comes after all others, and makes
+ * its row's k weights NaN.
+ * In:  logits[T,E] of type dtype, rows `stride` elements apart; scoring (null:
+ *      softmax, no bias, no groups, not renormalized, scale 1).
+ * Out: topk_idx[T,k], topk_w[T,k].
+ * 1 <= k <= 8, E <= 256, groups <= 32 and a divisor of E, group_top <= E / groups,
+ * k <= top_groups * (E / groups). Pointers aligned to their type.
+ */
+moe_status moe_route_logits(int64_t T, int32_t E, int32_t k, moe_dtype dtype, const void* logits, int64_t stride,
+                            const moe_scoring* scoring, int32_t* topk_idx, float* topk_w, moe_stream_t stream);
+
+/* relu: max(x, 0); silu: x / (1 + e^-x); gelu: x (1 + erf(x / sqrt 2)) / 2; gelu_tanh:
+ * x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2 */
+typedef enum {
+    MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_GELU_TANH = 4
+} moe_activation;
+
+/* A weight's layout: [G,K,N] (as the bf16 entry points' weights) or [G,N,K]. */
+typedef enum { MOE_WEIGHT_KN = 0, MOE_WEIGHT_NK = 1 } moe_weight_layout;
+
+typedef struct {
+    const void* bias;            /* [G,N], or null */
+    moe_dtype bias_dtype;        /* fp32, or the operands' type */
+    moe_activation activation;
+    const void* residual;        /* [R,N] of the output's type, or null; may be the output's memory with its stride */
+    int64_t residual_stride;     /* elements from row to row */
+} moe_epilogue;
+
+/* Bytes of moe_linear's workspace, for any sizes. Its first MOE_LINEAR_WORKSPACE_ZEROS
+ * bytes have to be zero before its first use, and again after moe_check has returned
+ * MOE_ERR_TIMEOUT for it; the calls leave them as the next call needs them. Two calls
+ * that share a workspace must not overlap. */
+#define MOE_LINEAR_WORKSPACE_ZEROS 256
+size_t moe_linear_workspace_size(void);
+
+/*
+ * Grouped product: out[p,:] = act(a[p,:] w[g] + bias[g]) + residual[p,:] for the rows
+ * p of group g, offsets[g] <= p < offsets[g+1] (offsets null = one group of R
+ * rows; G is then 1). Sums, bias, activation and residual in fp32, rounded once.
+ * Rows outside [offsets[0], offsets[G]) are not written. Offsets that decrease or
+ * leave [0, R] set MOE_ERR_DEVICE_BOUNDS in the device error word and nothing is
+ * computed.
+ * In:  a[R,K] of type dtype (bf16 or fp16), rows a_stride elements apart;
+ *      offsets[G+1] (device); w of type dtype; epilogue (nullable).
+ * Out: out[R,N] of type out_dtype (dtype or fp32), rows out_stride apart; its memory
+ *      may be the residual's, and no other input's.
+ * K and N multiples of 8, G <= 256; a and w 16-byte aligned, a_stride a multiple of 8,
+ * the others aligned to their type.
+ */
+moe_status moe_linear(int64_t R, int32_t K, int32_t N, int32_t G, moe_dtype dtype, const void* a, int64_t a_stride,
+                      const int32_t* offsets, const void* w, moe_weight_layout layout, const moe_epilogue* epilogue,
+                      moe_dtype out_dtype, void* out, int64_t out_stride, void* ws, size_t ws_bytes,
+                      moe_stream_t stream);
+
+/*
+ * The weighted sum of experts' rows, back in token order:
+ *   out[t,:] = sum over ranks j (in order) of topk_w[t,j] y[inv_pos[t,j],:]
+ *              + residual[t,:], in fp32, rounded once.
+ * A rank whose inv_pos lies outside [0, R) (a dropped assignment: -1) adds nothing.
+ * In:  y[R,H] of type dtype; inv_pos[T,k] (moe_permute's), topk_w[T,k]; residual[T,H]
+ *      of type out_dtype (nullable; may be the output's memory with its stride).
+ * Out: out[T,H] of type out_dtype.
+ * 1 <= k <= 8; H a multiple of 8; y, residual and out 16-byte aligned with rows of
+ * multiples of 16 bytes, their strides in elements.
+ */
+moe_status moe_combine_rows(int64_t T, int32_t H, int32_t k, int64_t R, moe_dtype dtype, const void* y,
+                            int64_t y_stride, const int32_t* inv_pos, const float* topk_w, moe_dtype out_dtype,
+                            const void* residual, int64_t residual_stride, void* out, int64_t out_stride,
+                            moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,145 @@
+// api_ops.cu -- the C ABI of moe_route_logits, moe_linear and moe_combine_rows
+// (include/moe.h): argument checks, TMA descriptors and launches. Host code only.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/moe.h"
+#include "api.h"
+#include "kernels.cuh"
+#include "ops.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int32_t kMaxTopK = 8;
+constexpr int32_t kMaxExperts = 256;
+constexpr int32_t kMaxGroupsOfExperts = 32;
+
+static_assert(kLinearWorkspaceBytes >= MOE_LINEAR_WORKSPACE_ZEROS, "the zeros lie in the workspace");
+
+bool is_dtype(moe_dtype t) { return t == MOE_BF16 || t == MOE_FP16 || t == MOE_FP32; }
+int size_of(moe_dtype t) { return t == MOE_FP32 ? 4 : 2; }
+bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_route_logits(int64_t T, int32_t E, int32_t k, moe_dtype dtype, const void* logits, int64_t stride,
+                            const moe_scoring* scoring, int32_t* topk_idx, float* topk_w, moe_stream_t stream)
+{
+    const moe_scoring plain{MOE_SCORES_SOFTMAX, nullptr, 1, 1, 1, 0, 1.0f};
+    const moe_scoring& c = scoring ? *scoring : plain;
+    if (T < 0 || E <= 0 || k <= 0 || k > E) return MOE_ERR_INVALID_ARG;
+    if (c.scores != MOE_SCORES_SOFTMAX && c.scores != MOE_SCORES_SIGMOID) return MOE_ERR_INVALID_ARG;
+    if (c.groups <= 0 || E % c.groups || c.top_groups <= 0 || c.top_groups > c.groups) return MOE_ERR_INVALID_ARG;
+    if ((c.group_top != 1 && c.group_top != 2) || c.group_top > E / c.groups) return MOE_ERR_INVALID_ARG;
+    if (k > c.top_groups * (E / c.groups) || !std::isfinite(c.scale)) return MOE_ERR_INVALID_ARG;
+    if (!is_dtype(dtype) || k > kMaxTopK || E > kMaxExperts || c.groups > kMaxGroupsOfExperts) return MOE_ERR_UNSUPPORTED;
+    if (T >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if (!logits || !topk_idx || !topk_w || (T > 1 && stride < E)) return MOE_ERR_INVALID_ARG;
+    if (!aligned_to(logits, size_of(dtype)) || !aligned_to(c.bias, 4) || !aligned_to(topk_idx, 4) ||
+        !aligned_to(topk_w, 4))
+        return MOE_ERR_INVALID_ARG;
+    const int sms = num_sms_current();
+    if (sms <= 0) return MOE_ERR_CUDA;
+    Range range("moe/route_logits");
+    const RouteLogitsArgs a{logits, stride, c.bias, topk_idx, topk_w, T, E, k, c.scores == MOE_SCORES_SIGMOID,
+                            c.groups, c.top_groups, c.group_top, c.renormalize != 0, c.scale};
+    return finish(launch_route_logits(dtype, a, sms, (cudaStream_t)stream), nullptr, (cudaStream_t)stream);
+}
+
+size_t moe_linear_workspace_size(void) { return kLinearWorkspaceBytes; }
+
+moe_status moe_linear(int64_t R, int32_t K, int32_t N, int32_t G, moe_dtype dtype, const void* a, int64_t a_stride,
+                      const int32_t* offsets, const void* w, moe_weight_layout layout, const moe_epilogue* epilogue,
+                      moe_dtype out_dtype, void* out, int64_t out_stride, void* ws, size_t ws_bytes,
+                      moe_stream_t stream)
+{
+    const moe_epilogue plain{nullptr, MOE_FP32, MOE_ACT_NONE, nullptr, 0};
+    const moe_epilogue& e = epilogue ? *epilogue : plain;
+    if (R < 0 || K <= 0 || N <= 0 || G <= 0 || (!offsets && G != 1)) return MOE_ERR_INVALID_ARG;
+    if (layout != MOE_WEIGHT_KN && layout != MOE_WEIGHT_NK) return MOE_ERR_INVALID_ARG;
+    if (e.activation < MOE_ACT_NONE || e.activation > MOE_ACT_GELU_TANH) return MOE_ERR_INVALID_ARG;
+    if (dtype != MOE_BF16 && dtype != MOE_FP16) return MOE_ERR_UNSUPPORTED;
+    if (out_dtype != dtype && out_dtype != MOE_FP32) return MOE_ERR_UNSUPPORTED;
+    if (e.bias && e.bias_dtype != dtype && e.bias_dtype != MOE_FP32) return MOE_ERR_UNSUPPORTED;
+    if (K % 8 || N % 8 || G > kMaxExperts || R >= ((int64_t)1 << 31) - 256) return MOE_ERR_UNSUPPORTED;
+    // tiles, and a round of them more, are counted in 32 bits
+    if ((R / 128 + G) * (((int64_t)N + 127) / 128) >= ((int64_t)1 << 31) - (1 << 16)) return MOE_ERR_UNSUPPORTED;
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < kLinearWorkspaceBytes) return MOE_ERR_WORKSPACE;
+    if (R == 0) return MOE_OK;
+    if (!a || !w || !out || !aligned16(a) || !aligned16(w)) return MOE_ERR_INVALID_ARG;
+    if (R > 1 && (a_stride < K || a_stride % 8 || out_stride < N || (e.residual && e.residual_stride < N)))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned_to(out, size_of(out_dtype)) || !aligned_to(e.residual, size_of(out_dtype)) ||
+        (e.bias && !aligned_to(e.bias, size_of(e.bias_dtype))) || !aligned_to(offsets, 4))
+        return MOE_ERR_INVALID_ARG;
+    const int sms = num_sms_current();
+    if (sms <= 0) return MOE_ERR_CUDA;
+    Range range("moe/linear");
+    if (R == 1) a_stride = K;
+    const bool nk = layout == MOE_WEIGHT_NK;
+    const uint64_t a_dims[] = {(uint64_t)K, (uint64_t)R}, a_strides[] = {(uint64_t)a_stride * 2};
+    const uint32_t large[] = {kLinearBK, kLinearRowBox}, small[] = {kLinearBK, kLinearRowBoxSmall};
+    const uint64_t inner = nk ? K : N, outer = nk ? N : K;
+    const uint64_t w_dims[] = {inner, outer, (uint64_t)G}, w_strides[] = {inner * 2, inner * outer * 2};
+    const uint32_t w_box[] = {64, nk ? 128u : 64u, 1};
+    CUtensorMap tm_a, tm_a_small, tm_w;
+    if (!encode_map_b16(&tm_a, a, 2, a_dims, a_strides, large) || !encode_map_b16(&tm_a_small, a, 2, a_dims, a_strides, small) ||
+        !encode_map_b16(&tm_w, w, 3, w_dims, w_strides, w_box))
+        return MOE_ERR_CUDA;
+    LinearArgs args{};
+    args.R = (int32_t)R;
+    args.N = N;
+    args.K = K;
+    args.G = G;
+    args.offsets = offsets;
+    args.bias = e.bias;
+    args.bias_f32 = e.bias_dtype == MOE_FP32;
+    args.act = e.activation;
+    args.residual = e.residual;
+    args.residual_stride = e.residual_stride;
+    args.out = out;
+    args.out_stride = out_stride;
+    args.fp16 = dtype == MOE_FP16;
+    args.w_nk = nk;
+    args.err = static_cast<uint32_t*>(ws);
+    return finish(launch_linear(out_dtype, tm_a, tm_a_small, tm_w, args, sms, (cudaStream_t)stream), ws,
+                  (cudaStream_t)stream);
+}
+
+moe_status moe_combine_rows(int64_t T, int32_t H, int32_t k, int64_t R, moe_dtype dtype, const void* y,
+                            int64_t y_stride, const int32_t* inv_pos, const float* topk_w, moe_dtype out_dtype,
+                            const void* residual, int64_t residual_stride, void* out, int64_t out_stride,
+                            moe_stream_t stream)
+{
+    if (T < 0 || H <= 0 || k <= 0 || R < 0) return MOE_ERR_INVALID_ARG;
+    if (!is_dtype(dtype) || !is_dtype(out_dtype) || H % 8 || k > kMaxTopK || T >= ((int64_t)1 << 31))
+        return MOE_ERR_UNSUPPORTED;
+    // assignments, rows and blocks are counted in 32 bits
+    if (T * k >= ((int64_t)1 << 31) || R >= ((int64_t)1 << 31) || T * ((H + 1023) / 1024) >= ((int64_t)1 << 31))
+        return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if ((R > 0 && !y) || !inv_pos || !topk_w || !out) return MOE_ERR_INVALID_ARG;
+    if (!aligned_to(inv_pos, 4) || !aligned_to(topk_w, 4)) return MOE_ERR_INVALID_ARG;
+    const struct { const void* p; int64_t rows, stride; moe_dtype type; } parts[] = {
+        {y, R, y_stride, dtype}, {residual, T, residual_stride, out_dtype}, {out, T, out_stride, out_dtype}};
+    for (const auto& p : parts)
+        if (p.p && (!aligned16(p.p) || (p.rows > 1 && (p.stride < H || p.stride * size_of(p.type) % 16))))
+            return MOE_ERR_INVALID_ARG;
+    const int sms = num_sms_current();
+    if (sms <= 0) return MOE_ERR_CUDA;
+    Range range("moe/combine_rows");
+    const CombineRowsArgs a{y, inv_pos, topk_w, residual, out, T, R, y_stride, residual_stride, out_stride, H, k};
+    return finish(launch_combine_rows(dtype, out_dtype, a, sms, (cudaStream_t)stream), nullptr, (cudaStream_t)stream);
+}
+
+}  // extern "C"

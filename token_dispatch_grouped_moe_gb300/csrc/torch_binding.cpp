@@ -1,4 +1,5 @@
-// torch_binding.cpp -- the Python calls of the 8-bit operators: argument checks,
+// torch_binding.cpp -- the Python calls of the 8-bit operators, of routing from
+// logits, the product with an epilogue and the sum of experts' rows: argument checks,
 // the outputs' allocation and the C ABI call (include/moe.h), in C++.
 //
 // These operators take a few microseconds on the GPU at decode sizes, less than
@@ -256,6 +257,140 @@ PyObject* fp8_gated(PyObject* const* a)
     return tuple_of({h, scale});
 }
 
+// The moe_dtype of a tensor's type.
+moe_dtype code_of(const char* name, const Tensor& t, bool with_f32 = true)
+{
+    switch (t.scalar_type()) {
+    case at::kBFloat16: return MOE_BF16;
+    case at::kHalf: return MOE_FP16;
+    case at::kFloat:
+        if (with_f32) return MOE_FP32;
+        [[fallthrough]];
+    default: refuse(name, t, with_f32 ? "a bf16, fp16 or fp32 tensor" : "a bf16 or fp16 tensor");
+    }
+}
+
+int64_t integer(PyObject* o)
+{
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) throw BadArgument("expected whole numbers");
+    return v;
+}
+
+int32_t small_integer(PyObject* o, const char* name)
+{
+    const int64_t v = integer(o);
+    if (v < INT32_MIN || v > INT32_MAX) throw BadArgument(std::string(name) + ": out of range");
+    return (int32_t)v;
+}
+
+// route_logits(logits, k, sigmoid, bias, groups, top_groups, group_top, renormalize, scale, topk_idx, topk_w, stream)
+PyObject* route_logits(PyObject* const* a)
+{
+    const Tensor& logits = tensor_of(a[0], "logits");
+    const std::optional<Tensor> bias = optional_of(a[3], "bias");
+    std::optional<Tensor> idx = optional_of(a[9], "topk_idx"), w = optional_of(a[10], "topk_w");
+    const int32_t k = small_integer(a[1], "k");
+    const int sigmoid = PyObject_IsTrue(a[2]), renorm = PyObject_IsTrue(a[7]);
+    const double scale = PyFloat_AsDouble(a[8]);
+    moe_scoring c{};
+    c.groups = small_integer(a[4], "groups");
+    c.top_groups = small_integer(a[5], "top_groups");
+    c.group_top = small_integer(a[6], "group_top");
+    if (PyErr_Occurred()) return nullptr;
+    c.scores = sigmoid ? MOE_SCORES_SIGMOID : MOE_SCORES_SOFTMAX;
+    c.renormalize = renorm;
+    c.scale = (float)scale;
+    const int64_t T = dim(logits, "logits", 0, 2), E = logits.size(1);
+    const moe_dtype code = code_of("logits", logits);
+    const at::Device dev = logits.device();
+    expect_rows("logits", logits, logits.scalar_type(), T, E, dev);
+    if (bias) expect("bias", *bias, at::kFloat, {E}, dev);
+    if (idx) expect("topk_idx", *idx, at::kInt, {T, k}, dev);
+    if (w) expect("topk_w", *w, at::kFloat, {T, k}, dev);
+    if (k <= 0) return failed(MOE_ERR_INVALID_ARG);
+    if (E > INT32_MAX || k > E) return failed(E > INT32_MAX ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG);
+    const Launch launch(dev, a[11]);
+    if (!idx) idx = empty({T, k}, at::kInt, dev);
+    if (!w) w = empty({T, k}, at::kFloat, dev);
+    c.bias = static_cast<const float*>(ptr(bias));
+    const moe_status s = moe_route_logits(T, (int32_t)E, k, code, logits.data_ptr(), logits.stride(0), &c,
+                                          static_cast<int32_t*>(idx->data_ptr()), static_cast<float*>(w->data_ptr()),
+                                          launch.stream);
+    if (s != MOE_OK) return failed(s);
+    return tuple_of({idx, w});
+}
+
+// linear(a, w, ws, bias, activation, residual, offsets, f32, out, stream)
+PyObject* linear(PyObject* const* a)
+{
+    const Tensor &A = tensor_of(a[0], "a"), &w = tensor_of(a[1], "w"), &ws = tensor_of(a[2], "ws");
+    const std::optional<Tensor> bias = optional_of(a[3], "bias"), residual = optional_of(a[5], "residual"),
+                                offsets = optional_of(a[6], "offsets");
+    std::optional<Tensor> out = optional_of(a[8], "out");
+    moe_epilogue e{};
+    e.activation = (moe_activation)small_integer(a[4], "activation");
+    const int f32 = PyObject_IsTrue(a[7]);
+    if (f32 < 0) return nullptr;
+    const int64_t R = dim(A, "a", 0, 2), K = A.size(1), N = dim(w, "w", 2, 3), G = w.size(0);
+    const moe_dtype code = code_of("a", A, false);
+    const at::ScalarType type = A.scalar_type(), out_type = f32 ? at::kFloat : type;
+    const at::Device dev = A.device();
+    expect_rows("a", A, type, R, K, dev);
+    // [G, K, N] with contiguous n, or the view of [G, N, K] with contiguous k
+    const bool kn = w.is_contiguous(), nk = !kn && w.transpose(1, 2).is_contiguous();
+    if (w.scalar_type() != type || !is_size(w, {G, K, N}) || w.device() != dev || !(kn || nk))
+        refuse("w", w, described("(contiguous, or the transpose of a contiguous) a", type, {G, K, N}, dev));
+    if (bias) expect("bias", *bias, bias->scalar_type() == at::kFloat ? at::kFloat : type, {G, N}, dev);
+    if (residual) expect_rows("residual", *residual, out_type, R, N, dev);
+    if (offsets) expect("offsets", *offsets, at::kInt, {G + 1}, dev);
+    if (out) expect_rows("out", *out, out_type, R, N, dev);
+    if (ws.scalar_type() != at::kByte || ws.device() != dev || !ws.is_contiguous())
+        refuse("ws", ws, "a contiguous uint8 tensor on the same device");
+    if (K > INT32_MAX || N > INT32_MAX || G > INT32_MAX) return failed(MOE_ERR_UNSUPPORTED);
+    const Launch launch(dev, a[9]);
+    if (!out) out = empty({R, N}, out_type, dev);
+    e.bias = ptr(bias);
+    e.bias_dtype = bias && bias->scalar_type() != at::kFloat ? code : MOE_FP32;
+    e.residual = ptr(residual);
+    e.residual_stride = residual ? residual->stride(0) : 0;
+    const moe_status s = moe_linear(R, (int32_t)K, (int32_t)N, (int32_t)G, code, A.data_ptr(), A.stride(0),
+                                    static_cast<const int32_t*>(ptr(offsets)), w.data_ptr(),
+                                    nk ? MOE_WEIGHT_NK : MOE_WEIGHT_KN, &e, f32 ? MOE_FP32 : code, out->data_ptr(),
+                                    out->stride(0), ws.data_ptr(), (size_t)ws.numel(), launch.stream);
+    if (s != MOE_OK) return failed(s);
+    return wrap(out);
+}
+
+// combine_rows(y, inv_pos, topk_w, residual, out_dtype's code, out, stream)
+PyObject* combine_rows(PyObject* const* a)
+{
+    const Tensor &y = tensor_of(a[0], "y"), &inv = tensor_of(a[1], "inv_pos"), &w = tensor_of(a[2], "topk_w");
+    const std::optional<Tensor> residual = optional_of(a[3], "residual");
+    std::optional<Tensor> out = optional_of(a[5], "out");
+    const int32_t out_code = small_integer(a[4], "out_dtype");
+    const int64_t R = dim(y, "y", 0, 2), H = y.size(1), T = dim(w, "topk_w", 0, 2), k = w.size(1);
+    const moe_dtype code = code_of("y", y), oc = out_code < 0 ? code : (moe_dtype)out_code;
+    const at::ScalarType type = y.scalar_type();
+    const at::ScalarType out_type = oc == MOE_BF16 ? at::kBFloat16 : oc == MOE_FP16 ? at::kHalf : at::kFloat;
+    const at::Device dev = y.device();
+    expect_rows("y", y, type, R, H, dev);
+    expect("topk_w", w, at::kFloat, {T, k}, dev);
+    if (inv.scalar_type() != at::kInt || inv.numel() != T * k || inv.device() != dev || !inv.is_contiguous())
+        refuse("inv_pos", inv, described("T * k values in a contiguous", at::kInt, {T, k}, dev));
+    if (residual) expect_rows("residual", *residual, out_type, T, H, dev);
+    if (out) expect_rows("out", *out, out_type, T, H, dev);
+    if (H > INT32_MAX || k > INT32_MAX) return failed(MOE_ERR_UNSUPPORTED);
+    const Launch launch(dev, a[6]);
+    if (!out) out = empty({T, H}, out_type, dev);
+    const moe_status s = moe_combine_rows(T, (int32_t)H, (int32_t)k, R, code, y.data_ptr(), y.stride(0),
+                                          static_cast<const int32_t*>(inv.data_ptr()), f32(w), oc, ptr(residual),
+                                          residual ? residual->stride(0) : 0, out->data_ptr(), out->stride(0),
+                                          launch.stream);
+    if (s != MOE_OK) return failed(s);
+    return wrap(out);
+}
+
 // A method of N positional arguments: C++ exceptions become Python's.
 template <int N, PyObject* (*F)(PyObject* const*)>
 PyObject* method(PyObject*, PyObject* const* args, Py_ssize_t n)
@@ -280,6 +415,9 @@ PyObject* method(PyObject*, PyObject* const* args, Py_ssize_t n)
 PyMethodDef methods[] = {{"add_rmsnorm_fp8", FAST(7, add_rmsnorm_fp8)},
                          {"fp8_matmul", FAST(9, fp8_matmul)},
                          {"fp8_gated", FAST(9, fp8_gated)},
+                         {"route_logits", FAST(12, route_logits)},
+                         {"linear", FAST(10, linear)},
+                         {"combine_rows", FAST(7, combine_rows)},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -28,7 +28,7 @@ EXPORTS = ["moe_version", "moe_status_string", "moe_workspace_size", "moe_check"
            "moe_layer_plan", "moe_selftest_wait_timeout", "moe_launch_count", "moe_selftest_route_tc",
            "moe_layer_forward_host", "moe_host_chunks", "moe_fp8_workspace_size", "moe_add_rmsnorm_fp8",
            "moe_fp8_quantize_weight", "moe_fp8_matmul", "moe_fp8_gated", "moe_fp8_layer_forward",
-           "moe_selftest_fp8_form"]
+           "moe_selftest_fp8_form", "moe_route_logits", "moe_linear_workspace_size", "moe_linear", "moe_combine_rows"]
 
 OPT_GEMM0_A = 0
 GEMM0_A_PERMUTED = 0      # dispatch copies token rows to x_perm; GEMM0 loads dense tiles
@@ -86,6 +86,17 @@ class Plan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("router", "gemm0_a", "combine", "gemm_fusion", "tile_m",
                                               "tile_n", "tile_k", "stages", "cta_group",
                                               "cta_group_gemm1", "x_perm_copy")]
+
+
+class Scoring(ctypes.Structure):
+    _fields_ = [("scores", ctypes.c_int32), ("bias", ctypes.c_void_p), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class Epilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("bias_dtype", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64)]
 
 
 class Fp8Ffn(ctypes.Structure):
@@ -168,6 +179,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_fp8_layer_forward.restype = ctypes.c_int
     lib.moe_fp8_layer_forward.argtypes = [D, P, P, P, P, P, ctypes.POINTER(Gating), ctypes.POINTER(Fp8Ffn),
                                           ctypes.POINTER(Fp8Ffn), P, ctypes.POINTER(RoutingOut), P, sz, P]
+    lib.moe_route_logits.restype = ctypes.c_int
+    lib.moe_route_logits.argtypes = [i64, i32, i32, i32, P, i64, ctypes.POINTER(Scoring), P, P, P]
+    lib.moe_linear_workspace_size.restype = sz
+    lib.moe_linear_workspace_size.argtypes = []
+    lib.moe_linear.restype = ctypes.c_int
+    lib.moe_linear.argtypes = [i64, i32, i32, i32, i32, P, i64, P, P, i32, ctypes.POINTER(Epilogue), i32, P, i64, P, sz, P]
+    lib.moe_combine_rows.restype = ctypes.c_int
+    lib.moe_combine_rows.argtypes = [i64, i32, i32, i64, i32, P, i64, P, P, i32, P, i64, P, i64, P]
     _lib = lib
     return lib
 
@@ -522,7 +541,8 @@ def _expect(t, name, shape, dtype, device):
                          f"{t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
 
 
-# The calls below whose kernels take microseconds (the norm and the products)
+# The calls whose kernels take microseconds (the norm, the products, and the three
+# of the last section)
 # check their arguments, allocate and launch in C++ (csrc/torch_binding.cpp).
 _binding = None
 
@@ -709,3 +729,75 @@ class MoEFp8Layer(_Layer):
         out = fp8_layer_forward(self.dims(T), y, q, scale, self.Wg, self.routed, self.workspace(T, stream),
                                 bias=self.bias, shared=self.shared, routing=routing, stream=stream)
         return out, x if residual is None else r
+
+
+# ------------------------------- routing from logits, products with an epilogue --
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # moe_dtype
+SCORES = {"softmax": 0, "sigmoid": 1}                               # moe_scores
+ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}   # moe_activation
+LINEAR_WORKSPACE_ZEROS = 256   # bytes of a workspace that have to be zero before its first use
+
+
+def _one_of(value, table, name):
+    try:
+        return table[value]
+    except (KeyError, TypeError):
+        raise ValueError(f"{name}: one of {', '.join(map(str, table))} expected, got {value!r}") from None
+
+
+def route_logits(logits, k, scores="softmax", bias=None, groups=1, top_groups=1, group_top=1, renormalize=False,
+                 scale=1.0, topk_idx=None, topk_w=None, stream=None):
+    """Each token's k experts and weights from its logits [T,E] (bf16, fp16 or
+    fp32; any row stride from E on): (topk_idx [T,k] int32, topk_w [T,k] fp32).
+
+    s = softmax(logits) or sigmoid(logits) by ``scores``; the experts are those of
+    the largest s + bias (``bias`` [E] fp32, of the selection only), descending,
+    ties to the lower index. With ``groups`` > 1 only the experts of the
+    ``top_groups`` groups (of E / groups neighbours) of the largest value are
+    selected: a group's value is its largest s + bias, or with ``group_top=2`` the sum
+    of its two largest. The weights are s of the selected, divided by their sum
+    with ``renormalize``, times ``scale``. A logit of -inf is an expert with score 0; a NaN
+    makes its row's weights NaN."""
+    r = (_binding or _load_binding()).route_logits(logits, k, _one_of(scores, SCORES, "scores"), bias, groups,
+                                                   top_groups, group_top, renormalize, scale, topk_idx, topk_w,
+                                                   _handle(stream, logits))
+    if type(r) is int:
+        raise MoeError(r, "moe_route_logits")
+    return r
+
+
+def linear_workspace(device=None) -> torch.Tensor:
+    """A workspace of :func:`linear` (any sizes), zeros where the calls need them."""
+    return _zero_headed(int(load().moe_linear_workspace_size()), LINEAR_WORKSPACE_ZEROS, device)
+
+
+def linear(a, w, ws, bias=None, activation=None, residual=None, offsets=None, out_dtype=None, out=None, stream=None):
+    """out[p] = act(a[p] w[g] + bias[g]) + residual[p] for the rows p of group g,
+    offsets[g] <= p < offsets[g+1] (one group without offsets): a [R,K] in bf16 or
+    fp16 (any row stride that is a multiple of 8), w [G,K,N] of its type, contiguous
+    or the transpose of a contiguous [G,N,K]; bias [G,N] in fp32 or a's type;
+    ``activation`` None, "relu", "silu", "gelu" or "gelu_tanh"; out and residual [R,N]
+    (any row stride from N on) in a's type or, with ``out_dtype``, fp32. ``out`` may be
+    the residual's memory. Rows outside every group are not written."""
+    f32 = out_dtype is torch.float32
+    if not f32 and out_dtype is not None and out_dtype is not a.dtype:
+        raise ValueError(f"out_dtype: {a.dtype} or fp32 expected, got {out_dtype}")
+    r = (_binding or _load_binding()).linear(a, w, ws, bias, _one_of(activation, ACTIVATIONS, "activation"), residual,
+                                             offsets, f32, out, _handle(stream, a))
+    if type(r) is int:
+        raise MoeError(r, "moe_linear")
+    return r
+
+
+def combine_rows(y, inv_pos, topk_w, residual=None, out_dtype=None, out=None, stream=None):
+    """out[t] = sum_j topk_w[t,j] y[inv_pos[t,j]] + residual[t], ranks in order, in
+    fp32: the experts' rows y [R,H] (bf16, fp16 or fp32, any row stride of
+    multiples of 16 bytes) back in token order. inv_pos (T * k int32, as of
+    :func:`permute`) outside [0, R) adds nothing; out and residual [T,H] are of
+    ``out_dtype`` (y's by default), and may be the same memory."""
+    code = -1 if out_dtype is None else _one_of(out_dtype, DTYPES, "out_dtype")
+    r = (_binding or _load_binding()).combine_rows(y, inv_pos, topk_w, residual, code, out, _handle(stream, y))
+    if type(r) is int:
+        raise MoeError(r, "moe_combine_rows")
+    return r
