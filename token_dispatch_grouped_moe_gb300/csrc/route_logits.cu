@@ -68,11 +68,20 @@ __device__ __forceinline__ float rcp(float x)
     return r;
 }
 
+// The warp's largest value (a NaN gives way).
+__device__ __forceinline__ float max_f32(float v)
+{
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
 // e^x within 2^-22 + 2^-23 of itself (0 below 2^-126, inf above the range): ex2's
 // 2^-22, the product's rounding made good by its residual
 __device__ __forceinline__ float exp_near(float x)
 {
-    constexpr float kLog2e = 1.44269504088896340736f;
     constexpr float kLog2eLow = 1.925963033500e-8f;   // log2(e) - kLog2e
     constexpr float kLn2 = 0.69314718055994530942f;
     x = fminf(fmaxf(x, -120.0f), 120.0f);
@@ -80,6 +89,16 @@ __device__ __forceinline__ float exp_near(float x)
     const float r = fmaf(x, kLog2e, -n) + x * kLog2eLow;
     return ex2(n) * fmaf(r, kLn2, 1.0f);
 }
+
+__device__ __forceinline__ float sigmoid_near(float x) { return rcp(1.0f + exp_near(-x)); }
+
+// How far a score in fp32 may be from itself, absolutely. Sigmoid: s (1 - s) times
+// e^-x's error (2^-22, and of a plain product with log2(e) 2 |x| 2^-24, where |x| s
+// (1 - s) < 1/4), a sum and a reciprocal: 4.5 * 2^-24. Softmax, in the largest
+// score: e^d within (4 + 3 |d|) 2^-24, the sum of up to 256 within (20.5 + 21) 2^-24
+// (16 in a lane, 5 steps), a reciprocal and a product: 49 * 2^-24 for every d.
+constexpr float kSigmoidTol = 5.0f * 0x1p-24f;
+constexpr float kSoftmaxTol = 26.0f * 0x1p-23f;
 
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -299,76 +318,371 @@ __device__ __noinline__ void exact_row(const RouteLogitsArgs& a, int64_t t, int 
     store_row(a, t, lane, id, nan ? __int_as_float(0x7fc00000) : (float)w);
 }
 
+// A row with every expert's key kept, in fp32 with the bounds above, and in fp64
+// where they do not decide: rows that the short way below does not take.
 template <int V, typename T>
-__global__ void __launch_bounds__(32 * kWarps) route_logits_kernel(const RouteLogitsArgs a)
+__device__ __noinline__ void careful_row(const RouteLogitsArgs& a, int64_t t, int lane, float b_most)
 {
-    pdl_wait();
-    pdl_launch_dependents();
-    const int lane = threadIdx.x & 31;
     const Place<V> p(a, lane);
-    float b[V];
+    float l[V], b[V], s[V];
+    load_row<V, T>(a, t, p, l);
     load_bias<V>(a, p, b);
-    float b_most = 0.0f;   // the largest finite |bias|
+    bool bad = false;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-        if (fabsf(b[j]) < __builtin_huge_valf()) b_most = fmaxf(b_most, fabsf(b[j]));
-    b_most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(b_most)));
+    for (int j = 0; j < V; ++j) bad = bad || !(l[j] < __builtin_huge_valf());
+    float s_most, tol;
+    if (a.sigmoid) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j] = sigmoid_near(l[j]);
+        s_most = 1.0f;
+        tol = kSigmoidTol;
+    } else {
+        float m = row_max<V>(l);
+        if (m == kNegInf) m = 0.0f;
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            s[j] = exp_near(l[j] - m);
+            sum += s[j];
+        }
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+        const float inv = sum > 0.0f ? rcp(sum) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j] *= inv;
+        s_most = inv;
+        tol = kSoftmaxTol * inv;
+    }
+    tol += 0x1p-24f * (s_most + b_most) + 0x1p-90f;
+    int id = 0;
+    float score = 0.0f, logit = 0.0f;
+    bool again = order_row<V, float>(a, p, lane, l, b, s, tol, id, score, logit) || __any_sync(kAll, bad);
+    float w = lane < a.k ? score : 0.0f;
+    if (a.renorm) {
+        again = again || __any_sync(kAll, lane < a.k && score < kTiny && logit > kNegInf);
+        float sum = w;
+        for (int d = 4; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+        w = sum > 0.0f ? __fdividef(w, sum) : 0.0f;
+    }
+    if (again) exact_row<V, T>(a, t, lane);
+    else store_row(a, t, lane, id, w * a.scale);
+}
 
-    for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.T; t += (int64_t)gridDim.x * kWarps) {
-        float l[V], s[V];
-        load_row<V, T>(a, t, p, l);
-        bool bad = false;
+// 16 bytes, or all of them, of a lane's logits at a time
+template <int V, typename T>
+__device__ __forceinline__ void load_whole(const T* p, float (&l)[V])
+{
+    constexpr int BYTES = V * (int)sizeof(T) < 16 ? V * (int)sizeof(T) : 16;
+    constexpr int N = BYTES / (int)sizeof(T);
 #pragma unroll
-        for (int j = 0; j < V; ++j) bad = bad || !(l[j] < __builtin_huge_valf());
-        float s_most, tol;
-        if (a.sigmoid) {
-            // 1 + e and the reciprocal: within 2.25 * 2^-22 of the score
+    for (int j = 0; j < V; j += N) {
+        alignas(16) T v[N];
+        if constexpr (BYTES == 16) *reinterpret_cast<uint4*>(v) = __ldg(reinterpret_cast<const uint4*>(p + j));
+        else if constexpr (BYTES == 8) *reinterpret_cast<uint2*>(v) = __ldg(reinterpret_cast<const uint2*>(p + j));
+        else if constexpr (BYTES == 4) *reinterpret_cast<uint32_t*>(v) = __ldg(reinterpret_cast<const uint32_t*>(p + j));
+        else v[0] = p[j];
 #pragma unroll
-            for (int j = 0; j < V; ++j) s[j] = rcp(1.0f + exp_near(-l[j]));
-            s_most = 1.0f;
-            tol = 2.5f * 0x1p-22f;
-        } else {
-            // e^d within (|d| / 2 + 3) 2^-23 of itself (d's own rounding), the sum of
-            // up to 256 (lane by lane, then 5 steps) within 17 * 2^-23: together less
-            // than 24 * 2^-23 of the largest score, for every expert
-            float m = row_max<V>(l);
-            if (m == kNegInf) m = 0.0f;
-            float sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                s[j] = exp_near(l[j] - m);
-                sum += s[j];
-            }
-            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
-            const float inv = sum > 0.0f ? rcp(sum) : 0.0f;
-#pragma unroll
-            for (int j = 0; j < V; ++j) s[j] *= inv;
-            s_most = inv;
-            tol = 24.0f * 0x1p-23f * inv;
-        }
-        tol += 0x1p-24f * (s_most + b_most) + 0x1p-90f;
-        int id = 0;
-        float score = 0.0f, logit = 0.0f;
-        bool again = order_row<V, float>(a, p, lane, l, b, s, tol, id, score, logit) || __any_sync(kAll, bad);
-        float w = lane < a.k ? score : 0.0f;
-        if (a.renorm) {
-            again = again || __any_sync(kAll, lane < a.k && score < kTiny && logit > kNegInf);
-            float sum = w;
-            for (int d = 4; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
-            w = sum > 0.0f ? __fdividef(w, sum) : 0.0f;
-        }
-        if (again) exact_row<V, T>(a, t, lane);
-        else store_row(a, t, lane, id, w * a.scale);
+        for (int i = 0; i < N; ++i) l[j + i] = to_float(v[i]);
     }
 }
 
+// The two largest of two pairs, each ordered.
+__device__ __forceinline__ void merge_two(float& x, float& y, float ox, float oy)
+{
+    const float lo = fminf(x, ox);
+    x = fmaxf(x, ox);
+    y = fmaxf(fmaxf(y, oy), lo);
+}
+
+// The sum of e^(l - m) over a row in fp64 (rolled up: this code is cold, and what
+// it costs is its fetching).
 template <int V, typename T>
+__device__ __noinline__ double sum64(const T* row, int first, int n, float m)
+{
+    double sum = 0.0;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) sum += exp((double)to_float(row[first + j]) - (double)m);
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+    return sum;
+}
+
+__device__ __noinline__ double score64(float l, int sigmoid, float m, double sum)
+{
+    return sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)m) / sum;
+}
+
+// Which groups are kept, by values in fp64: lane i < total has the score + bias
+// `key` of an expert of `group`, the lanes together all that may be among a group's
+// one (or two) largest. A bit a group.
+__device__ __noinline__ unsigned settle_groups(const RouteLogitsArgs& a, int lane, int total, int group, double key)
+{
+    double x = -__builtin_huge_val(), y = x;   // lane g: the two largest of group g
+#pragma unroll 1
+    for (int i = 0; i < total; ++i) {
+        const double k = __shfl_sync(kAll, key, i);
+        const int g = __shfl_sync(kAll, group, i);
+        if (g != lane) continue;
+        if (k > x) { y = x; x = k; }
+        else if (k > y) y = k;
+    }
+    const double value = a.group_top == 2 ? x + y : x;
+    int place = 0;
+#pragma unroll 1
+    for (int g = 0; g < a.groups; ++g) {
+        const double v = __shfl_sync(kAll, value, g);
+        place += v > value || (v == value && g < lane);
+    }
+    return __ballot_sync(kAll, lane < a.groups && place < a.top_groups);
+}
+
+// Lists the experts of the lanes with `mine` whose v is at least `least` in `list`, in
+// index order; how many there are (over 32: none is listed).
+template <int V>
+__device__ __forceinline__ int list_experts(uint8_t* list, int lane, const float (&v)[V], int first, int n, bool mine,
+                                            float least)
+{
+    int count = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if (mine && j < n && v[j] >= least) ++count;
+    int at = count;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(kAll, at, d);
+        if (lane >= d) at += o;
+    }
+    const int total = __shfl_sync(kAll, at, 31);
+    if (total > 32) return total;
+    at -= count;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if (mine && j < n && v[j] >= least) list[at++] = (uint8_t)(first + j);
+    __syncwarp();
+    return total;
+}
+
+// The short way, which nearly every row takes: keys in fp32, the groups, then a
+// bound that at least k keys reach (the k-th largest of the lanes' best); the few
+// experts that reach it go one to a lane, and are put in order there, in fp64 where
+// fp32 does not tell two of them apart. FULL: every lane holds V experts, and they
+// may be read in vectors. SCORES: keys or group values are scores (else keys are the
+// logits).
+template <int V, typename T, bool FULL, bool SCORES>
+__global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 4 : 2) route_logits_kernel(const RouteLogitsArgs a)
+{
+    __shared__ uint8_t listed[kWarps][32];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    uint8_t* list = listed[threadIdx.x >> 5];
+    const Place<V> p(a, lane);
+    const int n = FULL ? V : p.n;
+    const bool biased = SCORES && a.bias != nullptr;
+    const bool pairs = SCORES && a.groups > 1 && a.group_top == 2;   // group values are sums of scores
+    float b[V];
+    float b_most = 0.0f;   // the largest finite |bias|
+    if constexpr (SCORES) {
+        load_bias<V>(a, p, b);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (fabsf(b[j]) < __builtin_huge_valf()) b_most = fmaxf(b_most, fabsf(b[j]));
+        b_most = max_f32(b_most);
+    }
+
+    for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.T; t += (int64_t)gridDim.x * kWarps) {
+        const T* row = static_cast<const T*>(a.logits) + t * a.stride;
+        float l[V];
+        if constexpr (FULL) {
+            load_whole<V, T>(row + p.first, l);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) l[j] = j < n ? to_float(row[p.first + j]) : 0.0f;
+        }
+        float odd = 0.0f;   // NaN with any infinity or NaN in the row
+#pragma unroll
+        for (int j = 0; j < V; ++j) odd = fmaf(l[j], 0.0f, odd);
+        bool careful = false;
+        if (__any_sync(kAll, odd != odd)) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) careful = careful || !(l[j] < __builtin_huge_valf());
+            careful = __any_sync(kAll, careful);
+        }
+        float m = 0.0f, inv = 1.0f, tol = 0.0f;
+        float c[V];   // scores + bias
+        if (!a.sigmoid && (SCORES || !a.renorm)) {
+            m = l[0];
+#pragma unroll
+            for (int j = 1; j < V; ++j) m = fmaxf(m, l[j]);
+            m = max_f32(n > 0 ? m : kNegInf);
+            careful = careful || m == kNegInf;
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                c[j] = ex2((l[j] - m) * kLog2e);
+                if (j < n) sum += c[j];
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+            inv = rcp(sum);
+            if constexpr (SCORES) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) c[j] = fmaf(c[j], inv, b[j]);
+                tol = kSoftmaxTol * inv + 0x1p-24f * (inv + b_most);
+            }
+        } else if constexpr (SCORES) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) c[j] = rcp(1.0f + ex2(-kLog2e * l[j])) + b[j];
+            tol = kSigmoidTol + 0x1p-24f * (1.0f + b_most);
+        }
+        float key[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            key[j] = biased ? c[j] : l[j];
+            if (!FULL && j >= n) key[j] = kNegInf;
+        }
+        float best = key[0];
+#pragma unroll
+        for (int j = 1; j < V; ++j) best = fmaxf(best, key[j]);
+        bool kept = FULL || n > 0;
+        if (a.groups > 1) {
+            float value, last;   // of the group; the least of what makes it up
+            if (!pairs) {
+                value = best;
+                for (int d = 1; d < p.lanes; d <<= 1) value = fmaxf(value, __shfl_xor_sync(kAll, value, d));
+                last = value;
+            } else {
+                constexpr int H = V > 1 ? V / 2 : 1;
+                float x[H], y[H];
+#pragma unroll
+                for (int j = 0; j < H; ++j) {
+                    const float u = FULL || 2 * j < n ? c[2 * j] : kNegInf;
+                    const float v = V > 1 && (FULL || 2 * j + 1 < n) ? c[V > 1 ? 2 * j + 1 : 0] : kNegInf;
+                    x[j] = fmaxf(u, v);
+                    y[j] = fminf(u, v);
+                }
+#pragma unroll
+                for (int w = 1; w < H; w <<= 1)
+#pragma unroll
+                    for (int j = 0; j < H; j += 2 * w) merge_two(x[j], y[j], x[j + w], y[j + w]);
+                for (int d = 1; d < p.lanes; d <<= 1)
+                    merge_two(x[0], y[0], __shfl_xor_sync(kAll, x[0], d), __shfl_xor_sync(kAll, y[0], d));
+                value = x[0] + y[0];
+                last = y[0];
+            }
+            float rest = value, least = kNegInf;
+            for (int g = 0; g < a.top_groups; ++g) {
+                least = max_f32(rest);
+                if (rest == least) rest = kNegInf;
+            }
+            kept = kept && value >= least;
+            // as many groups as are wanted (equal values: more), and the next one well below
+            const unsigned firsts = __ballot_sync(kAll, kept && (lane & (p.lanes - 1)) == 0);
+            bool near = __popc(firsts) != a.top_groups;
+            if (SCORES && (biased || pairs)) near = near || !(least - max_f32(rest) > (pairs ? 8.0f : 2.0f) * tol);
+            if (near && !careful) {
+                const float(&from)[V] = SCORES && (biased || pairs) ? c : key;
+                const int total = list_experts<V>(list, lane, from, p.first, n, FULL || n > 0, last - 2.0f * tol);
+                careful = total > 32;
+                if (!careful) {
+                    const int e = lane < total ? list[lane] : 0;
+                    const float le = to_float(row[e]);
+                    double k64 = (double)le;
+                    if (SCORES && (biased || pairs)) {
+                        const double sum = a.sigmoid ? 1.0 : sum64<V, T>(row, p.first, n, m);
+                        k64 = score64(le, a.sigmoid, m, sum) + (biased ? (double)__ldg(a.bias + e) : 0.0);
+                    }
+                    const unsigned mask = settle_groups(a, lane, total, e / (a.E / a.groups), k64);
+                    kept = n > 0 && ((mask >> p.group) & 1u);
+                }
+            }
+            if (!kept) best = kNegInf;
+        }
+        // at least k keys (or all) are as large as the k-th largest of the lanes' best
+        float least = kNegInf;
+        for (int r = 0; r < a.k; ++r) {
+            least = max_f32(best);
+            if (best == least) best = kNegInf;
+        }
+        // those experts, one a lane from here on
+        int total = 33;
+        if (!careful) total = list_experts<V>(list, lane, key, p.first, n, kept, least - 2.0f * tol);
+        if (total > 32) {
+            careful_row<V, T>(a, t, lane, b_most);
+            continue;
+        }
+        const bool mine = lane < total;
+        const int e = mine ? list[lane] : 0;
+        const float le = to_float(row[e]);
+        int place = 0;
+        float s;
+        if (biased) {
+            const float be = __ldg(a.bias + e);
+            s = a.sigmoid ? sigmoid_near(le) : exp_near(le - m) * inv;
+            // before this one for certain, and before it or equal to it as far as fp32 tells
+            const float k = mine ? s + be : kNegInf;
+            int maybe = 0;
+            for (int i = 0; i < total; ++i) {
+                const float d = __shfl_sync(kAll, k, i) - k;
+                if (d > 2.0f * tol) ++place;
+                if (d >= -2.0f * tol) ++maybe;
+            }
+            if (__any_sync(kAll, mine && place < a.k && maybe - place != 1)) {
+                // in fp64, ties by index
+                const double sum = a.sigmoid ? 1.0 : sum64<V, T>(row, p.first, n, m);
+                const double k64 = score64(le, a.sigmoid, m, sum) + (double)be;
+                place = 0;
+#pragma unroll 1
+                for (int i = 0; i < total; ++i) {
+                    const double o = __shfl_sync(kAll, k64, i);
+                    place += o > k64 || (o == k64 && i < lane);
+                }
+            }
+        } else {
+            const float k = mine ? le : kNegInf;
+            for (int i = 0; i < total; ++i) {
+                const float o = __shfl_sync(kAll, k, i);
+                if (o > k || (o == k && i < lane)) ++place;
+            }
+            // a renormalized softmax: the sum over all experts cancels
+            if (!SCORES && !a.sigmoid && a.renorm) m = max_f32(k);
+            s = a.sigmoid ? sigmoid_near(le) : exp_near(le - m) * inv;
+        }
+        const bool chosen = mine && place < a.k;
+        bool again = false;
+        if (a.renorm) {
+            again = __any_sync(kAll, chosen && s < kTiny);
+            float sum = chosen ? s : 0.0f;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+            s = __fdividef(s, sum);
+        }
+        if (again) {
+            careful_row<V, T>(a, t, lane, b_most);
+        } else if (chosen) {
+            a.topk_idx[t * a.k + place] = e;
+            a.topk_w[t * a.k + place] = s * a.scale;
+        }
+    }
+}
+
+template <int V, typename T, bool FULL, bool SCORES>
 cudaError_t launch(const RouteLogitsArgs& a, int num_sms, cudaStream_t s)
 {
     int64_t blocks = (a.T + kWarps - 1) / kWarps;
     const int64_t most = (int64_t)num_sms * 8;
     if (blocks > most) blocks = most;
-    return launch_pdl(route_logits_kernel<V, T>, dim3((unsigned)blocks), dim3(32 * kWarps), 0, s, a);
+    return launch_pdl(route_logits_kernel<V, T, FULL, SCORES>, dim3((unsigned)blocks), dim3(32 * kWarps), 0, s, a);
+}
+
+template <int V, typename T>
+cudaError_t launch_place(const RouteLogitsArgs& a, int num_sms, int lanes, cudaStream_t s)
+{
+    constexpr int BYTES = V * (int)sizeof(T) < 16 ? V * (int)sizeof(T) : 16;
+    const bool full = lanes * a.groups == 32 && a.E == 32 * V && reinterpret_cast<uintptr_t>(a.logits) % BYTES == 0 &&
+                      (a.T == 1 || a.stride * (int)sizeof(T) % BYTES == 0);
+    const bool scores = a.bias || (a.groups > 1 && a.group_top == 2);
+    if (scores) return full ? launch<V, T, true, true>(a, num_sms, s) : launch<V, T, false, true>(a, num_sms, s);
+    return full ? launch<V, T, true, false>(a, num_sms, s) : launch<V, T, false, false>(a, num_sms, s);
 }
 
 template <typename T>
@@ -377,11 +691,11 @@ cudaError_t launch_type(const RouteLogitsArgs& a, int num_sms, cudaStream_t s)
     int lanes = 32 / a.groups;
     while (lanes & (lanes - 1)) lanes &= lanes - 1;
     const int per_lane = (a.E / a.groups + lanes - 1) / lanes;
-    if (per_lane <= 1) return launch<1, T>(a, num_sms, s);
-    if (per_lane <= 2) return launch<2, T>(a, num_sms, s);
-    if (per_lane <= 4) return launch<4, T>(a, num_sms, s);
-    if (per_lane <= 8) return launch<8, T>(a, num_sms, s);
-    if (per_lane <= 16) return launch<16, T>(a, num_sms, s);
+    if (per_lane <= 1) return launch_place<1, T>(a, num_sms, lanes, s);
+    if (per_lane <= 2) return launch_place<2, T>(a, num_sms, lanes, s);
+    if (per_lane <= 4) return launch_place<4, T>(a, num_sms, lanes, s);
+    if (per_lane <= 8) return launch_place<8, T>(a, num_sms, lanes, s);
+    if (per_lane <= 16) return launch_place<16, T>(a, num_sms, lanes, s);
     return cudaErrorInvalidValue;
 }
 
