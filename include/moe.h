@@ -614,7 +614,7 @@ typedef struct {
  * bytes have to be zero before its first use, and again after moe_check has returned
  * MOE_ERR_TIMEOUT for it; the calls leave them as the next call needs them. Two calls
  * that share a workspace must not overlap. */
-#define MOE_LINEAR_WORKSPACE_ZEROS 256
+#define MOE_LINEAR_WORKSPACE_ZEROS 2304
 size_t moe_linear_workspace_size(void);
 
 /*
@@ -628,7 +628,7 @@ size_t moe_linear_workspace_size(void);
  *      offsets[G+1] (device); w of type dtype; epilogue (nullable).
  * Out: out[R,N] of type out_dtype (dtype or fp32), rows out_stride apart; its memory
  *      may be the residual's, and no other input's.
- * K and N multiples of 8, G <= 256; a and w 16-byte aligned, a_stride a multiple of 8,
+ * K and N multiples of 8 up to 2^30, G <= 256; a and w 16-byte aligned, a_stride a multiple of 8,
  * the others aligned to their type.
  */
 moe_status moe_linear(int64_t R, int32_t K, int32_t N, int32_t G, moe_dtype dtype, const void* a, int64_t a_stride,

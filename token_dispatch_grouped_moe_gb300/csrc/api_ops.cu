@@ -18,10 +18,16 @@ constexpr int32_t kMaxTopK = 8;
 constexpr int32_t kMaxExperts = 256;
 constexpr int32_t kMaxGroupsOfExperts = 32;
 
-static_assert(kLinearWorkspaceBytes >= MOE_LINEAR_WORKSPACE_ZEROS, "the zeros lie in the workspace");
+static_assert(kLinearPartOffset == MOE_LINEAR_WORKSPACE_ZEROS, "what has to be zero lies before the parts");
 
 bool is_dtype(moe_dtype t) { return t == MOE_BF16 || t == MOE_FP16 || t == MOE_FP32; }
 int size_of(moe_dtype t) { return t == MOE_FP32 ? 4 : 2; }
+// The form of a product over R rows in G groups.
+LinearForm linear_form(int64_t R, int32_t K, int32_t N, int32_t G, int sms)
+{
+    return N > 128 && R > (int64_t)128 * G ? kLinearPair : kLinearOne;
+}
+
 bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
 
 }  // namespace
@@ -71,7 +77,8 @@ moe_status moe_linear(int64_t R, int32_t K, int32_t N, int32_t G, moe_dtype dtyp
     if (dtype != MOE_BF16 && dtype != MOE_FP16) return MOE_ERR_UNSUPPORTED;
     if (out_dtype != dtype && out_dtype != MOE_FP32) return MOE_ERR_UNSUPPORTED;
     if (e.bias && e.bias_dtype != dtype && e.bias_dtype != MOE_FP32) return MOE_ERR_UNSUPPORTED;
-    if (K % 8 || N % 8 || G > kMaxExperts || R >= ((int64_t)1 << 31) - 256) return MOE_ERR_UNSUPPORTED;
+    if (K % 8 || N % 8 || K > (1 << 30) || N > (1 << 30) || G > kMaxExperts || R >= ((int64_t)1 << 31) - 256)
+        return MOE_ERR_UNSUPPORTED;
     // tiles, and a round of them more, are counted in 32 bits
     if ((R / 128 + G) * (((int64_t)N + 127) / 128) >= ((int64_t)1 << 31) - (1 << 16)) return MOE_ERR_UNSUPPORTED;
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < kLinearWorkspaceBytes) return MOE_ERR_WORKSPACE;
@@ -111,8 +118,13 @@ moe_status moe_linear(int64_t R, int32_t K, int32_t N, int32_t G, moe_dtype dtyp
     args.out_stride = out_stride;
     args.fp16 = dtype == MOE_FP16;
     args.w_nk = nk;
+    unsigned char* b = static_cast<unsigned char*>(ws);
+    args.ticket = reinterpret_cast<int32_t*>(b + kLinearTicketOffset);
+    args.part = reinterpret_cast<float*>(b + kLinearPartOffset);
     args.err = static_cast<uint32_t*>(ws);
-    return finish(launch_linear(out_dtype, tm_a, tm_a_small, tm_w, args, sms, (cudaStream_t)stream), ws,
+    const LinearForm form = linear_form(R, K, N, G, sms);
+    args.tile_rows = form == kLinearOne ? 128 : 256;
+    return finish(launch_linear(form, out_dtype, tm_a, tm_a_small, tm_w, args, sms, (cudaStream_t)stream), ws,
                   (cudaStream_t)stream);
 }
 

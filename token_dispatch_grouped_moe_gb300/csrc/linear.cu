@@ -22,6 +22,15 @@
 //   warps 0..7  epilogue: warp w reads TMEM lanes 32 (w mod 4) .. + 31 (columns n,
 //               one a thread) and half of the rows;
 //   warp 8      TMA producer; warp 9 TMEM allocator and MMA issuer.
+// CTA pairs (PAIR): a 2-CTA cluster shares one tcgen05.mma.cta_group::2 of 256
+// columns n, each CTA staging its 128 of them and half of the rows; both CTAs'
+// boxes complete on rank 0's barrier, rank 0 issues, its commits arrive in both CTAs,
+// and both CTAs' epilogue warps release a TMEM buffer on rank 0.
+// When the tiles do not fill the SMs evenly (few rows), K is cut: the blocks of the
+// tiles that are left over, end to end, go to the CTAs in equal runs; each CTA writes
+// the sums of a tile that it has only a part of to the workspace and takes a ticket,
+// and the last one adds the parts in the order of their blocks (so the result does
+// not depend on which came last) and runs the epilogue. No CTA waits for another.
 // Every wait is bounded (ptx.cuh).
 #include <atomic>
 #include <cstdint>
@@ -37,7 +46,7 @@
 namespace moe {
 namespace {
 
-constexpr int BM = 128;             // columns of the output in a tile
+constexpr int BM = 128;             // columns of the output that a CTA has of a tile
 constexpr int BK = kLinearBK;
 constexpr int W_BYTES = BM * BK * 2;
 constexpr int STRETCH = 8;          // k blocks between two reads of TMEM
@@ -49,43 +58,65 @@ constexpr int NUM_THREADS = 32 * EPI_WARPS + 128;
 constexpr int EPI_REGS = 216;
 constexpr int OTHER_REGS = 72;
 constexpr int MAX_GROUPS = 256;
-constexpr int ROW_STEP = 16;        // the MMA's N is a multiple of this
 constexpr int BAND = 16;            // row tiles that are taken together
 
-template <int BN>
+// BN: rows of a tile at most.
+template <bool PAIR, int BN>
 struct Cfg {
-    static constexpr int STAGE_BYTES = W_BYTES + BN * BK * 2;
-    static constexpr int STAGES = BN == 256 ? 4 : 6;
-    static constexpr int TMEM_COLS = 2 * BN;
+    static constexpr int A_ROWS = PAIR ? BN / 2 : BN;           // rows that a CTA stages
+    static constexpr int STAGE_BYTES = W_BYTES + A_ROWS * BK * 2;
+    static constexpr int STAGES = 6;
+    static constexpr int TMEM_COLS = 2 * BN;                    // two buffers
+    static constexpr int TILE_N = PAIR ? 2 * BM : BM;           // columns of one work item
+    static constexpr int ROW_STEP = PAIR ? 32 : 16;             // the MMA's N is a multiple of this
 };
 
 struct Tile {
     int g, row0, rows, n0;
 };
 
+// The schedule: the first `full` tiles whole, round robin over the CTAs; the K
+// blocks of the rest, end to end, in `segments` equal runs, one a CTA. A run
+// that begins or ends inside a tile computes a part of its sums.
+struct Plan {
+    int tiles, full, segments;
+    int part_rows;   // rows a part has room for: those of the fullest tile
+};
+
 template <int STAGES>
 struct SmemTail {
     uint64_t full[STAGES];
     uint64_t empty[STAGES];
-    uint64_t tfull[2];
-    uint64_t tempty[2];
+    uint64_t tfull[2];                 // a stretch's sums are there
+    uint64_t tempty[2];                // they are read (a pair: by both CTAs, on rank 0's)
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
+    int last;                          // cut tiles: this CTA took the tile's last ticket
+    int most_rows;                     // rows of the fullest tile
     int tile_start[MAX_GROUPS + 1];    // row tiles before each group
     int offsets[MAX_GROUPS + 1];
 };
 
-template <int BN>
+template <bool PAIR, int BN>
 constexpr size_t smem_bytes()
 {
-    return 1024 + (size_t)Cfg<BN>::STAGES * Cfg<BN>::STAGE_BYTES + sizeof(SmemTail<Cfg<BN>::STAGES>);
+    using C = Cfg<PAIR, BN>;
+    return 1024 + (size_t)C::STAGES * C::STAGE_BYTES + sizeof(SmemTail<C::STAGES>);
 }
-static_assert(smem_bytes<256>() <= 227 * 1024 && smem_bytes<128>() <= 227 * 1024, "shared memory");
+static_assert(smem_bytes<false, 128>() <= 227 * 1024 && smem_bytes<true, 256>() <= 227 * 1024, "shared memory");
+
+// A group's rows are spread evenly over its row tiles.
+template <int STEP>
+__device__ __forceinline__ int rows_per_tile(int rows, int tiles)
+{
+    return (int)(((unsigned)(rows + tiles - 1) / (unsigned)tiles + STEP - 1) / STEP * STEP);
+}
 
 // Tile w: group-major; within a group, bands of BAND row tiles, in a band n tile by
 // n tile (neighbouring CTAs share a tile of w, and a band's rows stay in L2 while
-// all of w passes). A group's rows are spread evenly over its row tiles.
+// all of w passes).
+template <int TILE_N, int STEP>
 __device__ __forceinline__ Tile decode_tile(int w, int n_tiles, const int* ts, const int* offs, int G)
 {
     int lo = 0, hi = G;
@@ -96,27 +127,157 @@ __device__ __forceinline__ Tile decode_tile(int w, int n_tiles, const int* ts, c
     Tile r;
     r.g = lo;
     const int mt = ts[lo + 1] - ts[lo];
-    int tl = w - ts[lo] * n_tiles;
-    const int band = tl / (BAND * n_tiles);
-    tl -= band * BAND * n_tiles;
-    const int in_band = min(BAND, mt - band * BAND);
-    const int n_tile = tl / in_band;
-    const int m_tile = band * BAND + tl - n_tile * in_band;
-    const int rows = offs[lo + 1] - offs[lo];
-    const int per = ((rows + mt - 1) / mt + ROW_STEP - 1) / ROW_STEP * ROW_STEP;
+    unsigned tl = (unsigned)(w - ts[lo] * n_tiles);
+    const unsigned band = tl / (unsigned)(BAND * n_tiles);
+    tl -= band * (unsigned)(BAND * n_tiles);
+    const unsigned in_band = min((unsigned)BAND, mt - band * BAND);
+    const unsigned n_tile = tl / in_band;
+    const int m_tile = (int)(band * BAND + tl - n_tile * in_band);
+    const int per = rows_per_tile<STEP>(offs[lo + 1] - offs[lo], mt);
     r.row0 = offs[lo] + m_tile * per;
     r.rows = min(per, offs[lo + 1] - r.row0);
-    r.n0 = n_tile * BM;
+    r.n0 = (int)n_tile * TILE_N;
     return r;
 }
 
-__device__ __forceinline__ float gelu(float x) { return 0.5f * x * erfcf(x * -0.70710678118654752440f); }
+struct Piece {
+    int tile, kb0, kb1;
+};
+
+struct Walk {   // make_plan keeps the products below 2^32
+    uint32_t tile, step, full, k_blocks, pos, end;
+
+    __device__ __forceinline__ Walk(const Plan& p, int unit, int n_units, int k_blocks_)
+        : tile(unit), step(n_units), full(p.full), k_blocks(k_blocks_), pos(0), end(0)
+    {
+        if (unit < p.segments) {
+            const uint32_t total = (uint32_t)(p.tiles - p.full) * k_blocks;
+            pos = total * (uint32_t)unit / (uint32_t)p.segments;
+            end = total * (uint32_t)(unit + 1) / (uint32_t)p.segments;
+        }
+    }
+
+    __device__ __forceinline__ bool next(Piece& p)
+    {
+        if (tile < full) {
+            p = {(int)tile, 0, (int)k_blocks};
+            tile += step;
+            return true;
+        }
+        if (pos >= end) return false;
+        const uint32_t q = pos / k_blocks, kb0 = pos - q * k_blocks;
+        p = {(int)(full + q), (int)kb0, (int)min(k_blocks, kb0 + (end - pos))};
+        pos += (uint32_t)p.kb1 - kb0;
+        return true;
+    }
+};
+
+// The parts of tile q of the segments' tiles: the first segment that holds
+// blocks of it, and how many do. Segment c keeps a part that begins with its
+// tile in slot 2c + 1, one that begins inside it in slot 2c.
+__device__ __forceinline__ int first_part(const Plan& p, int q, int k_blocks, int& parts)
+{
+    const uint32_t total = (uint32_t)(p.tiles - p.full) * (uint32_t)k_blocks;
+    auto segment_of = [&](uint32_t block) { return (int)(((block + 1) * (uint32_t)p.segments - 1) / total); };
+    const int first = segment_of((uint32_t)q * (uint32_t)k_blocks);
+    parts = segment_of((uint32_t)(q + 1) * (uint32_t)k_blocks - 1) - first + 1;
+    return first;
+}
+
+// The plan with the least estimated time, counted in K blocks of one CTA, one
+// candidate a lane (the warp calls it together): lane 0 every tile whole; lane l the
+// tiles, where they fill less than one round, in l + 1 parts each; lane 31 the tiles
+// beyond the whole rounds but one (or all of them) in equal runs. Cutting costs the
+// parts' publication, twice where the runs do not line up with tiles, and the join's
+// trips to L2.
+template <int CG>
+__device__ __forceinline__ Plan make_plan(int tiles, int rows, int k_blocks, int n_units, int lane)
+{
+    // parts have room, and the products of Walk and first_part stay below 2^32
+    const bool room = 2 * n_units * CG * rows <= kLinearPartRows && 2 * n_units * CG <= kLinearMaxTickets &&
+                      k_blocks < (1 << 30) / (n_units * n_units);
+    const int rounds = (int)((unsigned)tiles / (unsigned)n_units);
+    const int last = tiles - rounds * n_units;
+    const float whole = (float)k_blocks + kLinearTileCost;
+    int full = tiles, segments = 0;
+    float cost = (float)(rounds + (last > 0)) * whole;
+    bool fits = lane == 0;
+    if (lane > 0 && room && tiles > 0) {
+        const bool even = lane < 31;
+        const int whole_rounds = !even && rounds > 1 ? rounds - 1 : 0;
+        fits = even ? rounds == 0 && lane < kLinearMaxSplit && tiles * (lane + 1) <= n_units : last > 0;
+        if (fits) {
+            full = whole_rounds * n_units;
+            segments = even ? tiles * (lane + 1) : n_units;
+            const uint32_t left = (uint32_t)(tiles - full);   // below 2 n_units
+            const uint32_t total = left * (uint32_t)k_blocks;
+            const int parts = even ? lane + 1 : (int)((unsigned)n_units / left) + 2;
+            fits = total >= 2u * (uint32_t)segments;
+            cost = (float)whole_rounds * whole + __fdividef((float)total, (float)segments) + 0.5f +
+                   (even ? 1.0f : 2.0f) * kLinearCutCost + kLinearJoinCost * (float)(rows * parts);
+        }
+    }
+    // the least cost (its low bits give way to the lane)
+    const uint32_t key = fits ? (__float_as_uint(cost) & ~31u) | (uint32_t)lane : 0xffffffffu;
+    const int best = (int)(__reduce_min_sync(0xffffffffu, key) & 31u);
+    return Plan{tiles, __shfl_sync(0xffffffffu, full, best), __shfl_sync(0xffffffffu, segments, best), rows};
+}
+
+__device__ __forceinline__ void epilogue_barrier()   // the epilogue warps only
+{
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * EPI_WARPS) : "memory");
+}
+
+// Adds this thread's rows c < rows of a tile's parts to acc, in the parts' order: a
+// row of a part is BM floats, one a column (src: this thread's column of its row 0).
+// ROWS rows of PARTS parts are in flight together (each a trip to L2).
+template <int HALF, int ROWS, int PARTS>
+__device__ __forceinline__ void add_parts(float (&acc)[HALF], const float* src, int rows, int parts, int64_t stride)
+{
+    // the first part begins with the tile, the others inside it (first_part)
+    auto slot = [&](int s) { return (int64_t)(s == 0 ? 1 : 2 * s) * stride; };
+#pragma unroll
+    for (int c = 0; c < (ROWS < 32 ? ROWS : HALF); c += ROWS) {
+        if (c >= rows) break;
+        for (int s0 = 0; s0 < parts; s0 += PARTS) {
+            float v[PARTS][ROWS];
+#pragma unroll
+            for (int s = 0; s < PARTS; ++s)
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i)
+                    v[s][i] = s0 + s < parts && c + i < rows ? __ldcg(src + slot(s0 + s) + (c + i) * BM) : 0.0f;
+#pragma unroll
+            for (int s = 0; s < PARTS; ++s)
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i) acc[c + i] += v[s][i];
+        }
+    }
+}
+
+// x (1 + erf(x / sqrt 2)) / 2 = max(x, 0) - |x| q, q = erfc(|x| / sqrt 2) / 2. erfc(z) =
+// (a1 t + ... + a5 t^5) e^(-z^2), t = 1 / (1 + p z), within 1.5e-7 (Abramowitz and
+// Stegun, Handbook of Mathematical Functions, 7.1.26; the factor 1/2 is in the
+// coefficients here). With erfcf a prefill of 16384 rows, 8 experts 4096 -> 14336,
+// takes 2180 us instead of 1420.
+__device__ __forceinline__ float gelu(float x)
+{
+    const float z = fabsf(x) * 0.70710678118654752440f;
+    const float t = __fdividef(1.0f, fmaf(0.3275911f, z, 1.0f));
+    float q = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
+    q = fmaf(q, t, 0.5f * 1.421413741f);
+    q = fmaf(q, t, 0.5f * -0.284496736f);
+    q = fmaf(q, t, 0.5f * 0.254829592f);
+    q = q * t * __expf(-z * z);
+    return fmaf(-fabsf(x), q, fmaxf(x, 0.0f));
+}
+
 // 0.5 x (1 + tanh(u)) = x / (1 + e^(-2u)), u = sqrt(2/pi) (x + 0.044715 x^3)
 __device__ __forceinline__ float gelu_tanh(float x)
 {
     const float u2 = x * fmaf(0.071354816272600125f, x * x, 1.5957691216057308f);
     return __fdividef(x, 1.0f + __expf(-u2));
 }
+
 __device__ __forceinline__ float silu_of(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
 
 template <int N>
@@ -143,6 +304,20 @@ __device__ __forceinline__ void activate(float (&v)[N], int act)
     }
 }
 
+template <bool PAIR>
+__device__ __forceinline__ void load_2d(uint32_t dst, const void* map, int c0, int c1, uint32_t bar)
+{
+    if (PAIR) tma_load_2d_pair(dst, map, c0, c1, bar); else tma_load_2d(dst, map, c0, c1, bar);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void load_3d(uint32_t dst, const void* map, int c0, int c1, int c2, uint32_t bar)
+{
+    if (PAIR) tma_load_3d_pair(dst, map, c0, c1, c2, bar); else tma_load_3d(dst, map, c0, c1, c2, bar);
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 __device__ __forceinline__ float as_float(float v) { return v; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float as_float(__half v) { return __half2float(v); }
@@ -150,7 +325,7 @@ __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
 
-template <typename OUT, int BN>
+template <typename OUT, bool PAIR, int BN>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_a_small,
               const __grid_constant__ CUtensorMap tm_w, const LinearArgs args)
@@ -158,14 +333,19 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t tiles_addr = (raw_addr + 1023u) & ~1023u;
-    using C = Cfg<BN>;
+    using C = Cfg<PAIR, BN>;
     constexpr int HALF = BN / 2;       // rows of an epilogue thread
     constexpr int STAGES = C::STAGES;
+    constexpr int CG = PAIR ? 2 : 1;   // tcgen05 CTA group
     SmemTail<STAGES>* st =
         reinterpret_cast<SmemTail<STAGES>*>(smem_raw + (tiles_addr - raw_addr) + (size_t)STAGES * C::STAGE_BYTES);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int G = args.G;
+    // a pair walks the schedule together, each CTA with its half of every tile's columns
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+    const int unit = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+    const int n_units = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -174,7 +354,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&st->tfull[a]), 1);
-            mbar_init(smem_u32(&st->tempty[a]), EPI_WARPS);
+            mbar_init(smem_u32(&st->tempty[a]), CG * EPI_WARPS);
         }
         mbar_init(smem_u32(&st->drain), 1);
         st->abort = 0;
@@ -186,52 +366,76 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         tma_prefetch_desc(&tm_w);
     }
     if (warp == 9) {
-        tmem_alloc(smem_u32(&st->tmem_base), C::TMEM_COLS);
-        tmem_relinquish();
+        tmem_alloc<CG>(smem_u32(&st->tmem_base), C::TMEM_COLS);
+        tmem_relinquish<CG>();
     }
-    pdl_wait();
-    pdl_launch_dependents();
+    // a dense product's schedule does not wait for the kernel before it
+    if (args.offsets) pdl_wait();
     if (warp == 0) {
-        // the row tiles before each group (a scan, 32 groups at a time); offsets that
+        // the row tiles before each group, a lane a run of up to PER groups; offsets that
         // decrease or leave [0, R] are reported and give no tiles at all, so no row
         // outside the operands is touched
-        bool good = true;
-        int tiles = 0;
-        for (int g0 = 0; g0 < G; g0 += 32) {
-            const int g = g0 + lane;
-            int n = 0;
-            if (g < G) {
-                const int first = args.offsets ? args.offsets[g] : 0;
-                const int end = args.offsets ? args.offsets[g + 1] : args.R;
-                good = good && first >= 0 && first <= end && end <= args.R;
-                st->offsets[g] = first;
-                if (g == G - 1) st->offsets[G] = end;
-                n = good ? (end - first + BN - 1) / BN : 0;
-            }
-            int incl = n;
+        constexpr int PER = MAX_GROUPS / 32;
+        const int per = (G + 31) / 32, g0 = lane * per;
+        int off[PER + 1];
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, d);
-                if (lane >= d) incl += v;
-            }
-            if (g < G) st->tile_start[g] = tiles + incl - n;
-            tiles += __shfl_sync(0xffffffffu, incl, 31);
+        for (int i = 0; i <= PER; ++i) {
+            off[i] = g0 + i ? args.R : 0;
+            if (args.offsets && i <= per && g0 + i <= G) off[i] = args.offsets[g0 + i];
         }
+        bool good = true;
+        int tiles[PER], sum = 0;
+        int most = 0;   // rows of the fullest tile
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            tiles[i] = 0;
+            if (i < per && g0 + i < G) {
+                good = good && off[i] >= 0 && off[i] <= off[i + 1] && off[i + 1] <= args.R;
+                const int rows = good ? off[i + 1] - off[i] : 0;
+                if (rows) {
+                    tiles[i] = (int)((unsigned)(rows + args.tile_rows - 1) / (unsigned)args.tile_rows);
+                    most = max(most, rows_per_tile<C::ROW_STEP>(rows, tiles[i]));
+                    sum += tiles[i];
+                }
+            }
+        }
+        int incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += v;
+        }
+        int before = incl - sum;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (i < per && g0 + i < G) {
+                st->offsets[g0 + i] = off[i];
+                st->tile_start[g0 + i] = before;
+                before += tiles[i];
+                if (g0 + i == G - 1) st->offsets[G] = off[i + 1];
+            }
         good = __all_sync(0xffffffffu, good);
+        most = __reduce_max_sync(0xffffffffu, most);
+        const int all = __shfl_sync(0xffffffffu, incl, 31);
         if (lane == 0) {
-            st->tile_start[G] = good ? tiles : 0;
+            st->tile_start[G] = good ? all : 0;
+            st->most_rows = most;
             if (!good) report_error(args.err, MOE_DEV_ERR_BOUNDS);
         }
     }
     tc_fence_before();
-    __syncthreads();
+    // a pair: both CTAs' barriers are initialised before either signals the other's
+    if (PAIR) cluster_sync(); else __syncthreads();
     tc_fence_after();
 
     const uint32_t tmem_base = st->tmem_base;
-    const int n_tiles = (args.N + BM - 1) / BM;
+    const int n_tiles = (args.N + C::TILE_N - 1) / C::TILE_N;
     const int k_blocks = (args.K + BK - 1) / BK;
-    const int tiles = st->tile_start[G] * n_tiles;
+    const Plan plan = make_plan<CG>(st->tile_start[G] * n_tiles, st->most_rows, k_blocks, n_units, lane);
     volatile int* abort = &st->abort;
+    auto decode = [&](int tile) {
+        return decode_tile<C::TILE_N, C::ROW_STEP>(tile, n_tiles, st->tile_start, st->offsets, G);
+    };
 
     if (warp >= 8) {
         setmaxnreg_dec<OTHER_REGS>();
@@ -242,37 +446,47 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                 uint32_t phase = 0;
                 int issued = 0;
                 bool ok = true;
-                for (int w = blockIdx.x; ok && w < tiles; w += gridDim.x) {
-                    const Tile it = decode_tile(w, n_tiles, st->tile_start, st->offsets, G);
-                    // boxes of 128 rows, then of 32 up to the tile's last row
-                    const int large = it.rows / kLinearRowBox;
-                    const int small = (it.rows - large * kLinearRowBox + kLinearRowBoxSmall - 1) / kLinearRowBoxSmall;
+                Walk walk(plan, unit, n_units, k_blocks);
+                Piece pc;
+                bool more = walk.next(pc);
+                Tile it = more ? decode(pc.tile) : Tile{0, 0, 0, 0};
+                if (!args.offsets) pdl_wait();
+                for (; ok && more; more = walk.next(pc)) {
+                    if (issued) it = decode(pc.tile);
+                    // this CTA's rows: boxes of 128, then of 32 up to the last one that the MMA
+                    // reads (a pair: each CTA its half of them)
+                    const int rows = PAIR ? (it.rows + 31) / 32 * 16 : it.rows;
+                    const int row0 = it.row0 + (int)rank * rows;
+                    const int n0 = it.n0 + (int)rank * BM;
+                    const int large = rows / kLinearRowBox;
+                    const int small = (rows - large * kLinearRowBox + kLinearRowBoxSmall - 1) / kLinearRowBoxSmall;
                     const uint32_t bytes = W_BYTES + (uint32_t)(large * kLinearRowBox + small * kLinearRowBoxSmall) * BK * 2;
-                    for (int kb = 0; kb < k_blocks; ++kb) {
+                    for (int kb = pc.kb0; kb < pc.kb1; ++kb) {
                         if (!mbar_wait(smem_u32(&st->empty[stage]), phase ^ 1u, abort, args.err)) {
                             ok = false;
                             break;
                         }
-                        const uint32_t full = smem_u32(&st->full[stage]);
+                        uint32_t full = smem_u32(&st->full[stage]);
                         const uint32_t w_dst = tiles_addr + stage * C::STAGE_BYTES;
                         uint32_t a_dst = w_dst + W_BYTES;
-                        mbar_arrive_expect_tx(full, bytes);
+                        if (rank == 0) mbar_arrive_expect_tx(full, CG * bytes);
+                        if (PAIR) full = mapa_shared(full, 0);
                         if (args.w_nk) {
-                            tma_load_3d(w_dst, &tm_w, kb * BK, it.n0, it.g, full);
+                            load_3d<PAIR>(w_dst, &tm_w, kb * BK, n0, it.g, full);
                         } else {
-                            tma_load_3d(w_dst, &tm_w, it.n0, kb * BK, it.g, full);
-                            tma_load_3d(w_dst + W_BYTES / 2, &tm_w, it.n0 + 64, kb * BK, it.g, full);
+                            load_3d<PAIR>(w_dst, &tm_w, n0, kb * BK, it.g, full);
+                            load_3d<PAIR>(w_dst + W_BYTES / 2, &tm_w, n0 + 64, kb * BK, it.g, full);
                         }
-                        int row = it.row0;
+                        int row = row0;
                         for (int i = 0; i < large; ++i, row += kLinearRowBox, a_dst += kLinearRowBox * BK * 2)
-                            tma_load_2d(a_dst, &tm_a, kb * BK, row, full);
+                            load_2d<PAIR>(a_dst, &tm_a, kb * BK, row, full);
                         for (int i = 0; i < small; ++i, row += kLinearRowBoxSmall, a_dst += kLinearRowBoxSmall * BK * 2)
-                            tma_load_2d(a_dst, &tm_a_small, kb * BK, row, full);
+                            load_2d<PAIR>(a_dst, &tm_a_small, kb * BK, row, full);
                         ++issued;
                         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                     }
                 }
-                if (!ok) {
+                if (!PAIR && !ok) {
                     // drain: wait (bounded) for the loads still in flight
                     for (int i = 0; i < min(issued, STAGES); ++i) {
                         if (stage == 0) { stage = STAGES - 1; phase ^= 1u; } else { --stage; }
@@ -283,8 +497,9 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             __syncwarp();
         } else if (warp == 9) {
             // ============================ MMA issuer ==============================
-            // the whole warp walks the tiles and waits (uniform control flow, so the
-            // descriptors stay in uniform registers); one elected lane issues
+            // the whole warp walks the pieces and waits (uniform control flow, so the
+            // descriptors stay in uniform registers); one elected lane issues (a
+            // pair: of the rank-0 CTA, for both)
             const uint32_t leader = elect_one_sync();
             // w with contiguous n: 64 n x 8 k atoms, the second 64 n 8 KB on, a K step of
             // 16 rows of 128 bytes; with contiguous k (as a): 32 bytes along the row
@@ -293,32 +508,38 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             const uint64_t w_step = args.w_nk ? 2 : 16 * 128 / 16;
             const uint64_t a_desc = smem_desc_sw128(tiles_addr + W_BYTES, 16, 1024);
             const uint32_t fmt = args.fp16 ? 0u : 1u;
-            const uint32_t idesc0 = (1u << 4) | (fmt << 7) | (fmt << 10) | ((args.w_nk ? 0u : 1u) << 15) | ((BM >> 4) << 24);
+            const uint32_t idesc0 =
+                (1u << 4) | (fmt << 7) | (fmt << 10) | ((args.w_nk ? 0u : 1u) << 15) | ((C::TILE_N >> 4) << 24);
             int stage = 0;
             uint32_t phase = 0;
             int buf = 0;
             uint32_t buf_phase = 0;
             bool ok = true;
             bool any = false;
-            for (int w = blockIdx.x; ok && w < tiles; w += gridDim.x) {
-                const Tile it = decode_tile(w, n_tiles, st->tile_start, st->offsets, G);
-                const uint32_t idesc = idesc0 | ((uint32_t)((it.rows + ROW_STEP - 1) / ROW_STEP * ROW_STEP >> 3) << 17);
-                for (int kb = 0; kb < k_blocks; ++kb) {
-                    const bool opens = kb % STRETCH == 0;
+            Walk walk(plan, unit, n_units, k_blocks);
+            for (Piece pc; ok && rank == 0 && walk.next(pc);) {
+                const Tile it = decode(pc.tile);
+                const uint32_t idesc =
+                    idesc0 | ((uint32_t)((it.rows + C::ROW_STEP - 1) / C::ROW_STEP * C::ROW_STEP >> 3) << 17);
+                for (int kb = pc.kb0; kb < pc.kb1; ++kb) {
+                    const int in = (kb - pc.kb0) % STRETCH;
+                    const bool opens = in == 0;
                     ok = __all_sync(0xffffffffu,
                                     mbar_wait(smem_u32(&st->full[stage]), phase, abort, args.err) &&
-                                        (!opens || mbar_wait(smem_u32(&st->tempty[buf]), buf_phase ^ 1u, abort, args.err)));
+                                        (!opens || mbar_wait<PAIR, PAIR>(smem_u32(&st->tempty[buf]), buf_phase ^ 1u,
+                                                                         abort, args.err)));
                     if (!ok) break;
                     tc_fence_after();
-                    const bool closes = kb % STRETCH == STRETCH - 1 || kb == k_blocks - 1;
+                    const bool closes = in == STRETCH - 1 || kb == pc.kb1 - 1;
                     if (leader) {
                         const uint32_t d = tmem_base + buf * BN;
                         const uint64_t at = (uint64_t)(stage * (C::STAGE_BYTES >> 4));
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk)
-                            tc_mma_f16(d, w_desc + at + w_step * kk, a_desc + at + 2 * kk, idesc, !opens || kk != 0 ? 1u : 0u);
-                        tc_commit(smem_u32(&st->empty[stage]));
-                        if (closes) tc_commit(smem_u32(&st->tfull[buf]));
+                            tc_mma_f16<CG>(d, w_desc + at + w_step * kk, a_desc + at + 2 * kk, idesc,
+                                           !opens || kk != 0 ? 1u : 0u);
+                        tc_commit<CG>(smem_u32(&st->empty[stage]));
+                        if (closes) tc_commit<CG>(smem_u32(&st->tfull[buf]));
                     }
                     __syncwarp();
                     any = true;
@@ -328,26 +549,52 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             }
             if (!ok && any && leader) {
                 // drain: every MMA issued so far must finish before TMEM is freed
-                tc_commit(smem_u32(&st->drain));
+                if (PAIR) tc_commit_pair_local(smem_u32(&st->drain));
+                else tc_commit(smem_u32(&st->drain));
                 mbar_wait_drain(smem_u32(&st->drain), 0);
             }
             __syncwarp();
         }
+        if (!args.offsets) pdl_wait();
+        pdl_launch_dependents();
     } else {
         setmaxnreg_inc<EPI_REGS>();
+        if (!args.offsets) pdl_wait();
+        pdl_launch_dependents();
         // ============================== epilogue ==============================
         const int c0 = (warp >> 2) * HALF;             // this thread's rows of the tile
         const uint32_t t_row = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + c0;
         int buf = 0;
         uint32_t buf_phase = 0;
         bool ok = true;
-        for (int w = blockIdx.x; ok && w < tiles; w += gridDim.x) {
-            const Tile it = decode_tile(w, n_tiles, st->tile_start, st->offsets, G);
+        // after an abort every epilogue warp still walks all pieces, without waiting
+        // for the tensor cores, so that the barriers below stay matched
+        Walk walk(plan, unit, n_units, k_blocks);
+        for (Piece pc; walk.next(pc);) {
+            const Tile it = decode(pc.tile);
             const int rows = it.rows - c0;             // of them there are so many
+            const int n = it.n0 + (int)rank * BM + (warp & 3) * 32 + lane;
+            float bias = 0.0f;
+            if (args.bias && n < args.N) {
+                const int64_t at = (int64_t)it.g * args.N + n;
+                bias = args.bias_f32 ? __ldg(static_cast<const float*>(args.bias) + at)
+                       : args.fp16   ? __half2float(static_cast<const __half*>(args.bias)[at])
+                                     : __bfloat162float(static_cast<const __nv_bfloat16*>(args.bias)[at]);
+            }
+            if (args.residual && pc.kb1 == k_blocks && (int)threadIdx.x < it.rows) {
+                // a row of the residual's tile to L2, for the epilogue (8192 x 4096 x 4096:
+                // 267 us without, 183 with, 170 without a residual)
+                const int n0 = it.n0 + (int)rank * BM;
+                const int cols = min(BM, args.N - n0);
+                const OUT* res = static_cast<const OUT*>(args.residual) +
+                                 (int64_t)(it.row0 + (int)threadIdx.x) * args.residual_stride + n0;
+                for (int c = 0; c < cols; c += 128 / (int)sizeof(OUT)) prefetch_l2(res + c);
+                if (cols > 0) prefetch_l2(res + cols - 1);
+            }
             float acc[HALF];
 #pragma unroll
             for (int i = 0; i < HALF; ++i) acc[i] = 0.0f;
-            for (int kb = 0; kb < k_blocks; kb += STRETCH) {
+            for (int kb = pc.kb0; kb < pc.kb1 && ok; kb += STRETCH) {
                 ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&st->tfull[buf]), buf_phase, abort, args.err));
                 if (!ok) break;
                 tc_fence_after();
@@ -364,19 +611,51 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&st->tempty[buf]));
+                if (lane == 0) {
+                    if (PAIR && rank != 0) mbar_arrive_remote_tmem(mapa_shared(smem_u32(&st->tempty[buf]), 0));
+                    else mbar_arrive(smem_u32(&st->tempty[buf]));
+                }
                 if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
             }
-            if (!ok) break;
-            const int n = it.n0 + (warp & 3) * 32 + lane;
-            if (n < args.N) {
-                float bias = 0.0f;
-                if (args.bias) {
-                    const int64_t at = (int64_t)it.g * args.N + n;
-                    bias = args.bias_f32 ? __ldg(static_cast<const float*>(args.bias) + at)
-                           : args.fp16   ? __half2float(static_cast<const __half*>(args.bias)[at])
-                                         : __bfloat162float(static_cast<const __nv_bfloat16*>(args.bias)[at]);
+            if (pc.kb1 - pc.kb0 < k_blocks) {
+                // publish this piece's part and take a ticket; the last piece of the tile
+                // adds the parts up
+                const int64_t stride = (int64_t)plan.part_rows * CG * BM;
+                float* base = args.part + ((int64_t)rank * plan.part_rows + c0) * BM + (warp & 3) * 32 + lane;
+                float* part = base + (2 * unit + (pc.kb0 == 0)) * stride;
+                if (ok) {
+#pragma unroll
+                    for (int c = 0; c < HALF; ++c)
+                        if (c < rows) __stcg(part + c * BM, acc[c]);
                 }
+                const int q = pc.tile - plan.full;
+                int parts;
+                const int first = first_part(plan, q, k_blocks, parts);
+                epilogue_barrier();
+                if (threadIdx.x == 0) {
+                    // the barrier orders the warps' parts before this thread's fence, and the
+                    // fence behind the ticket orders it before the other CTAs' parts are read
+                    int last = 0;
+                    __threadfence();
+                    if (!*abort) {
+                        int32_t* ticket = args.ticket + q * CG + rank;
+                        last = atomicAdd(ticket, 1) == parts - 1;
+                        if (last) *ticket = 0;   // as found, for the next call
+                    }
+                    __threadfence();
+                    st->last = last;
+                }
+                epilogue_barrier();
+                if (!st->last) continue;
+#pragma unroll
+                for (int i = 0; i < HALF; ++i) acc[i] = 0.0f;
+                const float* src = base + 2 * first * stride;
+                if (rows <= 2) add_parts<HALF, 2, 16>(acc, src, rows, parts, stride);
+                else if (rows <= 8) add_parts<HALF, 8, 4>(acc, src, rows, parts, stride);
+                else add_parts<HALF, 32, 1>(acc, src, rows, parts, stride);
+            }
+            if (!ok) continue;
+            if (n < args.N) {
                 OUT* out = static_cast<OUT*>(args.out) + (int64_t)(it.row0 + c0) * args.out_stride + n;
                 const OUT* res = static_cast<const OUT*>(args.residual);
                 if (res) res += (int64_t)(it.row0 + c0) * args.residual_stride + n;
@@ -406,54 +685,91 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     // ---- teardown: every role is done (or has drained after an abort)
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR) {
+        // after an abort, give the copies and commits already issued for this
+        // CTA (some by the other CTA) time to land; then neither CTA leaves
+        // while the other may still use its shared memory or TMEM
+        if (threadIdx.x == 0 && *abort) sleep_ns(1000000);
+        cluster_sync();
+    }
     if (warp == 9) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, C::TMEM_COLS);
+        tmem_dealloc<CG>(tmem_base, C::TMEM_COLS);
     }
 }
 
 constexpr int kMaxDevices = 64;
 
-template <typename OUT, int BN>
+template <typename OUT, bool PAIR, int BN>
 cudaError_t launch(const CUtensorMap& tm_a, const CUtensorMap& tm_a_small, const CUtensorMap& tm_w, const LinearArgs& a,
                    int num_sms, cudaStream_t s)
 {
-    auto kern = linear_kernel<OUT, BN>;
-    constexpr size_t smem = smem_bytes<BN>();
-    // asked of the runtime once per kernel and device
-    static std::atomic<uint64_t> done{0};
+    auto kern = linear_kernel<OUT, PAIR, BN>;
+    constexpr size_t smem = smem_bytes<PAIR, BN>();
+    if (a.tile_rows <= 0 || a.tile_rows > BN || a.tile_rows % Cfg<PAIR, BN>::ROW_STEP) return cudaErrorInvalidValue;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    const uint64_t bit = (uint64_t)1 << dev;
-    if (!(done.load(std::memory_order_acquire) & bit)) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = PAIR ? 2 : 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(PAIR ? num_sms & ~1 : num_sms));
+    cfg.blockDim = dim3(NUM_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    // asked of the runtime once per kernel and device: its shared memory, and how many
+    // pairs can be resident at once (shared memory and the GPCs' SM pairs decide)
+    static std::atomic<int> units[kMaxDevices];
+    int n = units[dev].load(std::memory_order_acquire);
+    if (n <= 0) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
-        done.fetch_or(bit, std::memory_order_release);
+        n = num_sms;
+        if (PAIR) {
+            e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+            if (e != cudaSuccess) return e;
+        }
+        if (n <= 0) return cudaErrorInvalidConfiguration;
+        units[dev].store(n, std::memory_order_release);
     }
-    return launch_pdl(kern, dim3((unsigned)num_sms), dim3(NUM_THREADS), smem, s, tm_a, tm_a_small, tm_w, a);
+    if (PAIR) cfg.gridDim = dim3((unsigned)(2 * (n < num_sms / 2 ? n : num_sms / 2)));
+    cfg.numAttrs = 2;   // the occupancy query above saw the cluster shape only
+    if (!PAIR) {
+        cfg.attrs = attr + 1;
+        cfg.numAttrs = 1;
+    }
+    e = cudaLaunchKernelEx(&cfg, kern, tm_a, tm_a_small, tm_w, a);
+    if (e == cudaSuccess) count_launch();
+    return e;
 }
 
 template <typename OUT>
-cudaError_t launch_out(const CUtensorMap& tm_a, const CUtensorMap& tm_a_small, const CUtensorMap& tm_w,
+cudaError_t launch_out(LinearForm form, const CUtensorMap& tm_a, const CUtensorMap& tm_a_small, const CUtensorMap& tm_w,
                        const LinearArgs& a, int num_sms, cudaStream_t s)
 {
-    if ((int64_t)a.R <= (int64_t)128 * a.G) return launch<OUT, 128>(tm_a, tm_a_small, tm_w, a, num_sms, s);
-    return launch<OUT, 256>(tm_a, tm_a_small, tm_w, a, num_sms, s);
+    return form == kLinearPair ? launch<OUT, true, 256>(tm_a, tm_a_small, tm_w, a, num_sms, s)
+                               : launch<OUT, false, 128>(tm_a, tm_a_small, tm_w, a, num_sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_linear(moe_dtype out_dtype, const CUtensorMap& tm_a, const CUtensorMap& tm_a_small,
+cudaError_t launch_linear(LinearForm form, moe_dtype out_dtype, const CUtensorMap& tm_a, const CUtensorMap& tm_a_small,
                           const CUtensorMap& tm_w, const LinearArgs& a, int num_sms, cudaStream_t s)
 {
     if (a.R == 0) return cudaSuccess;
     if (a.R < 0 || a.G < 1 || a.G > MAX_GROUPS || (!a.offsets && a.G != 1)) return cudaErrorInvalidValue;
     switch (out_dtype) {
-    case MOE_BF16: return launch_out<__nv_bfloat16>(tm_a, tm_a_small, tm_w, a, num_sms, s);
-    case MOE_FP16: return launch_out<__half>(tm_a, tm_a_small, tm_w, a, num_sms, s);
-    case MOE_FP32: return launch_out<float>(tm_a, tm_a_small, tm_w, a, num_sms, s);
+    case MOE_BF16: return launch_out<__nv_bfloat16>(form, tm_a, tm_a_small, tm_w, a, num_sms, s);
+    case MOE_FP16: return launch_out<__half>(form, tm_a, tm_a_small, tm_w, a, num_sms, s);
+    case MOE_FP32: return launch_out<float>(form, tm_a, tm_a_small, tm_w, a, num_sms, s);
     }
     return cudaErrorInvalidValue;
 }

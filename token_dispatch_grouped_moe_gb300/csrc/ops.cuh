@@ -15,8 +15,23 @@ namespace moe {
 
 // ---------------------------------------------------------------- linear --
 
-// The workspace of the product: the error word.
-constexpr size_t kLinearWorkspaceBytes = 256;
+// Cut tiles of the product: their parts together hold at most kLinearPartRows rows
+// of 128 fp32 sums in the workspace; costs in K blocks.
+constexpr int kLinearMaxSplit = 16;
+constexpr int kLinearMaxTickets = 512;
+constexpr int kLinearPartRows = 81920;
+constexpr float kLinearTileCost = 2.0f;
+constexpr float kLinearCutCost = 4.0f;
+constexpr float kLinearJoinCost = 0.05f;
+
+// The workspace of the product: the error word, the tiles' tickets (zero between
+// calls), the parts.
+constexpr size_t kLinearTicketOffset = 256;
+constexpr size_t kLinearPartOffset = 256 + (size_t)kLinearMaxTickets * 4;
+constexpr size_t kLinearWorkspaceBytes = kLinearPartOffset + (size_t)kLinearPartRows * 128 * 4;
+
+// one CTA per MMA, tiles of 128 columns and up to 128 rows; a CTA pair per MMA, 256 and 256
+enum LinearForm { kLinearOne = 0, kLinearPair = 1 };
 
 struct LinearArgs {
     int32_t R;                  // rows of a
@@ -33,6 +48,9 @@ struct LinearArgs {
     int64_t out_stride;
     int32_t fp16;               // operands: fp16, or bf16
     int32_t w_nk;               // the weights' layout: [G, N, K], or [G, K, N]
+    int32_t tile_rows;          // rows of a tile at most
+    int32_t* ticket;            // [kLinearMaxTickets], zero
+    float* part;                // [kLinearPartRows, 128]
     uint32_t* err;
 };
 
@@ -42,7 +60,7 @@ constexpr int kLinearRowBoxSmall = 32;
 
 // tm_a / tm_a_small: a [R, K], boxes of 64 values x 128 / 32 rows; tm_w: [G, K, N],
 // box 64 n x 64 k, or [G, N, K], box 64 k x 128 n. 128-byte swizzle.
-cudaError_t launch_linear(moe_dtype out_dtype, const CUtensorMap& tm_a, const CUtensorMap& tm_a_small,
+cudaError_t launch_linear(LinearForm form, moe_dtype out_dtype, const CUtensorMap& tm_a, const CUtensorMap& tm_a_small,
                           const CUtensorMap& tm_w, const LinearArgs& a, int num_sms, cudaStream_t s);
 
 // A TMA tensor map of 16-bit values, dims innermost first (rank 2 or 3, strides

@@ -736,7 +736,7 @@ class MoEFp8Layer(_Layer):
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # moe_dtype
 SCORES = {"softmax": 0, "sigmoid": 1}                               # moe_scores
 ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}   # moe_activation
-LINEAR_WORKSPACE_ZEROS = 256   # bytes of a workspace that have to be zero before its first use
+LINEAR_WORKSPACE_ZEROS = 2304   # bytes of a workspace that have to be zero before its first use
 
 
 def _one_of(value, table, name):
