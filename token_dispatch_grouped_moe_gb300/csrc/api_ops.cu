@@ -22,10 +22,38 @@ static_assert(kLinearPartOffset == MOE_LINEAR_WORKSPACE_ZEROS, "what has to be z
 
 bool is_dtype(moe_dtype t) { return t == MOE_BF16 || t == MOE_FP16 || t == MOE_FP32; }
 int size_of(moe_dtype t) { return t == MOE_FP32 ? 4 : 2; }
-// The form of a product over R rows in G groups.
+// The estimated cycles of a product in tiles of up to `cap` rows, for groups of equal size.
+float linear_cycles(bool pair, int cap, int64_t R, int32_t K, int32_t N, int32_t G, int sms)
+{
+    const int step = pair ? 32 : 16, cols = pair ? 256 : 128, units = pair ? sms / 2 : sms;
+    if (units <= 0) return INFINITY;
+    const int64_t active = R < G ? R : G, rows = (R + active - 1) / active;
+    const int64_t m_tiles = (rows + cap - 1) / cap, n_tiles = ((int64_t)N + cols - 1) / cols;
+    const int per = (int)(((rows + m_tiles - 1) / m_tiles + step - 1) / step * step);
+    const int64_t tiles = active * m_tiles * n_tiles;
+    if (tiles >= ((int64_t)1 << 31)) return INFINITY;
+    float best = INFINITY;
+    for (int l = 0; l < 32; ++l) {
+        const LinearCandidate c = linear_candidate(pair, l, (int)tiles, (int)(active * n_tiles), per,
+                                                   (K + kLinearBK - 1) / kLinearBK, units);
+        if (c.fits && c.cycles < best) best = c.cycles;
+    }
+    return best;
+}
+
+// The form of a product over R rows in G groups: a pair where its estimate is less by a
+// thirtieth at least; few rows in the form that leaves room for the next kernel's CTA.
+// Measured, one CTA / pair, us, K x N: 4096 x 256, 8192 rows 20.8 / 25.5; 4096 x 1024, 2000
+// 20.5 / 24.4, 4096 35.0 / 27.1; 1024 x 4096, 400 9.8 / 10.5, 700 13.1 / 12.7; 4096 x 4096,
+// 400 20.1 / 22.3, 700 31.8 / 25.4; 4096 x 14336, 100 24.3 / 26.5, 160 39.1 / 27.8; 14336 x
+// 4096, 100 30.0 / 40.7, 160 42.4 / 40.0; 64 groups 2048 x 1408, 128 each 69.1 / 80.3, 180
+// 94.6 / 78.9. Up to 32 / 128 rows, one CTA: 1 row 4096 x 14336 23.5 / 24.1, 8 rows 4096 x
+// 4096 9.5 / 10.4, 14336 x 4096 24.0 / 23.7, 32 rows 1024 x 4096 8.3 / 7.1.
 LinearForm linear_form(int64_t R, int32_t K, int32_t N, int32_t G, int sms)
 {
-    return N > 128 && R > (int64_t)128 * G ? kLinearPair : kLinearOne;
+    if (G == 1 && R <= 16) return kLinearFew;
+    const bool pair = linear_cycles(true, 256, R, K, N, G, sms) * (30.0f / 29.0f) < linear_cycles(false, 128, R, K, N, G, sms);
+    return pair ? kLinearPair : kLinearOne;
 }
 
 bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
@@ -123,7 +151,7 @@ moe_status moe_linear(int64_t R, int32_t K, int32_t N, int32_t G, moe_dtype dtyp
     args.part = reinterpret_cast<float*>(b + kLinearPartOffset);
     args.err = static_cast<uint32_t*>(ws);
     const LinearForm form = linear_form(R, K, N, G, sms);
-    args.tile_rows = form == kLinearOne ? 128 : 256;
+    args.tile_rows = form == kLinearFew ? 32 : form == kLinearOne ? 128 : 256;
     return finish(launch_linear(form, out_dtype, tm_a, tm_a_small, tm_w, args, sms, (cudaStream_t)stream), ws,
                   (cudaStream_t)stream);
 }

@@ -20,8 +20,12 @@
 // Kernel shape: one CTA per SM (384 threads), persistent over (group, row tile, n
 // tile) tiles computed from the group offsets:
 //   warps 0..7  epilogue: warp w reads TMEM lanes 32 (w mod 4) .. + 31 (columns n,
-//               one a thread) and half of the rows;
-//   warp 8      TMA producer; warp 9 TMEM allocator and MMA issuer.
+//               one a thread) and half of the rows (up to 32 rows: warps 0..3, all);
+//   the others  TMEM allocator and MMA issuer; three TMA producers, every third K
+//               block each: the wait, the barrier's bytes and three to six copies take
+//               one thread 650-850 cycles, more than the block's MMAs (one producer:
+//               8192 x 4096 x 4096 161 us instead of 150, 16384 rows of 8 experts 4096 ->
+//               14336 1260 instead of 1120).
 // CTA pairs (PAIR): a 2-CTA cluster shares one tcgen05.mma.cta_group::2 of 256
 // columns n, each CTA staging its 128 of them and half of the rows; both CTAs'
 // boxes complete on rank 0's barrier, rank 0 issues, its commits arrive in both CTAs,
@@ -34,6 +38,7 @@
 // Every wait is bounded (ptx.cuh).
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -50,22 +55,26 @@ constexpr int BM = 128;             // columns of the output that a CTA has of a
 constexpr int BK = kLinearBK;
 constexpr int W_BYTES = BM * BK * 2;
 constexpr int STRETCH = 8;          // k blocks between two reads of TMEM
-constexpr int EPI_WARPS = 8;
-constexpr int NUM_THREADS = 32 * EPI_WARPS + 128;
-// registers: 12 warps are launched with 168 each; the epilogue warps (up to 128
-// sums and 64 loads in flight) take 216 once the other warpgroup has gone down to
-// 72 (8 * 216 + 4 * 72 = 12 * 168)
+constexpr int PRODUCERS = 3;
+// registers with 8 epilogue warps: 12 warps are launched with 168 each; the epilogue
+// warps (up to 128 sums and 64 loads in flight) take 216 once the other warpgroup has
+// gone down to 72 (8 * 216 + 4 * 72 = 12 * 168)
 constexpr int EPI_REGS = 216;
 constexpr int OTHER_REGS = 72;
 constexpr int MAX_GROUPS = 256;
 constexpr int BAND = 16;            // row tiles that are taken together
 
-// BN: rows of a tile at most.
+// BN: rows of a tile at most. The form for few rows (32) leaves room for a second
+// CTA on its SM: that of the next kernel, which gets ready meanwhile.
 template <bool PAIR, int BN>
 struct Cfg {
+    static constexpr int EPI_WARPS = BN <= 32 ? 4 : 8;
+    static constexpr int HALF = BN / (EPI_WARPS / 4);           // rows of an epilogue thread
+    static constexpr int NUM_THREADS = 32 * EPI_WARPS + 128;
+    static constexpr int CTAS = BN <= 32 ? 2 : 1;               // that fit on an SM
     static constexpr int A_ROWS = PAIR ? BN / 2 : BN;           // rows that a CTA stages
     static constexpr int STAGE_BYTES = W_BYTES + A_ROWS * BK * 2;
-    static constexpr int STAGES = 6;
+    static constexpr int STAGES = BN <= 32 ? 5 : 6;
     static constexpr int TMEM_COLS = 2 * BN;                    // two buffers
     static constexpr int TILE_N = PAIR ? 2 * BM : BM;           // columns of one work item
     static constexpr int ROW_STEP = PAIR ? 32 : 16;             // the MMA's N is a multiple of this
@@ -80,7 +89,7 @@ struct Tile {
 // that begins or ends inside a tile computes a part of its sums.
 struct Plan {
     int tiles, full, segments;
-    int part_rows;   // rows a part has room for: those of the fullest tile
+    int part_rows;   // rows a part has room for: those of the fullest tile, in 32s
 };
 
 template <int STAGES>
@@ -94,6 +103,7 @@ struct SmemTail {
     int abort;
     int last;                          // cut tiles: this CTA took the tile's last ticket
     int most_rows;                     // rows of the fullest tile
+    int groups;                        // that have rows
     int tile_start[MAX_GROUPS + 1];    // row tiles before each group
     int offsets[MAX_GROUPS + 1];
 };
@@ -104,7 +114,8 @@ constexpr size_t smem_bytes()
     using C = Cfg<PAIR, BN>;
     return 1024 + (size_t)C::STAGES * C::STAGE_BYTES + sizeof(SmemTail<C::STAGES>);
 }
-static_assert(smem_bytes<false, 128>() <= 227 * 1024 && smem_bytes<true, 256>() <= 227 * 1024, "shared memory");
+static_assert(smem_bytes<false, 32>() <= 113 * 1024 && smem_bytes<false, 128>() <= 227 * 1024 &&
+                  smem_bytes<true, 256>() <= 227 * 1024, "shared memory");
 
 // A group's rows are spread evenly over its row tiles.
 template <int STEP>
@@ -184,72 +195,55 @@ __device__ __forceinline__ int first_part(const Plan& p, int q, int k_blocks, in
     return first;
 }
 
-// The plan with the least estimated time, counted in K blocks of one CTA, one
-// candidate a lane (the warp calls it together): lane 0 every tile whole; lane l the
-// tiles, where they fill less than one round, in l + 1 parts each; lane 31 the tiles
-// beyond the whole rounds but one (or all of them) in equal runs. Cutting costs the
-// parts' publication, twice where the runs do not line up with tiles, and the join's
-// trips to L2.
-template <int CG>
-__device__ __forceinline__ Plan make_plan(int tiles, int rows, int k_blocks, int n_units, int lane)
+// The plan with the least estimated time (linear_candidate), one candidate a lane; the
+// warp calls it together.
+template <bool PAIR>
+__device__ __forceinline__ Plan make_plan(int tiles, int w_tiles, int rows, int k_blocks, int n_units, int lane)
 {
-    // parts have room, and the products of Walk and first_part stay below 2^32
-    const bool room = 2 * n_units * CG * rows <= kLinearPartRows && 2 * n_units * CG <= kLinearMaxTickets &&
-                      k_blocks < (1 << 30) / (n_units * n_units);
-    const int rounds = (int)((unsigned)tiles / (unsigned)n_units);
-    const int last = tiles - rounds * n_units;
-    const float whole = (float)k_blocks + kLinearTileCost;
-    int full = tiles, segments = 0;
-    float cost = (float)(rounds + (last > 0)) * whole;
-    bool fits = lane == 0;
-    if (lane > 0 && room && tiles > 0) {
-        const bool even = lane < 31;
-        const int whole_rounds = !even && rounds > 1 ? rounds - 1 : 0;
-        fits = even ? rounds == 0 && lane < kLinearMaxSplit && tiles * (lane + 1) <= n_units : last > 0;
-        if (fits) {
-            full = whole_rounds * n_units;
-            segments = even ? tiles * (lane + 1) : n_units;
-            const uint32_t left = (uint32_t)(tiles - full);   // below 2 n_units
-            const uint32_t total = left * (uint32_t)k_blocks;
-            const int parts = even ? lane + 1 : (int)((unsigned)n_units / left) + 2;
-            fits = total >= 2u * (uint32_t)segments;
-            cost = (float)whole_rounds * whole + __fdividef((float)total, (float)segments) + 0.5f +
-                   (even ? 1.0f : 2.0f) * kLinearCutCost + kLinearJoinCost * (float)(rows * parts);
-        }
-    }
+    const LinearCandidate c = linear_candidate(PAIR, lane, tiles, w_tiles, rows, k_blocks, n_units);
     // the least cost (its low bits give way to the lane)
-    const uint32_t key = fits ? (__float_as_uint(cost) & ~31u) | (uint32_t)lane : 0xffffffffu;
+    const uint32_t key = c.fits ? (__float_as_uint(c.cycles) & ~31u) | (uint32_t)lane : 0xffffffffu;
     const int best = (int)(__reduce_min_sync(0xffffffffu, key) & 31u);
-    return Plan{tiles, __shfl_sync(0xffffffffu, full, best), __shfl_sync(0xffffffffu, segments, best), rows};
+    return Plan{tiles, __shfl_sync(0xffffffffu, c.full, best), __shfl_sync(0xffffffffu, c.segments, best),
+                linear_part_rows(rows)};
 }
 
+template <int WARPS>
 __device__ __forceinline__ void epilogue_barrier()   // the epilogue warps only
 {
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * EPI_WARPS) : "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory");
 }
 
-// Adds this thread's rows c < rows of a tile's parts to acc, in the parts' order: a
-// row of a part is BM floats, one a column (src: this thread's column of its row 0).
-// ROWS rows of PARTS parts are in flight together (each a trip to L2).
+// Adds this thread's rows c < rows of the parts s0 .. s1 - 1 of a tile to acc, in
+// order: a row of a part is BM floats, one a column (src: this thread's column of the
+// row 0 of slot 2 first). ROWS rows of PARTS parts are in flight together (each a
+// trip to L2).
 template <int HALF, int ROWS, int PARTS>
-__device__ __forceinline__ void add_parts(float (&acc)[HALF], const float* src, int rows, int parts, int64_t stride)
+__device__ __forceinline__ void add_parts(float (&acc)[HALF], const float* src, int rows, int begin, int end,
+                                          int64_t stride)
 {
     // the first part begins with the tile, the others inside it (first_part)
     auto slot = [&](int s) { return (int64_t)(s == 0 ? 1 : 2 * s) * stride; };
 #pragma unroll
     for (int c = 0; c < (ROWS < 32 ? ROWS : HALF); c += ROWS) {
         if (c >= rows) break;
-        for (int s0 = 0; s0 < parts; s0 += PARTS) {
+        for (int s0 = begin; s0 < end; s0 += PARTS) {
+            // (no branch between the loads, which would make them wait for one another: rows
+            // past the last are read as they are, a part has room for a multiple of 32; parts
+            // past the last are the last again)
             float v[PARTS][ROWS];
 #pragma unroll
+            for (int s = 0; s < PARTS; ++s) {
+                const float* part = src + slot(min(s0 + s, end - 1));
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i) v[s][i] = __ldcg(part + (c + i) * BM);
+            }
+#pragma unroll
             for (int s = 0; s < PARTS; ++s)
+                if (s0 + s < end) {
 #pragma unroll
-                for (int i = 0; i < ROWS; ++i)
-                    v[s][i] = s0 + s < parts && c + i < rows ? __ldcg(src + slot(s0 + s) + (c + i) * BM) : 0.0f;
-#pragma unroll
-            for (int s = 0; s < PARTS; ++s)
-#pragma unroll
-                for (int i = 0; i < ROWS; ++i) acc[c + i] += v[s][i];
+                    for (int i = 0; i < ROWS; ++i) acc[c + i] += v[s][i];
+                }
         }
     }
 }
@@ -318,15 +312,45 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const void* map, int c0, i
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-__device__ __forceinline__ float as_float(float v) { return v; }
-__device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float as_float(__half v) { return __half2float(v); }
+// A value's bits in a register, and what they are.
+__device__ __forceinline__ uint32_t load_raw(const float* p)
+{
+    uint32_t r;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(r) : "l"(p) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint32_t load_raw(const void* p)
+{
+    uint32_t r;
+    asm volatile("ld.global.u16 %0, [%1];" : "=r"(r) : "l"(p) : "memory");
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ float of_raw(uint32_t r)
+{
+    if constexpr (sizeof(T) == 4) return __uint_as_float(r);
+    else if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half((unsigned short)r));
+    else return __uint_as_float(r << 16);
+}
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
 
+// The rows of this CTA's part of a tile of the residual to L2, a thread a row.
+template <typename OUT, int EPI_THREADS>
+__device__ __forceinline__ void prefetch_residual(const LinearArgs& args, const Tile& it, uint32_t rank)
+{
+    const int n0 = it.n0 + (int)rank * BM, cols = min(BM, args.N - n0);
+    if (cols <= 0) return;
+    for (int r = threadIdx.x; r < it.rows; r += EPI_THREADS) {
+        const OUT* res = static_cast<const OUT*>(args.residual) + (int64_t)(it.row0 + r) * args.residual_stride + n0;
+        for (int c = 0; c < cols; c += 128 / (int)sizeof(OUT)) prefetch_l2(res + c);
+        prefetch_l2(res + cols - 1);
+    }
+}
+
 template <typename OUT, bool PAIR, int BN>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(Cfg<PAIR, BN>::NUM_THREADS, Cfg<PAIR, BN>::CTAS)
 linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_a_small,
               const __grid_constant__ CUtensorMap tm_w, const LinearArgs args)
 {
@@ -334,7 +358,8 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t tiles_addr = (raw_addr + 1023u) & ~1023u;
     using C = Cfg<PAIR, BN>;
-    constexpr int HALF = BN / 2;       // rows of an epilogue thread
+    constexpr int EPI_WARPS = C::EPI_WARPS;
+    constexpr int HALF = C::HALF;
     constexpr int STAGES = C::STAGES;
     constexpr int CG = PAIR ? 2 : 1;   // tcgen05 CTA group
     SmemTail<STAGES>* st =
@@ -360,12 +385,12 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         st->abort = 0;
         fence_barrier_init();
     }
-    if (warp == 8 && lane == 0) {
+    if (warp == EPI_WARPS && lane == 0) {
         tma_prefetch_desc(&tm_a);
         tma_prefetch_desc(&tm_a_small);
         tma_prefetch_desc(&tm_w);
     }
-    if (warp == 9) {
+    if (warp == EPI_WARPS + 1) {
         tmem_alloc<CG>(smem_u32(&st->tmem_base), C::TMEM_COLS);
         tmem_relinquish<CG>();
     }
@@ -385,7 +410,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         }
         bool good = true;
         int tiles[PER], sum = 0;
-        int most = 0;   // rows of the fullest tile
+        int most = 0, groups = 0;   // rows of the fullest tile; groups that have rows
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             tiles[i] = 0;
@@ -396,6 +421,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                     tiles[i] = (int)((unsigned)(rows + args.tile_rows - 1) / (unsigned)args.tile_rows);
                     most = max(most, rows_per_tile<C::ROW_STEP>(rows, tiles[i]));
                     sum += tiles[i];
+                    ++groups;
                 }
             }
         }
@@ -416,10 +442,12 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             }
         good = __all_sync(0xffffffffu, good);
         most = __reduce_max_sync(0xffffffffu, most);
+        groups = __reduce_add_sync(0xffffffffu, groups);
         const int all = __shfl_sync(0xffffffffu, incl, 31);
         if (lane == 0) {
             st->tile_start[G] = good ? all : 0;
             st->most_rows = most;
+            st->groups = groups;
             if (!good) report_error(args.err, MOE_DEV_ERR_BOUNDS);
         }
     }
@@ -431,28 +459,30 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     const uint32_t tmem_base = st->tmem_base;
     const int n_tiles = (args.N + C::TILE_N - 1) / C::TILE_N;
     const int k_blocks = (args.K + BK - 1) / BK;
-    const Plan plan = make_plan<CG>(st->tile_start[G] * n_tiles, st->most_rows, k_blocks, n_units, lane);
+    const Plan plan = make_plan<PAIR>(st->tile_start[G] * n_tiles, st->groups * n_tiles, st->most_rows, k_blocks, n_units, lane);
     volatile int* abort = &st->abort;
     auto decode = [&](int tile) {
         return decode_tile<C::TILE_N, C::ROW_STEP>(tile, n_tiles, st->tile_start, st->offsets, G);
     };
 
-    if (warp >= 8) {
-        setmaxnreg_dec<OTHER_REGS>();
-        if (warp == 8) {
-            // ============================ TMA producer ============================
+    if (warp >= EPI_WARPS) {
+        if constexpr (EPI_WARPS == 8) setmaxnreg_dec<OTHER_REGS>();
+        if (warp != EPI_WARPS + 1) {
+            // ============================ TMA producers ============================
             if (lane == 0) {
-                int stage = 0;
+                const int turn = max(0, warp - EPI_WARPS - 1);   // of the K blocks, counted over all pieces
+                int stage = turn;
                 uint32_t phase = 0;
                 int issued = 0;
+                int skip = turn;                                 // blocks before this producer's next one
                 bool ok = true;
                 Walk walk(plan, unit, n_units, k_blocks);
                 Piece pc;
                 bool more = walk.next(pc);
                 Tile it = more ? decode(pc.tile) : Tile{0, 0, 0, 0};
                 if (!args.offsets) pdl_wait();
-                for (; ok && more; more = walk.next(pc)) {
-                    if (issued) it = decode(pc.tile);
+                for (bool first = true; ok && more; more = walk.next(pc), first = false) {
+                    if (!first) it = decode(pc.tile);
                     // this CTA's rows: boxes of 128, then of 32 up to the last one that the MMA
                     // reads (a pair: each CTA its half of them)
                     const int rows = PAIR ? (it.rows + 31) / 32 * 16 : it.rows;
@@ -461,7 +491,8 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                     const int large = rows / kLinearRowBox;
                     const int small = (rows - large * kLinearRowBox + kLinearRowBoxSmall - 1) / kLinearRowBoxSmall;
                     const uint32_t bytes = W_BYTES + (uint32_t)(large * kLinearRowBox + small * kLinearRowBoxSmall) * BK * 2;
-                    for (int kb = pc.kb0; kb < pc.kb1; ++kb) {
+                    int kb = pc.kb0 + skip;
+                    for (; kb < pc.kb1; kb += PRODUCERS) {
                         if (!mbar_wait(smem_u32(&st->empty[stage]), phase ^ 1u, abort, args.err)) {
                             ok = false;
                             break;
@@ -483,19 +514,20 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                         for (int i = 0; i < small; ++i, row += kLinearRowBoxSmall, a_dst += kLinearRowBoxSmall * BK * 2)
                             load_2d<PAIR>(a_dst, &tm_a_small, kb * BK, row, full);
                         ++issued;
-                        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                        if ((stage += PRODUCERS) >= STAGES) { stage -= STAGES; phase ^= 1u; }
                     }
+                    skip = kb - pc.kb1;
                 }
                 if (!PAIR && !ok) {
                     // drain: wait (bounded) for the loads still in flight
-                    for (int i = 0; i < min(issued, STAGES); ++i) {
-                        if (stage == 0) { stage = STAGES - 1; phase ^= 1u; } else { --stage; }
+                    for (int i = 0; i < min(issued, (STAGES + PRODUCERS - 1) / PRODUCERS); ++i) {
+                        if ((stage -= PRODUCERS) < 0) { stage += STAGES; phase ^= 1u; }
                         mbar_wait_drain(smem_u32(&st->full[stage]), phase);
                     }
                 }
             }
             __syncwarp();
-        } else if (warp == 9) {
+        } else {
             // ============================ MMA issuer ==============================
             // the whole warp walks the pieces and waits (uniform control flow, so the
             // descriptors stay in uniform registers); one elected lane issues (a
@@ -558,11 +590,11 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         if (!args.offsets) pdl_wait();
         pdl_launch_dependents();
     } else {
-        setmaxnreg_inc<EPI_REGS>();
+        if constexpr (EPI_WARPS == 8) setmaxnreg_inc<EPI_REGS>();
         if (!args.offsets) pdl_wait();
         pdl_launch_dependents();
         // ============================== epilogue ==============================
-        const int c0 = (warp >> 2) * HALF;             // this thread's rows of the tile
+        const int c0 = (warp >> 2) * HALF;             // this thread's rows of the tile (from)
         const uint32_t t_row = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + c0;
         int buf = 0;
         uint32_t buf_phase = 0;
@@ -581,19 +613,27 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                        : args.fp16   ? __half2float(static_cast<const __half*>(args.bias)[at])
                                      : __bfloat162float(static_cast<const __nv_bfloat16*>(args.bias)[at]);
             }
-            if (args.residual && pc.kb1 == k_blocks && (int)threadIdx.x < it.rows) {
-                // a row of the residual's tile to L2, for the epilogue (8192 x 4096 x 4096:
-                // 267 us without, 183 with, 170 without a residual)
-                const int n0 = it.n0 + (int)rank * BM;
-                const int cols = min(BM, args.N - n0);
-                const OUT* res = static_cast<const OUT*>(args.residual) +
-                                 (int64_t)(it.row0 + (int)threadIdx.x) * args.residual_stride + n0;
-                for (int c = 0; c < cols; c += 128 / (int)sizeof(OUT)) prefetch_l2(res + c);
-                if (cols > 0) prefetch_l2(res + cols - 1);
-            }
+            const bool whole = pc.kb1 - pc.kb0 == k_blocks;
+            // without an activation the sums begin with the residual, whose loads pass while
+            // the tensor cores work; else it is added at the end, from L2, where it is asked
+            // for now (8192 x 4096 x 4096, us: 149 without a residual, 168 with; silu 158 and
+            // 184)
+            const bool early = args.residual && whole && args.act == MOE_ACT_NONE;
+            if (args.residual && !early && pc.kb1 == k_blocks) prefetch_residual<OUT, 32 * EPI_WARPS>(args, it, rank);
+            const int q = pc.tile - plan.full;         // of a cut tile: its number and parts
+            int parts = 0;
+            const int first = whole ? 0 : first_part(plan, q, k_blocks, parts);
             float acc[HALF];
 #pragma unroll
             for (int i = 0; i < HALF; ++i) acc[i] = 0.0f;
+            if (early && n < args.N && rows > 0) {
+                const OUT* res = static_cast<const OUT*>(args.residual) + (int64_t)(it.row0 + c0) * args.residual_stride + n;
+                uint32_t raw[HALF];   // all loads before the first use, without a branch between them
+#pragma unroll
+                for (int c = 0; c < HALF; ++c) raw[c] = load_raw(res + min(c, rows - 1) * args.residual_stride);
+#pragma unroll
+                for (int c = 0; c < HALF; ++c) acc[c] = of_raw<OUT>(raw[c]);
+            }
             for (int kb = pc.kb0; kb < pc.kb1 && ok; kb += STRETCH) {
                 ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&st->tfull[buf]), buf_phase, abort, args.err));
                 if (!ok) break;
@@ -617,7 +657,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                 }
                 if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
             }
-            if (pc.kb1 - pc.kb0 < k_blocks) {
+            if (!whole) {
                 // publish this piece's part and take a ticket; the last piece of the tile
                 // adds the parts up
                 const int64_t stride = (int64_t)plan.part_rows * CG * BM;
@@ -628,10 +668,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                     for (int c = 0; c < HALF; ++c)
                         if (c < rows) __stcg(part + c * BM, acc[c]);
                 }
-                const int q = pc.tile - plan.full;
-                int parts;
-                const int first = first_part(plan, q, k_blocks, parts);
-                epilogue_barrier();
+                epilogue_barrier<EPI_WARPS>();
                 if (threadIdx.x == 0) {
                     // the barrier orders the warps' parts before this thread's fence, and the
                     // fence behind the ticket orders it before the other CTAs' parts are read
@@ -645,37 +682,44 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                     __threadfence();
                     st->last = last;
                 }
-                epilogue_barrier();
+                epilogue_barrier<EPI_WARPS>();
                 if (!st->last) continue;
-#pragma unroll
-                for (int i = 0; i < HALF; ++i) acc[i] = 0.0f;
                 const float* src = base + 2 * first * stride;
-                if (rows <= 2) add_parts<HALF, 2, 16>(acc, src, rows, parts, stride);
-                else if (rows <= 8) add_parts<HALF, 8, 4>(acc, src, rows, parts, stride);
-                else add_parts<HALF, 32, 1>(acc, src, rows, parts, stride);
+                // the sum of two parts does not depend on their order: the other one is added
+                // to this CTA's
+                const int mine = unit - first;
+                const int begin = parts == 2 ? 1 - mine : 0, end = parts == 2 ? 2 - mine : parts;
+                if (parts != 2) {
+#pragma unroll
+                    for (int i = 0; i < HALF; ++i) acc[i] = 0.0f;
+                }
+                if (rows <= 2) add_parts<HALF, 2, 8>(acc, src, rows, begin, end, stride);
+                else if (rows <= 8) add_parts<HALF, 8, 4>(acc, src, rows, begin, end, stride);
+                else add_parts<HALF, 32, HALF == 128 ? 1 : 2>(acc, src, rows, begin, end, stride);
             }
             if (!ok) continue;
             if (n < args.N) {
                 OUT* out = static_cast<OUT*>(args.out) + (int64_t)(it.row0 + c0) * args.out_stride + n;
-                const OUT* res = static_cast<const OUT*>(args.residual);
+                const OUT* res = early ? nullptr : static_cast<const OUT*>(args.residual);
                 if (res) res += (int64_t)(it.row0 + c0) * args.residual_stride + n;
+                // CHUNK rows at a time (few rows: no more code is fetched than they need)
+                constexpr int CHUNK = HALF <= 32 ? 4 : 32;
 #pragma unroll
-                for (int c = 0; c < HALF; c += 32) {
+                for (int c = 0; c < HALF; c += CHUNK) {
                     if (c >= rows) break;
-                    float v[32];
+                    float v[CHUNK];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = acc[c + i] + bias;
+                    for (int i = 0; i < CHUNK; ++i) v[i] = acc[c + i] + bias;
                     activate(v, args.act);
                     if (res) {
-                        OUT r[32];
+                        uint32_t r[CHUNK];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c + i < rows) r[i] = res[(c + i) * args.residual_stride];
+                        for (int i = 0; i < CHUNK; ++i) r[i] = load_raw(res + min(c + i, rows - 1) * args.residual_stride);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] += as_float(r[i]);
+                        for (int i = 0; i < CHUNK; ++i) v[i] += of_raw<OUT>(r[i]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
+                    for (int i = 0; i < CHUNK; ++i)
                         if (c + i < rows) put(out + (c + i) * args.out_stride, v[i]);
                 }
             }
@@ -692,7 +736,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         if (threadIdx.x == 0 && *abort) sleep_ns(1000000);
         cluster_sync();
     }
-    if (warp == 9) {
+    if (warp == EPI_WARPS + 1) {
         tc_fence_after();
         tmem_dealloc<CG>(tmem_base, C::TMEM_COLS);
     }
@@ -720,7 +764,7 @@ cudaError_t launch(const CUtensorMap& tm_a, const CUtensorMap& tm_a_small, const
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(PAIR ? num_sms & ~1 : num_sms));
-    cfg.blockDim = dim3(NUM_THREADS);
+    cfg.blockDim = dim3(Cfg<PAIR, BN>::NUM_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
@@ -755,8 +799,12 @@ template <typename OUT>
 cudaError_t launch_out(LinearForm form, const CUtensorMap& tm_a, const CUtensorMap& tm_a_small, const CUtensorMap& tm_w,
                        const LinearArgs& a, int num_sms, cudaStream_t s)
 {
-    return form == kLinearPair ? launch<OUT, true, 256>(tm_a, tm_a_small, tm_w, a, num_sms, s)
-                               : launch<OUT, false, 128>(tm_a, tm_a_small, tm_w, a, num_sms, s);
+    switch (form) {
+    case kLinearFew: return launch<OUT, false, 32>(tm_a, tm_a_small, tm_w, a, num_sms, s);
+    case kLinearOne: return launch<OUT, false, 128>(tm_a, tm_a_small, tm_w, a, num_sms, s);
+    case kLinearPair: return launch<OUT, true, 256>(tm_a, tm_a_small, tm_w, a, num_sms, s);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace

@@ -15,14 +15,82 @@ namespace moe {
 
 // ---------------------------------------------------------------- linear --
 
+constexpr int kLinearBK = 64;        // K of a pipeline stage: one 128-byte swizzle span
+constexpr int kLinearRowBox = 128;   // rows of a large and a small box of a
+constexpr int kLinearRowBoxSmall = 32;
+
 // Cut tiles of the product: their parts together hold at most kLinearPartRows rows
-// of 128 fp32 sums in the workspace; costs in K blocks.
+// of 128 fp32 sums in the workspace.
 constexpr int kLinearMaxSplit = 16;
 constexpr int kLinearMaxTickets = 512;
 constexpr int kLinearPartRows = 81920;
-constexpr float kLinearTileCost = 2.0f;
-constexpr float kLinearCutCost = 4.0f;
-constexpr float kLinearJoinCost = 0.05f;
+
+// What the plan and the form are chosen by, in cycles. A K block (64) of a tile of r
+// rows: shared memory passes the operands twice (128 bytes a cycle), 128 columns and r
+// rows of one CTA, or r / 2 of each of a pair; that is more than the MMAs' own time for
+// fewer than 256 rows of a pair, and for any of one CTA. Measured (cycles a block):
+// pair, 256 rows 520; one CTA, 128 rows 480. Where every tile of the weights is read
+// once, from memory, a CTA has no more than its stages in flight: 520.
+constexpr float kLinearBytesPerCycle = 3580.0f;   // of the memory (6.8 TB/s at 1.9 GHz)
+inline __host__ __device__ float linear_block_cycles(bool pair, int rows, bool streamed)
+{
+    const float block = 256.0f + (pair ? 1.0f : 2.0f) * (float)rows;
+    return streamed && block < 520.0f ? 520.0f : block;
+}
+// Publishing and joining the parts of a cut tile (measured: 128 rows in two parts on one
+// CTA 10000 cycles, 256 on a pair 24000).
+inline __host__ __device__ float linear_cut_cycles(bool pair, int rows, int parts, bool even)
+{
+    return (pair ? 1.5f : 1.0f) *
+           ((even ? 1.0f : 2.0f) * (2500.0f + 20.0f * (float)rows) + 1500.0f + 13.0f * (float)(rows * parts));
+}
+inline __host__ __device__ int linear_part_rows(int rows) { return (rows + 31) / 32 * 32; }
+
+// A way to run `tiles` tiles of up to `rows` rows on n_units CTAs (or pairs): the first
+// `full` whole, the K blocks of the rest in `segments` equal runs. Candidate 0: every
+// tile whole; l: the tiles, where they fill less than one round, in l + 1 parts each;
+// 31: the tiles beyond the whole rounds but one (or all of them) in equal runs. None
+// is faster than the w_tiles different tiles of the weights come from memory: where
+// they bound the product, the CTAs that have a tile of a round that is not full get the
+// memory's whole rate, up to what a CTA has in flight. Cutting costs the parts'
+// publication, twice where the runs do not line up with tiles, and the join's trips to L2.
+struct LinearCandidate {
+    bool fits;
+    int full, segments;
+    float cycles;
+};
+inline __host__ __device__ LinearCandidate linear_candidate(bool pair, int l, int tiles, int w_tiles, int rows,
+                                                            int k_blocks, int n_units)
+{
+    const int cg = pair ? 2 : 1;
+    const int rounds = (int)((unsigned)tiles / (unsigned)n_units), last = tiles - rounds * n_units;
+    const float block = linear_block_cycles(pair, rows, w_tiles == tiles);
+    const float bytes = (float)w_tiles * (float)k_blocks * (float)(cg * 128 * kLinearBK * 2) * (1.0f / kLinearBytesPerCycle);
+    LinearCandidate c{l == 0, tiles, 0, 0.0f};
+    if (l == 0) {
+        const float whole = tiles ? bytes * ((float)(tiles - last) / (float)tiles) : 0.0f;
+        const float run = (float)rounds * (float)k_blocks * block;
+        c.cycles = run > whole ? run : whole;
+        if (last) c.cycles += bytes - whole > (float)k_blocks * block ? bytes - whole : (float)k_blocks * block;
+        return c;
+    }
+    // parts have room, and the products of the schedule stay below 2^32
+    if (tiles == 0 || 2 * n_units * cg * linear_part_rows(rows) > kLinearPartRows || 2 * n_units * cg > kLinearMaxTickets ||
+        k_blocks >= (1 << 30) / (n_units * n_units))
+        return c;
+    const bool even = l < 31;
+    if (even ? rounds > 0 || l >= kLinearMaxSplit || tiles * (l + 1) > n_units : last == 0) return c;
+    const int whole_rounds = !even && rounds > 1 ? rounds - 1 : 0;
+    c.full = whole_rounds * n_units;
+    c.segments = even ? tiles * (l + 1) : n_units;
+    const unsigned left = (unsigned)(tiles - c.full);   // below 2 n_units
+    const unsigned total = left * (unsigned)k_blocks;
+    const int parts = even ? l + 1 : (int)((unsigned)n_units / left) + 2;
+    c.fits = total >= 2u * (unsigned)c.segments;
+    const float run = ((float)(whole_rounds * k_blocks) + (float)total / (float)c.segments + 0.5f) * block;
+    c.cycles = (run > bytes ? run : bytes) + linear_cut_cycles(pair, rows, parts, even);
+    return c;
+}
 
 // The workspace of the product: the error word, the tiles' tickets (zero between
 // calls), the parts.
@@ -30,8 +98,8 @@ constexpr size_t kLinearTicketOffset = 256;
 constexpr size_t kLinearPartOffset = 256 + (size_t)kLinearMaxTickets * 4;
 constexpr size_t kLinearWorkspaceBytes = kLinearPartOffset + (size_t)kLinearPartRows * 128 * 4;
 
-// one CTA per MMA, tiles of 128 columns and up to 128 rows; a CTA pair per MMA, 256 and 256
-enum LinearForm { kLinearOne = 0, kLinearPair = 1 };
+// one CTA per MMA, tiles of 128 columns and up to 32 or 128 rows; a CTA pair per MMA, 256 and 256
+enum LinearForm { kLinearFew = 0, kLinearOne = 1, kLinearPair = 2 };
 
 struct LinearArgs {
     int32_t R;                  // rows of a
@@ -53,10 +121,6 @@ struct LinearArgs {
     float* part;                // [kLinearPartRows, 128]
     uint32_t* err;
 };
-
-constexpr int kLinearBK = 64;        // K of a pipeline stage: one 128-byte swizzle span
-constexpr int kLinearRowBox = 128;   // rows of a large and a small box of a
-constexpr int kLinearRowBoxSmall = 32;
 
 // tm_a / tm_a_small: a [R, K], boxes of 64 values x 128 / 32 rows; tm_w: [G, K, N],
 // box 64 n x 64 k, or [G, N, K], box 64 k x 128 n. 128-byte swizzle.
