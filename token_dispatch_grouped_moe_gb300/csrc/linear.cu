@@ -12,10 +12,11 @@
 // form serves a token of a decode step and a prefill. The operands are read as
 // they lie in memory: w with contiguous n (an M-major operand) or contiguous k.
 //
-// The tensor cores' running sum is cut every 512 k: the epilogue warps add each
-// stretch to fp32 registers while the next one is computed into the other TMEM
-// buffer (its 32 partial sums rounded towards zero are far below a bf16 step; of
-// thousands they would not be below fp32's).
+// The tensor cores' running sum is cut every 2048 k (512 for fp32 outputs): the
+// epilogue warps add each stretch to fp32 registers while the next one is computed
+// into the other TMEM buffer. Its 128 partial sums of 16 products, rounded towards
+// zero, are off by 4e-6 of the result at most times, far below a 16-bit step; those
+// of 32 by 5e-7, as a sum in fp32 is.
 //
 // Kernel shape: one CTA per SM (384 threads), persistent over (group, row tile, n
 // tile) tiles computed from the group offsets:
@@ -54,7 +55,6 @@ namespace {
 constexpr int BM = 128;             // columns of the output that a CTA has of a tile
 constexpr int BK = kLinearBK;
 constexpr int W_BYTES = BM * BK * 2;
-constexpr int STRETCH = 8;          // k blocks between two reads of TMEM
 constexpr int PRODUCERS = 3;
 // registers with 8 epilogue warps: 12 warps are launched with 168 each; the epilogue
 // warps (up to 128 sums and 64 loads in flight) take 216 once the other warpgroup has
@@ -553,8 +553,8 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                 const Tile it = decode(pc.tile);
                 const uint32_t idesc =
                     idesc0 | ((uint32_t)((it.rows + C::ROW_STEP - 1) / C::ROW_STEP * C::ROW_STEP >> 3) << 17);
+                int in = 0;   // of the stretch
                 for (int kb = pc.kb0; kb < pc.kb1; ++kb) {
-                    const int in = (kb - pc.kb0) % STRETCH;
                     const bool opens = in == 0;
                     ok = __all_sync(0xffffffffu,
                                     mbar_wait(smem_u32(&st->full[stage]), phase, abort, args.err) &&
@@ -562,7 +562,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                                                                          abort, args.err)));
                     if (!ok) break;
                     tc_fence_after();
-                    const bool closes = in == STRETCH - 1 || kb == pc.kb1 - 1;
+                    const bool closes = ++in == args.stretch || kb == pc.kb1 - 1;
                     if (leader) {
                         const uint32_t d = tmem_base + buf * BN;
                         const uint64_t at = (uint64_t)(stage * (C::STAGE_BYTES >> 4));
@@ -576,7 +576,10 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                     __syncwarp();
                     any = true;
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                    if (closes && ++buf == 2) { buf = 0; buf_phase ^= 1u; }
+                    if (closes) {
+                        in = 0;
+                        if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
+                    }
                 }
             }
             if (!ok && any && leader) {
@@ -634,7 +637,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
 #pragma unroll
                 for (int c = 0; c < HALF; ++c) acc[c] = of_raw<OUT>(raw[c]);
             }
-            for (int kb = pc.kb0; kb < pc.kb1 && ok; kb += STRETCH) {
+            for (int kb = pc.kb0; kb < pc.kb1 && ok; kb += args.stretch) {
                 ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&st->tfull[buf]), buf_phase, abort, args.err));
                 if (!ok) break;
                 tc_fence_after();
