@@ -166,7 +166,7 @@ moe_status moe_combine_rows(int64_t T, int32_t H, int32_t k, int64_t R, moe_dtyp
     if (!is_dtype(dtype) || !is_dtype(out_dtype) || H % 8 || k > kMaxTopK || T >= ((int64_t)1 << 31))
         return MOE_ERR_UNSUPPORTED;
     // assignments, rows and blocks are counted in 32 bits
-    if (T * k >= ((int64_t)1 << 31) || R >= ((int64_t)1 << 31) || T * ((H + 1023) / 1024) >= ((int64_t)1 << 31))
+    if (T * k >= ((int64_t)1 << 31) || R >= ((int64_t)1 << 31) || T * ((H + 255) / 256) >= ((int64_t)1 << 31))
         return MOE_ERR_UNSUPPORTED;
     if (T == 0) return MOE_OK;
     if ((R > 0 && !y) || !inv_pos || !topk_w || !out) return MOE_ERR_INVALID_ARG;
@@ -176,11 +176,9 @@ moe_status moe_combine_rows(int64_t T, int32_t H, int32_t k, int64_t R, moe_dtyp
     for (const auto& p : parts)
         if (p.p && (!aligned16(p.p) || (p.rows > 1 && (p.stride < H || p.stride * size_of(p.type) % 16))))
             return MOE_ERR_INVALID_ARG;
-    const int sms = num_sms_current();
-    if (sms <= 0) return MOE_ERR_CUDA;
     Range range("moe/combine_rows");
     const CombineRowsArgs a{y, inv_pos, topk_w, residual, out, T, R, y_stride, residual_stride, out_stride, H, k};
-    return finish(launch_combine_rows(dtype, out_dtype, a, sms, (cudaStream_t)stream), nullptr, (cudaStream_t)stream);
+    return finish(launch_combine_rows(dtype, out_dtype, a, (cudaStream_t)stream), nullptr, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -161,7 +161,6 @@ struct CombineRowsArgs {
     int64_t T, R, y_stride, residual_stride, out_stride;
     int32_t H, k;
 };
-cudaError_t launch_combine_rows(moe_dtype dtype, moe_dtype out_dtype, const CombineRowsArgs& a, int num_sms,
-                                cudaStream_t s);
+cudaError_t launch_combine_rows(moe_dtype dtype, moe_dtype out_dtype, const CombineRowsArgs& a, cudaStream_t s);
 
 }  // namespace moe
