@@ -26,8 +26,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
 BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["route.cu", "route_tc.cu", "permute.cu", "permute_static.cu", "grouped_gemm.cu", "combine.cu", "api.cu",
-           "selftest.cu", "fp8_gemm.cu", "fp8_quant.cu", "api_fp8.cu", "linear.cu", "route_logits.cu", "combine_rows.cu",
-           "api_ops.cu"]
+           "selftest.cu", "fp8_gemm.cu", "fp8_quant.cu", "api_fp8.cu", "linear.cu", "combine_rows.cu", "route_logits_bf16.cu",
+           "route_logits_fp16.cu", "route_logits_fp32.cu", "api_ops.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", *ARCH]
 

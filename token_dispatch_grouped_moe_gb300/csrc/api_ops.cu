@@ -86,8 +86,11 @@ moe_status moe_route_logits(int64_t T, int32_t E, int32_t k, moe_dtype dtype, co
     if (sms <= 0) return MOE_ERR_CUDA;
     Range range("moe/route_logits");
     const RouteLogitsArgs a{logits, stride, c.bias, topk_idx, topk_w, T, E, k, c.scores == MOE_SCORES_SIGMOID,
-                            c.groups, c.top_groups, c.group_top, c.renormalize != 0, c.scale};
-    return finish(launch_route_logits(dtype, a, sms, (cudaStream_t)stream), nullptr, (cudaStream_t)stream);
+                            c.groups, c.top_groups, c.group_top, c.renormalize != 0, c.scale, 1};
+    const auto launch = dtype == MOE_BF16 ? launch_route_logits_bf16
+                        : dtype == MOE_FP16 ? launch_route_logits_fp16
+                                            : launch_route_logits_fp32;
+    return finish(launch(a, sms, (cudaStream_t)stream), nullptr, (cudaStream_t)stream);
 }
 
 size_t moe_linear_workspace_size(void) { return kLinearWorkspaceBytes; }

@@ -1,4 +1,4 @@
-// ops.cuh -- the launchers of routing from logits (route_logits.cu), the
+// ops.cuh -- the launchers of routing from logits (route_logits.cuh), the
 // product with an epilogue (linear.cu) and the weighted sum of experts' rows
 // (combine_rows.cu), and their arguments. Internal.
 #pragma once
@@ -147,8 +147,12 @@ struct RouteLogitsArgs {
     int32_t groups, top_groups, group_top;
     int32_t renorm;
     float scale;
+    int32_t rows_per_warp;  // (set by the launcher)
 };
-cudaError_t launch_route_logits(moe_dtype dtype, const RouteLogitsArgs& a, int num_sms, cudaStream_t s);
+// by the logits' type
+cudaError_t launch_route_logits_bf16(const RouteLogitsArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_route_logits_fp16(const RouteLogitsArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_route_logits_fp32(const RouteLogitsArgs& a, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------- combine_rows --
 

@@ -1,4 +1,4 @@
-// route_logits.cu -- each token's experts and weights from its logits:
+// route_logits.cuh -- each token's experts and weights from its logits:
 //
 //   s = softmax(l) or 1 / (1 + e^-l)
 //   key = l without a bias (scores are in their logits' order), s + bias with one
@@ -13,6 +13,8 @@
 //
 // A warp takes a token. Its experts lie V a lane in index order, no group crossing
 // a lane: lanes_per_group = the largest power of two <= 32 / groups.
+#pragma once
+
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -76,6 +78,13 @@ __device__ __forceinline__ float max_f32(float v)
     return r;
 }
 
+__device__ __forceinline__ float max_or_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // e^x within 2^-22 + 2^-23 of itself (0 below 2^-126, inf above the range): ex2's
@@ -92,13 +101,20 @@ __device__ __forceinline__ float exp_near(float x)
 
 __device__ __forceinline__ float sigmoid_near(float x) { return rcp(1.0f + exp_near(-x)); }
 
-// How far a score in fp32 may be from itself, absolutely. Sigmoid: s (1 - s) times
-// e^-x's error (2^-22, and of a plain product with log2(e) 2 |x| 2^-24, where |x| s
-// (1 - s) < 1/4), a sum and a reciprocal: 4.5 * 2^-24. Softmax, in the largest
-// score: e^d within (4 + 3 |d|) 2^-24, the sum of up to 256 within (20.5 + 21) 2^-24
-// (16 in a lane, 5 steps), a reciprocal and a product: 49 * 2^-24 for every d.
-constexpr float kSigmoidTol = 5.0f * 0x1p-24f;
-constexpr float kSoftmaxTol = 26.0f * 0x1p-23f;
+// How far a key in fp32 may be from itself, beside what all keys of its row share.
+// Sigmoid: s (1 - s) times e^-x's error (2^-22, and of a plain product with log2(e) 2 |x|
+// 2^-24, where |x| s (1 - s) < 1/4), a sum and a reciprocal: 4.5 * 2^-24; softmax, in the
+// largest score (`most` = 1 / the sum): e^d within (6 + 3 |d|) 2^-24 of itself, times e^d
+// less than 7 * 2^-24; and the key's own rounding. A softmax's sum of up to 256 (within
+// (22.5 + 21) 2^-24: 16 in a lane, 5 steps), its reciprocal and the product scale all
+// scores of a row alike, by 47 * 2^-24 at most. That moves two scores against one another
+// by as much of their difference, and keys as near as this matters for have scores as
+// different as their biases, 2 b_most at most.
+__device__ __forceinline__ float sigmoid_tol(float b_most) { return 5.0f * 0x1p-24f + 0x1p-24f * (1.0f + b_most); }
+__device__ __forceinline__ float softmax_tol(float most, float b_most)
+{
+    return 7.0f * 0x1p-24f * most + 24.0f * 0x1p-24f * fminf(2.0f * b_most, most) + 0x1p-24f * (most + b_most);
+}
 
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -122,12 +138,17 @@ struct Place {
     }
 };
 
-template <int V, typename T>
-__device__ __forceinline__ void load_row(const RouteLogitsArgs& a, int64_t t, const Place<V>& p, float (&l)[V])
+template <typename T>
+__device__ __forceinline__ const T* row_of(const RouteLogitsArgs& a, int64_t t)
 {
-    const T* row = static_cast<const T*>(a.logits) + t * a.stride + p.first;
+    return static_cast<const T*>(a.logits) + t * a.stride;
+}
+
+template <int V, typename T>
+__device__ __forceinline__ void load_row(const T* row, const Place<V>& p, float (&l)[V])
+{
 #pragma unroll
-    for (int j = 0; j < V; ++j) l[j] = j < p.n ? to_float(row[j]) : kNegInf;
+    for (int j = 0; j < V; ++j) l[j] = j < p.n ? to_float(row[p.first + j]) : kNegInf;
 }
 
 template <int V>
@@ -282,7 +303,7 @@ __device__ __noinline__ void exact_row(const RouteLogitsArgs& a, int64_t t, int 
     const Place<V> p(a, lane);
     float l[V], b[V];
     double s[V];
-    load_row<V, T>(a, t, p, l);
+    load_row<V, T>(row_of<T>(a, t), p, l);
     load_bias<V>(a, p, b);
     bool nan = false;
 #pragma unroll
@@ -325,17 +346,16 @@ __device__ __noinline__ void careful_row(const RouteLogitsArgs& a, int64_t t, in
 {
     const Place<V> p(a, lane);
     float l[V], b[V], s[V];
-    load_row<V, T>(a, t, p, l);
+    load_row<V, T>(row_of<T>(a, t), p, l);
     load_bias<V>(a, p, b);
     bool bad = false;
 #pragma unroll
     for (int j = 0; j < V; ++j) bad = bad || !(l[j] < __builtin_huge_valf());
-    float s_most, tol;
+    float tol;
     if (a.sigmoid) {
 #pragma unroll
         for (int j = 0; j < V; ++j) s[j] = sigmoid_near(l[j]);
-        s_most = 1.0f;
-        tol = kSigmoidTol;
+        tol = sigmoid_tol(b_most);
     } else {
         float m = row_max<V>(l);
         if (m == kNegInf) m = 0.0f;
@@ -349,10 +369,9 @@ __device__ __noinline__ void careful_row(const RouteLogitsArgs& a, int64_t t, in
         const float inv = sum > 0.0f ? rcp(sum) : 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) s[j] *= inv;
-        s_most = inv;
-        tol = kSoftmaxTol * inv;
+        tol = softmax_tol(inv, b_most);
     }
-    tol += 0x1p-24f * (s_most + b_most) + 0x1p-90f;
+    tol += 0x1p-90f;
     int id = 0;
     float score = 0.0f, logit = 0.0f;
     bool again = order_row<V, float>(a, p, lane, l, b, s, tol, id, score, logit) || __any_sync(kAll, bad);
@@ -395,7 +414,7 @@ __device__ __forceinline__ void merge_two(float& x, float& y, float ox, float oy
 
 // The sum of e^(l - m) over a row in fp64 (rolled up: this code is cold, and what
 // it costs is its fetching).
-template <int V, typename T>
+template <typename T>
 __device__ __noinline__ double sum64(const T* row, int first, int n, float m)
 {
     double sum = 0.0;
@@ -440,10 +459,12 @@ template <int V>
 __device__ __forceinline__ int list_experts(uint8_t* list, int lane, const float (&v)[V], int first, int n, bool mine,
                                             float least)
 {
-    int count = 0;
+    unsigned bits = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j)
-        if (mine && j < n && v[j] >= least) ++count;
+        if (v[j] >= least && j < n) bits |= 1u << j;
+    if (!mine) bits = 0;
+    const int count = __popc(bits);
     int at = count;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -452,105 +473,73 @@ __device__ __forceinline__ int list_experts(uint8_t* list, int lane, const float
     }
     const int total = __shfl_sync(kAll, at, 31);
     if (total > 32) return total;
-    at -= count;
+    uint8_t* to = list + at - count;
     __syncwarp();
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-        if (mine && j < n && v[j] >= least) list[at++] = (uint8_t)(first + j);
+    for (; bits; bits &= bits - 1) *to++ = (uint8_t)(first + __ffs((int)bits) - 1);   // one or two
     __syncwarp();
     return total;
 }
 
-// The short way, which nearly every row takes: keys in fp32, the groups, then a
-// bound that at least k keys reach (the k-th largest of the lanes' best); the few
-// experts that reach it go one to a lane, and are put in order there, in fp64 where
-// fp32 does not tell two of them apart. FULL: every lane holds V experts, and they
-// may be read in vectors. SCORES: keys or group values are scores (else keys are the
-// logits).
-template <int V, typename T, bool FULL, bool SCORES>
-__global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 4 : 2) route_logits_kernel(const RouteLogitsArgs a)
-{
-    __shared__ uint8_t listed[kWarps][32];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    uint8_t* list = listed[threadIdx.x >> 5];
-    const Place<V> p(a, lane);
-    const int n = FULL ? V : p.n;
-    const bool biased = SCORES && a.bias != nullptr;
-    const bool pairs = SCORES && a.groups > 1 && a.group_top == 2;   // group values are sums of scores
-    float b[V];
-    float b_most = 0.0f;   // the largest finite |bias|
-    if constexpr (SCORES) {
-        load_bias<V>(a, p, b);
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (fabsf(b[j]) < __builtin_huge_valf()) b_most = fmaxf(b_most, fabsf(b[j]));
-        b_most = max_f32(b_most);
-    }
+// What the keys are: the logits (scores are in their order; group values too), or
+// scores + bias, or the logits with group values that are sums of two scores.
+enum RouteKeys { kByLogit = 0, kByBiased = 1, kByPairs = 2 };
 
-    for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.T; t += (int64_t)gridDim.x * kWarps) {
-        const T* row = static_cast<const T*>(a.logits) + t * a.stride;
-        float l[V];
-        if constexpr (FULL) {
-            load_whole<V, T>(row + p.first, l);
-        } else {
+// A row after its scan: the experts among which its k are, and what their scores and
+// order are computed with.
+struct Scanned {
+    int total;            // listed; over 32: the row takes the long way
+    float m, inv, tol;    // softmax: the largest logit, 1 / the sum; the bound on a key's error
+};
+
+// The scores, the groups, then a bound that at least k keys reach: the k-th largest of
+// the lanes' best. The few experts that reach it are listed.
+template <int V, typename T, bool FULL, RouteKeys KEYS>
+__device__ __forceinline__ Scanned scan_row(const RouteLogitsArgs& a, const Place<V>& p, int n, int lane, const T* row,
+                                            const float (&l)[V], const float (&b)[V], float b_most, uint8_t* list)
+{
+    Scanned r{33, 0.0f, 1.0f, 0.0f};
+    float c[V];   // scores + bias
+    if (!a.sigmoid && (KEYS != kByLogit || !a.renorm)) {
+        float m = l[0];
 #pragma unroll
-            for (int j = 0; j < V; ++j) l[j] = j < n ? to_float(row[p.first + j]) : 0.0f;
-        }
-        float odd = 0.0f;   // NaN with any infinity or NaN in the row
-#pragma unroll
-        for (int j = 0; j < V; ++j) odd = fmaf(l[j], 0.0f, odd);
-        bool careful = false;
-        if (__any_sync(kAll, odd != odd)) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) careful = careful || !(l[j] < __builtin_huge_valf());
-            careful = __any_sync(kAll, careful);
-        }
-        float m = 0.0f, inv = 1.0f, tol = 0.0f;
-        float c[V];   // scores + bias
-        if (!a.sigmoid && (SCORES || !a.renorm)) {
-            m = l[0];
-#pragma unroll
-            for (int j = 1; j < V; ++j) m = fmaxf(m, l[j]);
-            m = max_f32(n > 0 ? m : kNegInf);
-            careful = careful || m == kNegInf;
-            float sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                c[j] = ex2((l[j] - m) * kLog2e);
-                if (j < n) sum += c[j];
-            }
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
-            inv = rcp(sum);
-            if constexpr (SCORES) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) c[j] = fmaf(c[j], inv, b[j]);
-                tol = kSoftmaxTol * inv + 0x1p-24f * (inv + b_most);
-            }
-        } else if constexpr (SCORES) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) c[j] = rcp(1.0f + ex2(-kLog2e * l[j])) + b[j];
-            tol = kSigmoidTol + 0x1p-24f * (1.0f + b_most);
-        }
-        float key[V];
+        for (int j = 1; j < V; ++j) m = fmaxf(m, l[j]);
+        r.m = max_f32(FULL || n > 0 ? m : kNegInf);
+        float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            key[j] = biased ? c[j] : l[j];
-            if (!FULL && j >= n) key[j] = kNegInf;
+            c[j] = ex2((l[j] - r.m) * kLog2e);
+            if (FULL || j < n) sum += c[j];
         }
-        float best = key[0];
 #pragma unroll
-        for (int j = 1; j < V; ++j) best = fmaxf(best, key[j]);
-        bool kept = FULL || n > 0;
-        if (a.groups > 1) {
-            float value, last;   // of the group; the least of what makes it up
-            if (!pairs) {
-                value = best;
-                for (int d = 1; d < p.lanes; d <<= 1) value = fmaxf(value, __shfl_xor_sync(kAll, value, d));
-                last = value;
-            } else {
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+        r.inv = rcp(sum);   // a row of -inf, or with +inf or NaN: NaN
+        if (!(sum < __builtin_huge_valf())) return r;
+        if constexpr (KEYS != kByLogit) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) c[j] = KEYS == kByBiased ? fmaf(c[j], r.inv, b[j]) : c[j] * r.inv;
+            r.tol = softmax_tol(r.inv, b_most);
+        }
+    } else if constexpr (KEYS != kByLogit) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            c[j] = rcp(1.0f + ex2(-kLog2e * l[j]));
+            if (KEYS == kByBiased) c[j] += b[j];
+        }
+        r.tol = sigmoid_tol(b_most);
+    }
+    float key[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) key[j] = FULL || j < n ? (KEYS == kByBiased ? c[j] : l[j]) : kNegInf;
+    float best = key[0];
+#pragma unroll
+    for (int j = 1; j < V; ++j) best = max_or_nan(best, key[j]);
+    // a NaN logit or bias; +inf as a logit
+    if (__any_sync(kAll, KEYS == kByBiased ? best != best : !(best < __builtin_huge_valf()))) return r;
+    bool kept = FULL || n > 0;
+    if (a.groups > 1) {
+        float value, last;   // of the group; the least of what makes it up
+        if constexpr (KEYS == kByBiased || KEYS == kByPairs) {
+            if (a.group_top == 2) {
                 constexpr int H = V > 1 ? V / 2 : 1;
                 float x[H], y[H];
 #pragma unroll
@@ -569,125 +558,235 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 4 : 2) route_logits_kern
                 value = x[0] + y[0];
                 last = y[0];
             }
-            float rest = value, least = kNegInf;
-            for (int g = 0; g < a.top_groups; ++g) {
-                least = max_f32(rest);
-                if (rest == least) rest = kNegInf;
-            }
-            kept = kept && value >= least;
-            // as many groups as are wanted (equal values: more), and the next one well below
-            const unsigned firsts = __ballot_sync(kAll, kept && (lane & (p.lanes - 1)) == 0);
-            bool near = __popc(firsts) != a.top_groups;
-            if (SCORES && (biased || pairs)) near = near || !(least - max_f32(rest) > (pairs ? 8.0f : 2.0f) * tol);
-            if (near && !careful) {
-                const float(&from)[V] = SCORES && (biased || pairs) ? c : key;
-                const int total = list_experts<V>(list, lane, from, p.first, n, FULL || n > 0, last - 2.0f * tol);
-                careful = total > 32;
-                if (!careful) {
-                    const int e = lane < total ? list[lane] : 0;
-                    const float le = to_float(row[e]);
-                    double k64 = (double)le;
-                    if (SCORES && (biased || pairs)) {
-                        const double sum = a.sigmoid ? 1.0 : sum64<V, T>(row, p.first, n, m);
-                        k64 = score64(le, a.sigmoid, m, sum) + (biased ? (double)__ldg(a.bias + e) : 0.0);
-                    }
-                    const unsigned mask = settle_groups(a, lane, total, e / (a.E / a.groups), k64);
-                    kept = n > 0 && ((mask >> p.group) & 1u);
-                }
-            }
-            if (!kept) best = kNegInf;
         }
-        // at least k keys (or all) are as large as the k-th largest of the lanes' best
-        float least = kNegInf;
-        for (int r = 0; r < a.k; ++r) {
-            least = max_f32(best);
-            if (best == least) best = kNegInf;
+        if (KEYS == kByLogit || a.group_top != 2) {
+            value = best;
+            for (int d = 1; d < p.lanes; d <<= 1) value = fmaxf(value, __shfl_xor_sync(kAll, value, d));
+            last = value;
         }
-        // those experts, one a lane from here on
-        int total = 33;
-        if (!careful) total = list_experts<V>(list, lane, key, p.first, n, kept, least - 2.0f * tol);
-        if (total > 32) {
-            careful_row<V, T>(a, t, lane, b_most);
-            continue;
+        // down the groups' values until enough groups have been passed
+        const bool leads = (lane & (p.lanes - 1)) == 0 && (FULL || n > 0);
+        float rest = value, least;
+        unsigned equal;   // the groups of the last value, by their first lanes
+        int have = 0;
+        for (;;) {
+            least = max_f32(rest);
+            if (!(least > kNegInf)) return r;
+            equal = __ballot_sync(kAll, leads && rest == least);
+            have += __popc(equal);
+            if (have >= a.top_groups) break;
+            if (rest == least) rest = kNegInf;
         }
-        const bool mine = lane < total;
-        const int e = mine ? list[lane] : 0;
-        const float le = to_float(row[e]);
-        int place = 0;
-        float s;
-        if (biased) {
-            const float be = __ldg(a.bias + e);
-            s = a.sigmoid ? sigmoid_near(le) : exp_near(le - m) * inv;
-            // before this one for certain, and before it or equal to it as far as fp32 tells
-            const float k = mine ? s + be : kNegInf;
-            int maybe = 0;
-            for (int i = 0; i < total; ++i) {
-                const float d = __shfl_sync(kAll, k, i) - k;
-                if (d > 2.0f * tol) ++place;
-                if (d >= -2.0f * tol) ++maybe;
-            }
-            if (__any_sync(kAll, mine && place < a.k && maybe - place != 1)) {
-                // in fp64, ties by index
-                const double sum = a.sigmoid ? 1.0 : sum64<V, T>(row, p.first, n, m);
-                const double k64 = score64(le, a.sigmoid, m, sum) + (double)be;
-                place = 0;
-#pragma unroll 1
-                for (int i = 0; i < total; ++i) {
-                    const double o = __shfl_sync(kAll, k64, i);
-                    place += o > k64 || (o == k64 && i < lane);
-                }
-            }
-        } else {
-            const float k = mine ? le : kNegInf;
-            for (int i = 0; i < total; ++i) {
-                const float o = __shfl_sync(kAll, k, i);
-                if (o > k || (o == k && i < lane)) ++place;
-            }
-            // a renormalized softmax: the sum over all experts cancels
-            if (!SCORES && !a.sigmoid && a.renorm) m = max_f32(k);
-            s = a.sigmoid ? sigmoid_near(le) : exp_near(le - m) * inv;
+        bool near = false;
+        if constexpr (KEYS != kByLogit) {
+            // equal values across the border, or the next one not well below
+            const float next = max_f32(value < least ? value : kNegInf);
+            near = have > a.top_groups || !(least - next > (a.group_top == 2 ? 8.0f : 2.0f) * r.tol);
         }
-        const bool chosen = mine && place < a.k;
-        bool again = false;
-        if (a.renorm) {
-            again = __any_sync(kAll, chosen && s < kTiny);
-            float sum = chosen ? s : 0.0f;
+        // of the groups of the last value those of the lowest index
+        const unsigned lower = equal & ((1u << (p.group * p.lanes)) - 1u);
+        kept = kept && (value > least || (value == least && __popc(lower) < a.top_groups - have + __popc(equal)));
+        if (KEYS != kByLogit && near) {
+            const float(&from)[V] = KEYS == kByPairs ? c : key;
+            const int total = list_experts<V>(list, lane, from, p.first, n, FULL || n > 0, last - 2.0f * r.tol);
+            if (total > 32) return r;
+            const int e = lane < total ? list[lane] : 0;
+            const float le = to_float(row[e]);
+            const double sum = a.sigmoid ? 1.0 : sum64<T>(row, p.first, n, r.m);
+            const double k64 = score64(le, a.sigmoid, r.m, sum) + (KEYS == kByBiased ? (double)__ldg(a.bias + e) : 0.0);
+            const unsigned mask = settle_groups(a, lane, total, e / (a.E / a.groups), k64);
+            kept = n > 0 && ((mask >> p.group) & 1u);
+        }
+        if (!kept) best = kNegInf;
+    }
+    if constexpr (V == 1) {
+        if (a.groups == 1 && a.E <= 16) {   // all of them (32768 tokens, top 2 of 8: 11.1 -> 9.9 us)
+            if (lane < a.E) list[lane] = (uint8_t)lane;
+            __syncwarp();
+            r.total = a.E;
+            return r;
+        }
+    }
+    // at least k keys (or all) are as large as the k-th largest of the lanes' best
+    float least = kNegInf;
+    for (int i = 0; i < a.k; ++i) {
+        least = max_f32(best);
+        if (best == least) best = kNegInf;
+    }
+    r.total = list_experts<V>(list, lane, key, p.first, n, kept, least - 2.0f * r.tol);
+    return r;
+}
+
+// The listed experts of a row, one to each of W lanes (32, or 16 and another row in the
+// other half of the warp): their order, in fp64 where fp32 does not tell two of them
+// apart, and the k weights. The rows (a bit each) whose scores are too small for fp32,
+// which are not stored.
+template <int V, typename T, RouteKeys KEYS, int W>
+__device__ __forceinline__ unsigned order_listed(const RouteLogitsArgs& a, const Place<V>& p, int n, int lane, int64_t t0,
+                                                 const uint8_t* list, const Scanned& r0, const Scanned& r1)
+{
+    const bool second = W == 16 && lane >= 16;
+    const int sub = lane & (W - 1);
+    const int64_t t = t0 + second;
+    const T* row = row_of<T>(a, t);
+    const int total = second ? r1.total : r0.total;
+    const float m = second ? r1.m : r0.m, inv = second ? r1.inv : r0.inv, tol = second ? r1.tol : r0.tol;
+    const int most = W == 16 ? max(r0.total, r1.total) : r0.total;
+    const bool mine = sub < total;
+    const int e = mine ? list[(second ? 32 : 0) + sub] : 0;
+    const float le = mine ? to_float(row[e]) : kNegInf;
+    int place = 0;
+    float s;
+    if constexpr (KEYS == kByBiased) {
+        const float be = __ldg(a.bias + e);
+        s = a.sigmoid ? sigmoid_near(le) : exp_near(le - m) * inv;
+        // before this one for certain, and before it or equal to it as far as fp32 tells
+        const float k = mine ? s + be : kNegInf, far = k + 2.0f * tol, close = k - 2.0f * tol;
+        int maybe = 0;
+        for (int i = 0; i < most; i += 4) {
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
-            s = __fdividef(s, sum);
+            for (int q = 0; q < 4; ++q) {   // (lanes behind the last listed: -inf)
+                const float o = __shfl_sync(kAll, k, i + q, W);
+                if (o > far) ++place;
+                if (o >= close) ++maybe;
+            }
         }
-        if (again) {
-            careful_row<V, T>(a, t, lane, b_most);
-        } else if (chosen) {
-            a.topk_idx[t * a.k + place] = e;
-            a.topk_w[t * a.k + place] = s * a.scale;
+        if (__any_sync(kAll, mine && place < a.k && maybe - place != 1)) {
+            // in fp64, ties by index
+            double sum = 1.0;
+            if (!a.sigmoid) {
+                sum = sum64<T>(row_of<T>(a, t0), p.first, n, r0.m);
+                if (W == 16 && r1.total) {
+                    const double other = sum64<T>(row_of<T>(a, t0 + 1), p.first, n, r1.m);
+                    if (second) sum = other;
+                }
+            }
+            const double k64 = mine ? score64(le, a.sigmoid, m, sum) + (double)be : -__builtin_huge_val();
+            place = 0;
+#pragma unroll 1
+            for (int i = 0; i < most; ++i) {
+                const double o = __shfl_sync(kAll, k64, i, W);
+                place += o > k64 || (o == k64 && i < sub);
+            }
         }
+    } else {
+        for (int i = 0; i < most; i += 4) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float o = __shfl_sync(kAll, le, i + q, W);
+                if (o > le || (o == le && i + q < sub)) ++place;
+            }
+        }
+        float from = m;
+        if (KEYS == kByLogit && !a.sigmoid && a.renorm) {
+            // the sum over all experts cancels
+            from = le;
+#pragma unroll
+            for (int d = W / 2; d > 0; d >>= 1) from = fmaxf(from, __shfl_xor_sync(kAll, from, d));
+        }
+        s = a.sigmoid ? sigmoid_near(le) : exp_near(le - from) * inv;
+    }
+    const bool chosen = mine && place < a.k;
+    unsigned small = 0;
+    if (a.renorm) {
+        small = __ballot_sync(kAll, chosen && s < kTiny);
+        float sum = chosen ? s : 0.0f;
+#pragma unroll
+        for (int d = W / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+        s = __fdividef(s, sum);
+        if (W == 16) small = ((small & 0xffffu) != 0) | (((small >> 16) != 0) << 1);
+        else small = small != 0;
+    }
+    if (chosen && !((small >> second) & 1u)) {
+        a.topk_idx[t * a.k + place] = e;
+        a.topk_w[t * a.k + place] = s * a.scale;
+    }
+    return small;
+}
+
+// The short way, which nearly every row takes: two rows a warp are scanned, then their
+// listed experts put in order side by side. FULL: every lane holds V experts, and they
+// may be read in vectors.
+template <int V, typename T, bool FULL, RouteKeys KEYS>
+__global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 5 : 2) route_logits_kernel(const RouteLogitsArgs a)
+{
+    __shared__ uint8_t listed[kWarps][64];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    uint8_t* list = listed[threadIdx.x >> 5];
+    const Place<V> p(a, lane);
+    const int n = FULL ? V : p.n;
+    float b[V];
+    float b_most = 0.0f;   // the largest finite |bias|
+    if constexpr (KEYS == kByBiased) {
+        load_bias<V>(a, p, b);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (fabsf(b[j]) < __builtin_huge_valf()) b_most = fmaxf(b_most, fabsf(b[j]));
+        b_most = max_f32(b_most);
+    }
+    const int per = a.rows_per_warp;
+    for (int64_t t = per * ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)); t < a.T; t += per * (int64_t)gridDim.x * kWarps) {
+        const bool two = per == 2 && t + 1 < a.T;
+        const T *row0 = row_of<T>(a, t), *row1 = row_of<T>(a, two ? t + 1 : t);
+        float l0[V], l1[V];
+        if constexpr (FULL) {
+            load_whole<V, T>(row0 + p.first, l0);
+            load_whole<V, T>(row1 + p.first, l1);
+        } else {
+            load_row<V, T>(row0, p, l0);
+            load_row<V, T>(row1, p, l1);
+        }
+        const Scanned r0 = scan_row<V, T, FULL, KEYS>(a, p, n, lane, row0, l0, b, b_most, list);
+        Scanned r1{0, 0.0f, 1.0f, 0.0f};
+        if (two) r1 = scan_row<V, T, FULL, KEYS>(a, p, n, lane, row1, l1, b, b_most, list + 32);
+        unsigned small = 0;   // of the two rows
+        if (r0.total <= 16 && r1.total <= 16) {
+            small = order_listed<V, T, KEYS, 16>(a, p, n, lane, t, list, r0, r1);
+        } else {
+            small = 1;
+            if (r0.total <= 32) small = order_listed<V, T, KEYS, 32>(a, p, n, lane, t, list, r0, r0);
+            if (r1.total > 32) small |= 2;
+            else if (r1.total) small |= order_listed<V, T, KEYS, 32>(a, p, n, lane, t + 1, list + 32, r1, r1) << 1;
+        }
+        __syncwarp();
+        if (small & 1u) careful_row<16, T>(a, t, lane, b_most);
+        if (small & 2u) careful_row<16, T>(a, t + 1, lane, b_most);
     }
 }
 
-template <int V, typename T, bool FULL, bool SCORES>
-cudaError_t launch(const RouteLogitsArgs& a, int num_sms, cudaStream_t s)
+template <int V, typename T, bool FULL, RouteKeys KEYS>
+cudaError_t launch(RouteLogitsArgs a, int num_sms, cudaStream_t s)
 {
-    int64_t blocks = (a.T + kWarps - 1) / kWarps;
+    // two rows a warp, or one where there are not more rows than warps at a time
     const int64_t most = (int64_t)num_sms * 8;
+    a.rows_per_warp = a.T <= (int64_t)num_sms * 5 * kWarps ? 1 : 2;
+    int64_t blocks = (a.T + a.rows_per_warp * kWarps - 1) / (a.rows_per_warp * kWarps);
     if (blocks > most) blocks = most;
-    return launch_pdl(route_logits_kernel<V, T, FULL, SCORES>, dim3((unsigned)blocks), dim3(32 * kWarps), 0, s, a);
+    return launch_pdl(route_logits_kernel<V, T, FULL, KEYS>, dim3((unsigned)blocks), dim3(32 * kWarps), 0, s, a);
 }
 
 template <int V, typename T>
 cudaError_t launch_place(const RouteLogitsArgs& a, int num_sms, int lanes, cudaStream_t s)
 {
-    constexpr int BYTES = V * (int)sizeof(T) < 16 ? V * (int)sizeof(T) : 16;
-    const bool full = lanes * a.groups == 32 && a.E == 32 * V && reinterpret_cast<uintptr_t>(a.logits) % BYTES == 0 &&
-                      (a.T == 1 || a.stride * (int)sizeof(T) % BYTES == 0);
-    const bool scores = a.bias || (a.groups > 1 && a.group_top == 2);
-    if (scores) return full ? launch<V, T, true, true>(a, num_sms, s) : launch<V, T, false, true>(a, num_sms, s);
-    return full ? launch<V, T, true, false>(a, num_sms, s) : launch<V, T, false, false>(a, num_sms, s);
+    constexpr int size = (int)sizeof(T), bytes = V * size < 16 ? V * size : 16;
+    const bool full = lanes * a.groups == 32 && a.E == 32 * V && reinterpret_cast<uintptr_t>(a.logits) % bytes == 0 &&
+                      (a.T == 1 || a.stride * size % bytes == 0);
+    if (a.bias) return full ? launch<V, T, true, kByBiased>(a, num_sms, s) : launch<V, T, false, kByBiased>(a, num_sms, s);
+    if (a.groups > 1 && a.group_top == 2)
+        return full ? launch<V, T, true, kByPairs>(a, num_sms, s) : launch<V, T, false, kByPairs>(a, num_sms, s);
+    return full ? launch<V, T, true, kByLogit>(a, num_sms, s) : launch<V, T, false, kByLogit>(a, num_sms, s);
 }
 
+}  // namespace
+
+// The launcher of one type of logits (each is compiled by a file of its own, beside the
+// others).
 template <typename T>
-cudaError_t launch_type(const RouteLogitsArgs& a, int num_sms, cudaStream_t s)
+cudaError_t launch_route_logits_of(const RouteLogitsArgs& a, int num_sms, cudaStream_t s)
 {
+    if (a.T == 0) return cudaSuccess;
     int lanes = 32 / a.groups;
     while (lanes & (lanes - 1)) lanes &= lanes - 1;
     const int per_lane = (a.E / a.groups + lanes - 1) / lanes;
@@ -696,19 +795,6 @@ cudaError_t launch_type(const RouteLogitsArgs& a, int num_sms, cudaStream_t s)
     if (per_lane <= 4) return launch_place<4, T>(a, num_sms, lanes, s);
     if (per_lane <= 8) return launch_place<8, T>(a, num_sms, lanes, s);
     if (per_lane <= 16) return launch_place<16, T>(a, num_sms, lanes, s);
-    return cudaErrorInvalidValue;
-}
-
-}  // namespace
-
-cudaError_t launch_route_logits(moe_dtype dtype, const RouteLogitsArgs& a, int num_sms, cudaStream_t s)
-{
-    if (a.T == 0) return cudaSuccess;
-    switch (dtype) {
-    case MOE_BF16: return launch_type<__nv_bfloat16>(a, num_sms, s);
-    case MOE_FP16: return launch_type<__half>(a, num_sms, s);
-    case MOE_FP32: return launch_type<float>(a, num_sms, s);
-    }
     return cudaErrorInvalidValue;
 }
 
