@@ -412,27 +412,55 @@ __device__ __forceinline__ void merge_two(float& x, float& y, float ox, float oy
     y = fmaxf(fmaxf(y, oy), lo);
 }
 
-// The sum of e^(l - m) over a row in fp64 (rolled up: this code is cold, and what
-// it costs is its fetching).
+// e^x in fp64, |x| up to 700 (beyond: of 700): 2^n e^r, |r| <= ln(2) / 2, by the power
+// series of e^r up to r^13. (What follows in fp64 is inlined, without calls: a call in
+// the short way's loop would have its registers spilled for it: 22 accesses a row.)
+__device__ __forceinline__ double exp64(double x)
+{
+    constexpr double kLog2e64 = 1.4426950408889634074, kLn2High = 0.69314718055994530942, kLn2Low = 2.3190468138462996e-17;
+    x = fmin(fmax(x, -700.0), 700.0);
+    const double n = rint(x * kLog2e64);
+    const double r = fma(-n, kLn2Low, fma(-n, kLn2High, x));
+    double p = 1.0 / 6227020800.0;   // 1 / 13!
+    constexpr double kInverse[13] = {1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0,
+                                     1.0 / 5040.0, 1.0 / 720.0, 1.0 / 120.0, 1.0 / 24.0, 1.0 / 6.0, 0.5, 1.0, 1.0};
+#pragma unroll
+    for (int i = 0; i < 13; ++i) p = fma(p, r, kInverse[i]);
+    return p * __longlong_as_double((long long)((int)n + 1023) << 52);
+}
+
+// 1 / d for 1 <= d <= 256: rcp's 22 bits, doubled twice by Newton's iteration.
+__device__ __forceinline__ double inverse64(double d)
+{
+    double y = (double)rcp((float)d);
+    y = fma(y, fma(-d, y, 1.0), y);
+    return fma(y, fma(-d, y, 1.0), y);
+}
+
+// A score in fp64; softmax: from the largest logit and 1 / the sum.
+__device__ __forceinline__ double score64(float l, int sigmoid, float m, double inv)
+{
+    if (!sigmoid) return exp64((double)l - (double)m) * inv;
+    const double t = exp64(-fabs((double)l));
+    return (l < 0.0f ? t : 1.0) * inverse64(1.0 + t);
+}
+
+// 1 / the sum of e^(l - m) over a row in fp64 (rolled up, being cold).
 template <typename T>
-__device__ __noinline__ double sum64(const T* row, int first, int n, float m)
+__device__ __forceinline__ double inverse_sum64(const T* row, int first, int n, float m)
 {
     double sum = 0.0;
 #pragma unroll 1
-    for (int j = 0; j < n; ++j) sum += exp((double)to_float(row[first + j]) - (double)m);
+    for (int j = 0; j < n; ++j) sum += exp64((double)to_float(row[first + j]) - (double)m);
+#pragma unroll 1
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
-    return sum;
-}
-
-__device__ __noinline__ double score64(float l, int sigmoid, float m, double sum)
-{
-    return sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)m) / sum;
+    return inverse64(sum);
 }
 
 // Which groups are kept, by values in fp64: lane i < total has the score + bias
 // `key` of an expert of `group`, the lanes together all that may be among a group's
 // one (or two) largest. A bit a group.
-__device__ __noinline__ unsigned settle_groups(const RouteLogitsArgs& a, int lane, int total, int group, double key)
+__device__ __forceinline__ unsigned settle_groups(const RouteLogitsArgs& a, int lane, int total, int group, double key)
 {
     double x = -__builtin_huge_val(), y = x;   // lane g: the two largest of group g
 #pragma unroll 1
@@ -487,7 +515,7 @@ enum RouteKeys { kByLogit = 0, kByBiased = 1, kByPairs = 2 };
 // A row after its scan: the experts among which its k are, and what their scores and
 // order are computed with.
 struct Scanned {
-    int total;            // listed; over 32: the row takes the long way
+    int total;            // listed; over 32: the row takes a longer way
     float m, inv, tol;    // softmax: the largest logit, 1 / the sum; the bound on a key's error
 };
 
@@ -592,8 +620,8 @@ __device__ __forceinline__ Scanned scan_row(const RouteLogitsArgs& a, const Plac
             if (total > 32) return r;
             const int e = lane < total ? list[lane] : 0;
             const float le = to_float(row[e]);
-            const double sum = a.sigmoid ? 1.0 : sum64<T>(row, p.first, n, r.m);
-            const double k64 = score64(le, a.sigmoid, r.m, sum) + (KEYS == kByBiased ? (double)__ldg(a.bias + e) : 0.0);
+            const double inv = a.sigmoid ? 1.0 : inverse_sum64<T>(row, p.first, n, r.m);
+            const double k64 = score64(le, a.sigmoid, r.m, inv) + (KEYS == kByBiased ? (double)__ldg(a.bias + e) : 0.0);
             const unsigned mask = settle_groups(a, lane, total, e / (a.E / a.groups), k64);
             kept = n > 0 && ((mask >> p.group) & 1u);
         }
@@ -617,10 +645,19 @@ __device__ __forceinline__ Scanned scan_row(const RouteLogitsArgs& a, const Plac
     return r;
 }
 
+// The rows (a bit each) of the halves of a warp (W = 16), or its one row, that have a
+// lane with `which`.
+template <int W>
+__device__ __forceinline__ unsigned rows_with(bool which)
+{
+    const unsigned lanes = __ballot_sync(kAll, which);
+    return W == 16 ? (unsigned)((lanes & 0xffffu) != 0) | (unsigned)((lanes >> 16) != 0) << 1 : (unsigned)(lanes != 0);
+}
+
 // The listed experts of a row, one to each of W lanes (32, or 16 and another row in the
-// other half of the warp): their order, in fp64 where fp32 does not tell two of them
-// apart, and the k weights. The rows (a bit each) whose scores are too small for fp32,
-// which are not stored.
+// other half of the warp): their order, in fp64
+// where fp32 does not tell it, and the k weights. Returns the rows (a bit each)
+// that are not stored: whose scores are too small for fp32.
 template <int V, typename T, RouteKeys KEYS, int W>
 __device__ __forceinline__ unsigned order_listed(const RouteLogitsArgs& a, const Place<V>& p, int n, int lane, int64_t t0,
                                                  const uint8_t* list, const Scanned& r0, const Scanned& r1)
@@ -637,6 +674,7 @@ __device__ __forceinline__ unsigned order_listed(const RouteLogitsArgs& a, const
     const float le = mine ? to_float(row[e]) : kNegInf;
     int place = 0;
     float s;
+    unsigned later = 0;
     if constexpr (KEYS == kByBiased) {
         const float be = __ldg(a.bias + e);
         s = a.sigmoid ? sigmoid_near(le) : exp_near(le - m) * inv;
@@ -652,16 +690,16 @@ __device__ __forceinline__ unsigned order_listed(const RouteLogitsArgs& a, const
             }
         }
         if (__any_sync(kAll, mine && place < a.k && maybe - place != 1)) {
-            // in fp64, ties by index
-            double sum = 1.0;
+            // ties by index
+            double inv64 = 1.0;
             if (!a.sigmoid) {
-                sum = sum64<T>(row_of<T>(a, t0), p.first, n, r0.m);
+                inv64 = inverse_sum64<T>(row_of<T>(a, t0), p.first, n, r0.m);
                 if (W == 16 && r1.total) {
-                    const double other = sum64<T>(row_of<T>(a, t0 + 1), p.first, n, r1.m);
-                    if (second) sum = other;
+                    const double other = inverse_sum64<T>(row_of<T>(a, t0 + 1), p.first, n, r1.m);
+                    if (second) inv64 = other;
                 }
             }
-            const double k64 = mine ? score64(le, a.sigmoid, m, sum) + (double)be : -__builtin_huge_val();
+            const double k64 = mine ? score64(le, a.sigmoid, m, inv64) + (double)be : -__builtin_huge_val();
             place = 0;
 #pragma unroll 1
             for (int i = 0; i < most; ++i) {
@@ -687,28 +725,25 @@ __device__ __forceinline__ unsigned order_listed(const RouteLogitsArgs& a, const
         s = a.sigmoid ? sigmoid_near(le) : exp_near(le - from) * inv;
     }
     const bool chosen = mine && place < a.k;
-    unsigned small = 0;
     if (a.renorm) {
-        small = __ballot_sync(kAll, chosen && s < kTiny);
+        later |= rows_with<W>(chosen && s < kTiny);
         float sum = chosen ? s : 0.0f;
 #pragma unroll
         for (int d = W / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
         s = __fdividef(s, sum);
-        if (W == 16) small = ((small & 0xffffu) != 0) | (((small >> 16) != 0) << 1);
-        else small = small != 0;
     }
-    if (chosen && !((small >> second) & 1u)) {
+    if (chosen && !((later >> second) & 1u)) {
         a.topk_idx[t * a.k + place] = e;
         a.topk_w[t * a.k + place] = s * a.scale;
     }
-    return small;
+    return later;
 }
 
 // The short way, which nearly every row takes: two rows a warp are scanned, then their
 // listed experts put in order side by side. FULL: every lane holds V experts, and they
 // may be read in vectors.
 template <int V, typename T, bool FULL, RouteKeys KEYS>
-__global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 5 : 2) route_logits_kernel(const RouteLogitsArgs a)
+__global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 5 : 2) route_logits_kernel(const __grid_constant__ RouteLogitsArgs a)
 {
     __shared__ uint8_t listed[kWarps][64];
     pdl_wait();
@@ -741,18 +776,17 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 5 : 2) route_logits_kern
         const Scanned r0 = scan_row<V, T, FULL, KEYS>(a, p, n, lane, row0, l0, b, b_most, list);
         Scanned r1{0, 0.0f, 1.0f, 0.0f};
         if (two) r1 = scan_row<V, T, FULL, KEYS>(a, p, n, lane, row1, l1, b, b_most, list + 32);
-        unsigned small = 0;   // of the two rows
+        unsigned later = 0;   // of the two rows
         if (r0.total <= 16 && r1.total <= 16) {
-            small = order_listed<V, T, KEYS, 16>(a, p, n, lane, t, list, r0, r1);
+            later = order_listed<V, T, KEYS, 16>(a, p, n, lane, t, list, r0, r1);
         } else {
-            small = 1;
-            if (r0.total <= 32) small = order_listed<V, T, KEYS, 32>(a, p, n, lane, t, list, r0, r0);
-            if (r1.total > 32) small |= 2;
-            else if (r1.total) small |= order_listed<V, T, KEYS, 32>(a, p, n, lane, t + 1, list + 32, r1, r1) << 1;
+            later = 1;
+            if (r0.total <= 32) later = order_listed<V, T, KEYS, 32>(a, p, n, lane, t, list, r0, r0);
+            if (r1.total > 32) later |= 2;
+            else if (r1.total) later |= order_listed<V, T, KEYS, 32>(a, p, n, lane, t + 1, list + 32, r1, r1) << 1;
         }
         __syncwarp();
-        if (small & 1u) careful_row<16, T>(a, t, lane, b_most);
-        if (small & 2u) careful_row<16, T>(a, t + 1, lane, b_most);
+        for (; later; later &= later - 1) careful_row<16, T>(a, t + (later & 1u ? 0 : 1), lane, b_most);
     }
 }
 
