@@ -43,6 +43,10 @@ __device__ __forceinline__ uint64_t ordered(double v)
     const uint64_t u = (uint64_t)__double_as_longlong(v != v ? (double)kNegInf : v + 0.0);
     return u >> 63 ? ~u : u | (1ull << 63);
 }
+__device__ __forceinline__ double value64(uint64_t u)
+{
+    return __longlong_as_double((long long)(u >> 63 ? u ^ (1ull << 63) : ~u));
+}
 __device__ __forceinline__ float value_of(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u); }
 
 __device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kAll, v); }
@@ -445,13 +449,19 @@ __device__ __forceinline__ double score64(float l, int sigmoid, float m, double 
     return (l < 0.0f ? t : 1.0) * inverse64(1.0 + t);
 }
 
-// 1 / the sum of e^(l - m) over a row in fp64 (rolled up, being cold).
+// 1 / the sum of e^(l - m) over a row in fp64 (four at a time: it is cold, and short).
 template <typename T>
 __device__ __forceinline__ double inverse_sum64(const T* row, int first, int n, float m)
 {
     double sum = 0.0;
 #pragma unroll 1
-    for (int j = 0; j < n; ++j) sum += exp64((double)to_float(row[first + j]) - (double)m);
+    for (int j0 = 0; j0 < n; j0 += 4) {
+        double v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = exp64((double)to_float(row[first + min(j0 + i, n - 1)]) - (double)m);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += j0 + i < n ? v[i] : 0.0;
+    }
 #pragma unroll 1
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
     return inverse64(sum);
@@ -462,20 +472,19 @@ __device__ __forceinline__ double inverse_sum64(const T* row, int first, int n, 
 // one (or two) largest. A bit a group.
 __device__ __forceinline__ unsigned settle_groups(const RouteLogitsArgs& a, int lane, int total, int group, double key)
 {
-    double x = -__builtin_huge_val(), y = x;   // lane g: the two largest of group g
-#pragma unroll 1
+    const uint64_t mine = ordered(key);   // (compared as whole numbers: fp64 is slow)
+    uint64_t x = 0, y = 0;                // lane g: the two largest of group g
     for (int i = 0; i < total; ++i) {
-        const double k = __shfl_sync(kAll, key, i);
+        const uint64_t k = __shfl_sync(kAll, mine, i);
         const int g = __shfl_sync(kAll, group, i);
         if (g != lane) continue;
         if (k > x) { y = x; x = k; }
         else if (k > y) y = k;
     }
-    const double value = a.group_top == 2 ? x + y : x;
+    const uint64_t value = a.group_top == 2 ? ordered(value64(x) + value64(y)) : x;
     int place = 0;
-#pragma unroll 1
     for (int g = 0; g < a.groups; ++g) {
-        const double v = __shfl_sync(kAll, value, g);
+        const uint64_t v = __shfl_sync(kAll, value, g);
         place += v > value || (v == value && g < lane);
     }
     return __ballot_sync(kAll, lane < a.groups && place < a.top_groups);
@@ -620,7 +629,8 @@ __device__ __forceinline__ Scanned scan_row(const RouteLogitsArgs& a, const Plac
             if (total > 32) return r;
             const int e = lane < total ? list[lane] : 0;
             const float le = to_float(row[e]);
-            const double inv = a.sigmoid ? 1.0 : inverse_sum64<T>(row, p.first, n, r.m);
+            // (without a bias the sum does not matter)
+            const double inv = KEYS == kByPairs || a.sigmoid ? (double)r.inv : inverse_sum64<T>(row, p.first, n, r.m);
             const double k64 = score64(le, a.sigmoid, r.m, inv) + (KEYS == kByBiased ? (double)__ldg(a.bias + e) : 0.0);
             const unsigned mask = settle_groups(a, lane, total, e / (a.E / a.groups), k64);
             kept = n > 0 && ((mask >> p.group) & 1u);
@@ -699,11 +709,12 @@ __device__ __forceinline__ unsigned order_listed(const RouteLogitsArgs& a, const
                     if (second) inv64 = other;
                 }
             }
-            const double k64 = mine ? score64(le, a.sigmoid, m, inv64) + (double)be : -__builtin_huge_val();
+            // (compared as whole numbers: fp64 is slow)
+            const uint64_t k64 = mine ? ordered(score64(le, a.sigmoid, m, inv64) + (double)be) : 0;
             place = 0;
-#pragma unroll 1
+#pragma unroll 4
             for (int i = 0; i < most; ++i) {
-                const double o = __shfl_sync(kAll, k64, i, W);
+                const uint64_t o = __shfl_sync(kAll, k64, i, W);
                 place += o > k64 || (o == k64 && i < sub);
             }
         }
