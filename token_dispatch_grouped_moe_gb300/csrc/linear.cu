@@ -548,6 +548,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             uint32_t buf_phase = 0;
             bool ok = true;
             bool any = false;
+            bool ready = false;    // the next block is known to be there
             Walk walk(plan, unit, n_units, k_blocks);
             for (Piece pc; ok && rank == 0 && walk.next(pc);) {
                 const Tile it = decode(pc.tile);
@@ -557,25 +558,28 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                 for (int kb = pc.kb0; kb < pc.kb1; ++kb) {
                     const bool opens = in == 0;
                     ok = __all_sync(0xffffffffu,
-                                    mbar_wait(smem_u32(&st->full[stage]), phase, abort, args.err) &&
+                                    (ready || mbar_wait(smem_u32(&st->full[stage]), phase, abort, args.err)) &&
                                         (!opens || mbar_wait<PAIR, PAIR>(smem_u32(&st->tempty[buf]), buf_phase ^ 1u,
                                                                          abort, args.err)));
                     if (!ok) break;
                     tc_fence_after();
                     const bool closes = ++in == args.stretch || kb == pc.kb1 - 1;
+                    const int at_stage = stage;
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    // whether the next block is there, asked before this one's MMAs
+                    ready = mbar_test(smem_u32(&st->full[stage]), phase);
                     if (leader) {
                         const uint32_t d = tmem_base + buf * BN;
-                        const uint64_t at = (uint64_t)(stage * (C::STAGE_BYTES >> 4));
+                        const uint64_t at = (uint64_t)(at_stage * (C::STAGE_BYTES >> 4));
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk)
                             tc_mma_f16<CG>(d, w_desc + at + w_step * kk, a_desc + at + 2 * kk, idesc,
                                            !opens || kk != 0 ? 1u : 0u);
-                        tc_commit<CG>(smem_u32(&st->empty[stage]));
+                        tc_commit<CG>(smem_u32(&st->empty[at_stage]));
                         if (closes) tc_commit<CG>(smem_u32(&st->tfull[buf]));
                     }
                     __syncwarp();
                     any = true;
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                     if (closes) {
                         in = 0;
                         if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
