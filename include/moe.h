@@ -636,6 +636,12 @@ moe_status moe_linear(int64_t R, int32_t K, int32_t N, int32_t G, moe_dtype dtyp
                       moe_dtype out_dtype, void* out, int64_t out_stride, void* ws, size_t ws_bytes,
                       moe_stream_t stream);
 
+/* Test hook (host only): which kernel a product of these sizes runs on a device of
+ * num_sms SMs: 0 tiles of up to 32 rows, 1 of up to 128 (one CTA per MMA), 2 a CTA
+ * pair; -1 for sizes that the call refuses. The result does not depend on it but for
+ * the order of its sums. */
+int32_t moe_selftest_linear_form(int64_t R, int32_t K, int32_t N, int32_t G, int32_t num_sms);
+
 /*
  * The weighted sum of experts' rows, back in token order:
  *   out[t,:] = sum over ranks j (in order) of topk_w[t,j] y[inv_pos[t,j],:]

@@ -296,6 +296,31 @@ def test_route_masked_and_special_rows(lib, scores, bias, groups, top_groups, gr
 
 
 @gpu
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+def test_route_equal_rows(lib, scores):
+    """Rows of equal logits (a router before its training), more experts than a warp lists."""
+    x = torch.zeros(3000, 256, device="cuda")
+    for opts in (dict(), dict(bias=torch.zeros(256, device="cuda")), dict(groups=8, top_groups=3, group_top=2),
+                 dict(groups=8, top_groups=3), dict(renormalize=True, groups=4, top_groups=1)):
+        opts["scores"] = scores
+        check_route(lib.route_logits(x, 8, **opts), route64(x, 8, **opts))
+
+
+@gpu
+def test_route_on_a_side_stream(lib):
+    g = gen(21)
+    x = randn(g, 4000, 128)
+    want = lib.route_logits(x, 8, scores="sigmoid", renormalize=True)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+        y = x * 1.0
+    got = lib.route_logits(y, 8, scores="sigmoid", renormalize=True, stream=s)
+    s.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@gpu
 def test_route_strides_outputs_and_empty(lib):
     g = gen(3)
     wide = randn(g, 50, 200)
@@ -419,6 +444,88 @@ def test_linear(lib, ws, K, N, counts, dtype, out_dtype, layout):
     out = lib.linear(a, w, ws, bias=bias, activation="gelu", residual=res, offsets=off, out_dtype=od)
     assert lib.check(ws) == lib.MOE_OK
     check_linear(out, *linear64(a, w, ends, bias, "gelu", res), K)
+
+
+def test_linear_forms(lib):
+    """The form of each size, and sizes that have none."""
+    few, one, pair = lib.LINEAR_FORM_FEW, lib.LINEAR_FORM_ONE, lib.LINEAR_FORM_PAIR
+    for (R, K, N, G), want in {(1, 4096, 14336, 1): few, (16, 64, 64, 1): few, (17, 64, 64, 1): one, (1, 64, 64, 2): one,
+                               (100, 4096, 4096, 1): one, (8192, 4096, 256, 1): one, (20000, 4096, 128, 1): one,
+                               (768, 2048, 1408, 64): one, (8192, 4096, 4096, 1): pair, (160, 4096, 14336, 1): pair,
+                               (16384, 4096, 14336, 8): pair, (20000, 2048, 1408, 64): pair}.items():
+        assert lib.linear_form_selftest(R, K, N, G) == want, (R, K, N, G)
+    for R, K, N, G in (0, 64, 64, 1), (4, 60, 64, 1), (4, 64, 4, 1), (4, 64, 64, 257), (4, 0, 64, 1), (-1, 64, 64, 1):
+        assert lib.linear_form_selftest(R, K, N, G) == -1
+    assert lib.linear_form_selftest(4, 64, 64, 1, num_sms=0) == -1
+    assert lib.linear_form_selftest(8192, 4096, 4096, 1, num_sms=1) == one      # no SM for a pair's second CTA
+    forms = {lib.linear_form_selftest(max(1, sum(c)), K, N, len(c)) for K, N, c in LINEARS}
+    assert forms == {few, one, pair}                                          # what test_linear runs
+
+
+@gpu
+@pytest.mark.parametrize("R,K,N", [(1, 2048, 2048), (300, 4096, 512), (2048, 1024, 4096)])
+def test_linear_captured_beside_eager(lib, R, K, N):
+    """Each form captured and replayed on new inputs, with eager calls of another form and
+    of the same one between the replays (their workspace is another)."""
+    g = gen(R)
+    a, other = randn(g, R, K).bfloat16(), randn(g, R, K).bfloat16()
+    w, bias = weight(g, 1, K, N, torch.bfloat16, "kn"), randn(g, 1, N)
+    ws, graph_ws = lib.linear_workspace(), lib.linear_workspace()
+    want = [lib.linear(x, w, ws, bias=bias, activation="silu") for x in (a, other)]
+    x = a.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        lib.linear(x, w, graph_ws, bias=bias, activation="silu")
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        first = lib.linear(x, w, graph_ws, bias=bias, activation="silu")
+        second = lib.linear(x, w, graph_ws, bias=bias, activation="silu", out_dtype=torch.float32)
+    for rows, ref in ((other, want[1]), (a, want[0])):
+        x.copy_(rows)
+        graph.replay()
+        eager = lib.linear(a, w, ws, bias=bias, activation="silu")
+        lib.linear(a[:3], w, ws)
+        assert torch.equal(first, ref) and torch.equal(eager, want[0])
+        # (the fp32 sum differs from the one that was rounded by both sums' own errors, which are
+        # of the terms' magnitude, so it is held to the definition instead)
+        check_linear(second, *linear64(rows, w, [0, R], bias, "silu"), K)
+    assert lib.check(ws) == lib.MOE_OK and lib.check(graph_ws) == lib.MOE_OK
+
+
+@gpu
+def test_linear_workspace_of_every_form(lib, ws):
+    """One workspace for products of all forms and sizes, one after another, on two
+    streams in turn."""
+    g = gen(12)
+    jobs = []
+    for R, K, N, G in ((3, 8192, 512, 1), (900, 4160, 512, 1), (40, 2048, 264, 8), (3000, 512, 1024, 3), (1, 512, 128, 1)):
+        a, w = randn(g, R, K).bfloat16(), weight(g, G, K, N, torch.bfloat16, "nk")
+        off, _ = offsets_of([R // G] * (G - 1) + [R - R // G * (G - 1)])
+        jobs.append((a, w, off, lib.linear(a, w, ws, offsets=off).clone()))
+    side = torch.cuda.Stream()
+    for i, (a, w, off, want) in enumerate(jobs * 3):
+        stream = side if i % 2 else None
+        here = stream or torch.cuda.current_stream()
+        here.wait_stream(torch.cuda.current_stream() if stream else side)
+        got = lib.linear(a, w, ws, offsets=off, stream=stream)
+        here.synchronize()
+        assert torch.equal(got, want)
+    assert lib.check(ws) == lib.MOE_OK
+
+
+@gpu
+def test_linear_activations_of_extremes(lib, ws):
+    """Sums of infinity and of the largest magnitudes, through the bias."""
+    a = torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(1, 64, 64, dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros(1, 64, device="cuda")
+    x[0, :8] = torch.tensor([math.inf, 1e38, 1e20, 300.0, -300.0, -1e20, -1e38, math.nan])
+    for act in ("relu", "silu", "gelu", "gelu_tanh"):
+        y = lib.linear(a, w, ws, bias=x, activation=act, out_dtype=torch.float32)
+        assert torch.equal(y[0, :4], x[0, :4]), act
+        assert bool((y[0, 4:7] == 0).all()) and bool(y[0, 7].isnan()) and bool((y[0, 8:] == 0).all()), act
 
 
 @gpu

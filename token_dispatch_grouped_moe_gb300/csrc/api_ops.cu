@@ -22,6 +22,17 @@ static_assert(kLinearPartOffset == MOE_LINEAR_WORKSPACE_ZEROS, "what has to be z
 
 bool is_dtype(moe_dtype t) { return t == MOE_BF16 || t == MOE_FP16 || t == MOE_FP32; }
 int size_of(moe_dtype t) { return t == MOE_FP32 ? 4 : 2; }
+// The sizes of a product: R rows, G weights of [K, N].
+moe_status check_linear(int64_t R, int32_t K, int32_t N, int32_t G)
+{
+    if (R < 0 || K <= 0 || N <= 0 || G <= 0) return MOE_ERR_INVALID_ARG;
+    if (K % 8 || N % 8 || K > (1 << 30) || N > (1 << 30) || G > kMaxExperts || R >= ((int64_t)1 << 31) - 256)
+        return MOE_ERR_UNSUPPORTED;
+    // tiles, and a round of them more, are counted in 32 bits
+    if ((R / 128 + G) * (((int64_t)N + 127) / 128) >= ((int64_t)1 << 31) - (1 << 16)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
 // The estimated cycles of a product in tiles of up to `cap` rows, for groups of equal size.
 float linear_cycles(bool pair, int cap, int64_t R, int32_t K, int32_t N, int32_t G, int sms)
 {
@@ -108,10 +119,7 @@ moe_status moe_linear(int64_t R, int32_t K, int32_t N, int32_t G, moe_dtype dtyp
     if (dtype != MOE_BF16 && dtype != MOE_FP16) return MOE_ERR_UNSUPPORTED;
     if (out_dtype != dtype && out_dtype != MOE_FP32) return MOE_ERR_UNSUPPORTED;
     if (e.bias && e.bias_dtype != dtype && e.bias_dtype != MOE_FP32) return MOE_ERR_UNSUPPORTED;
-    if (K % 8 || N % 8 || K > (1 << 30) || N > (1 << 30) || G > kMaxExperts || R >= ((int64_t)1 << 31) - 256)
-        return MOE_ERR_UNSUPPORTED;
-    // tiles, and a round of them more, are counted in 32 bits
-    if ((R / 128 + G) * (((int64_t)N + 127) / 128) >= ((int64_t)1 << 31) - (1 << 16)) return MOE_ERR_UNSUPPORTED;
+    MOE_TRY_STATUS(check_linear(R, K, N, G));
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < kLinearWorkspaceBytes) return MOE_ERR_WORKSPACE;
     if (R == 0) return MOE_OK;
     if (!a || !w || !out || !aligned16(a) || !aligned16(w)) return MOE_ERR_INVALID_ARG;
@@ -158,6 +166,12 @@ moe_status moe_linear(int64_t R, int32_t K, int32_t N, int32_t G, moe_dtype dtyp
     args.stretch = out_dtype == MOE_FP32 ? 8 : 32;
     return finish(launch_linear(form, out_dtype, tm_a, tm_a_small, tm_w, args, sms, (cudaStream_t)stream), ws,
                   (cudaStream_t)stream);
+}
+
+int32_t moe_selftest_linear_form(int64_t R, int32_t K, int32_t N, int32_t G, int32_t num_sms)
+{
+    if (check_linear(R, K, N, G) != MOE_OK || R == 0 || num_sms <= 0) return -1;
+    return linear_form(R, K, N, G, num_sms);
 }
 
 moe_status moe_combine_rows(int64_t T, int32_t H, int32_t k, int64_t R, moe_dtype dtype, const void* y,

@@ -37,6 +37,20 @@
 // and the last one adds the parts in the order of their blocks (so the result does
 // not depend on which came last) and runs the epilogue. No CTA waits for another.
 // Every wait is bounded (ptx.cuh).
+//
+// What bounds it (one GB300):
+//   - many rows: the tensor cores. 8192 x 4096 x 4096 with bias and residual 150 us (1830
+//     TFLOP/s), 16384 rows of 8 experts 4096 -> 14336 with gelu_tanh 1110-1140 us (1690-1730;
+//     a plain library product reaches 1902 for a moment and 1712 at the power cap). A
+//     block's 512 cycles of MMAs are also what shared memory takes to pass its operands
+//     in and out (128 bytes a cycle), so one CTA per MMA, which passes twice as much for
+//     the same sums, stays at 1290 TFLOP/s: pairs, wherever there are tiles enough.
+//   - few rows: the weights' bytes. 789 tokens' top 8 of 64 experts 3584 -> 2560 195-199 us
+//     (6.3-6.4 TB/s), 128 tokens' top 6 2048 -> 1408 60 us (6.2).
+//   - one token, 4096 -> 14336: 23.5 us, of which 17 stream the weights at 7 TB/s; the
+//     first loads, the last tile's epilogue and the launch are the rest.
+//   - in between (100 to 1000 rows of one group): the join of cut tiles, or tiles that do
+//     not fill the SMs: 400 x 4096 x 4096 20 us.
 #include <atomic>
 #include <cstdint>
 #include <type_traits>
@@ -262,7 +276,7 @@ __device__ __forceinline__ float gelu(float x)
     q = fmaf(q, t, 0.5f * -0.284496736f);
     q = fmaf(q, t, 0.5f * 0.254829592f);
     q = q * t * __expf(-z * z);
-    return fmaf(-fabsf(x), q, fmaxf(x, 0.0f));
+    return fmaf(-fminf(fabsf(x), 1e30f), q, fmaxf(x, 0.0f));   // (an infinity times q = 0 is no number)
 }
 
 // 0.5 x (1 + tanh(u)) = x / (1 + e^(-2u)), u = sqrt(2/pi) (x + 0.044715 x^3)

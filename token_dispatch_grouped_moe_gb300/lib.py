@@ -28,7 +28,8 @@ EXPORTS = ["moe_version", "moe_status_string", "moe_workspace_size", "moe_check"
            "moe_layer_plan", "moe_selftest_wait_timeout", "moe_launch_count", "moe_selftest_route_tc",
            "moe_layer_forward_host", "moe_host_chunks", "moe_fp8_workspace_size", "moe_add_rmsnorm_fp8",
            "moe_fp8_quantize_weight", "moe_fp8_matmul", "moe_fp8_gated", "moe_fp8_layer_forward",
-           "moe_selftest_fp8_form", "moe_route_logits", "moe_linear_workspace_size", "moe_linear", "moe_combine_rows"]
+           "moe_selftest_fp8_form", "moe_route_logits", "moe_linear_workspace_size", "moe_linear", "moe_combine_rows",
+           "moe_selftest_linear_form"]
 
 OPT_GEMM0_A = 0
 GEMM0_A_PERMUTED = 0      # dispatch copies token rows to x_perm; GEMM0 loads dense tiles
@@ -185,6 +186,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_linear_workspace_size.argtypes = []
     lib.moe_linear.restype = ctypes.c_int
     lib.moe_linear.argtypes = [i64, i32, i32, i32, i32, P, i64, P, P, i32, ctypes.POINTER(Epilogue), i32, P, i64, P, sz, P]
+    lib.moe_selftest_linear_form.restype = i32
+    lib.moe_selftest_linear_form.argtypes = [i64, i32, i32, i32, i32]
     lib.moe_combine_rows.restype = ctypes.c_int
     lib.moe_combine_rows.argtypes = [i64, i32, i32, i64, i32, P, i64, P, P, i32, P, i64, P, i64, P]
     _lib = lib
@@ -788,6 +791,14 @@ def linear(a, w, ws, bias=None, activation=None, residual=None, offsets=None, ou
     if type(r) is int:
         raise MoeError(r, "moe_linear")
     return r
+
+
+LINEAR_FORM_FEW, LINEAR_FORM_ONE, LINEAR_FORM_PAIR = 0, 1, 2
+
+
+def linear_form_selftest(R, K, N, G=1, num_sms=152) -> int:
+    """Which kernel a product of these sizes runs (test hook moe_selftest_linear_form)."""
+    return int(load().moe_selftest_linear_form(R, K, N, G, num_sms))
 
 
 def combine_rows(y, inv_pos, topk_w, residual=None, out_dtype=None, out=None, stream=None):
