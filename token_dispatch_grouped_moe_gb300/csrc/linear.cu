@@ -231,7 +231,7 @@ __device__ __forceinline__ void epilogue_barrier()   // the epilogue warps only
 // Adds this thread's rows c < rows of the parts s0 .. s1 - 1 of a tile to acc, in
 // order: a row of a part is BM floats, one a column (src: this thread's column of the
 // row 0 of slot 2 first). ROWS rows of PARTS parts are in flight together (each a
-// trip to L2).
+// trip to L2): all that the registers hold.
 template <int HALF, int ROWS, int PARTS>
 __device__ __forceinline__ void add_parts(float (&acc)[HALF], const float* src, int rows, int begin, int end,
                                           int64_t stride)
@@ -243,8 +243,8 @@ __device__ __forceinline__ void add_parts(float (&acc)[HALF], const float* src, 
         if (c >= rows) break;
         for (int s0 = begin; s0 < end; s0 += PARTS) {
             // (no branch between the loads, which would make them wait for one another: rows
-            // past the last are read as they are, a part has room for a multiple of 32; parts
-            // past the last are the last again)
+            // past the last are read as they are, of this part or the next; parts past the
+            // last are the last again)
             float v[PARTS][ROWS];
 #pragma unroll
             for (int s = 0; s < PARTS; ++s) {
@@ -716,7 +716,9 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                 }
                 if (rows <= 2) add_parts<HALF, 2, 8>(acc, src, rows, begin, end, stride);
                 else if (rows <= 8) add_parts<HALF, 8, 4>(acc, src, rows, begin, end, stride);
-                else add_parts<HALF, 32, HALF == 128 ? 1 : 2>(acc, src, rows, begin, end, stride);
+                else if (HALF == 64 && parts == 2) add_parts<HALF, HALF, 1>(acc, src, rows, begin, end, stride);
+                else if (HALF == 128) add_parts<HALF, 32, 1>(acc, src, rows, begin, end, stride);
+                else add_parts<HALF, 32, 2>(acc, src, rows, begin, end, stride);
             }
             if (!ok) continue;
             if (n < args.N) {

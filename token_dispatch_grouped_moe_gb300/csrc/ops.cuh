@@ -74,8 +74,9 @@ inline __host__ __device__ LinearCandidate linear_candidate(bool pair, int l, in
         if (last) c.cycles += bytes - whole > (float)k_blocks * block ? bytes - whole : (float)k_blocks * block;
         return c;
     }
-    // parts have room, and the products of the schedule stay below 2^32
-    if (tiles == 0 || 2 * n_units * cg * linear_part_rows(rows) > kLinearPartRows || 2 * n_units * cg > kLinearMaxTickets ||
+    // parts have room (and one more: a join reads up to 63 rows on), and the products of the
+    // schedule stay below 2^32
+    if (tiles == 0 || (2 * n_units * cg + 2) * linear_part_rows(rows) > kLinearPartRows || 2 * n_units * cg > kLinearMaxTickets ||
         k_blocks >= (1 << 30) / (n_units * n_units))
         return c;
     const bool even = l < 31;
