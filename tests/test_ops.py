@@ -332,6 +332,15 @@ def test_route_strides_outputs_and_empty(lib):
     got = lib.route_logits(wide, 4, topk_idx=idx, topk_w=w)
     assert got[0].data_ptr() == idx.data_ptr() and got[1].data_ptr() == w.data_ptr()
     check_route((idx, w), route64(wide, 4))
+    # the two outputs of a call are apart, and either may outlive the other
+    ids, weights = lib.route_logits(wide, 4)
+    assert ids.is_contiguous() and weights.is_contiguous() and ids.shape == weights.shape == (50, 4)
+    want = weights.clone()
+    ids.fill_(-1)
+    assert torch.equal(weights, want) and torch.equal(w, want)
+    del ids
+    torch.full((400,), 7, dtype=torch.int32, device="cuda")
+    assert torch.equal(weights, want) and torch.equal(weights + 0, want) and bool((weights.sum(0) > 0).all())
     got = lib.route_logits(wide[:0], 4)
     assert got[0].shape == (0, 4) and got[1].shape == (0, 4)
     for bad in (dict(k=9), dict(k=0), dict(k=4, groups=7), dict(k=4, top_groups=2), dict(k=4, group_top=3)):

@@ -762,9 +762,10 @@ def route_logits(logits, k, scores="softmax", bias=None, groups=1, top_groups=1,
     of its two largest. The weights are s of the selected, divided by their sum
     with ``renormalize``, times ``scale``. A logit of -inf is an expert with score 0; a NaN
     makes its row's weights NaN."""
-    r = (_binding or _load_binding()).route_logits(logits, k, _one_of(scores, SCORES, "scores"), bias, groups,
-                                                   top_groups, group_top, renormalize, scale, topk_idx, topk_w,
-                                                   _handle(stream, logits))
+    sigmoid = scores == "sigmoid" or (scores != "softmax" and _one_of(scores, SCORES, "scores"))
+    r = (_binding or _load_binding()).route_logits(logits, k, sigmoid, bias, groups, top_groups, group_top, renormalize,
+                                                   scale, topk_idx, topk_w,
+                                                   None if stream is None else _handle(stream, logits))
     if type(r) is int:
         raise MoeError(r, "moe_route_logits")
     return r
@@ -786,8 +787,9 @@ def linear(a, w, ws, bias=None, activation=None, residual=None, offsets=None, ou
     f32 = out_dtype is torch.float32
     if not f32 and out_dtype is not None and out_dtype is not a.dtype:
         raise ValueError(f"out_dtype: {a.dtype} or fp32 expected, got {out_dtype}")
-    r = (_binding or _load_binding()).linear(a, w, ws, bias, _one_of(activation, ACTIVATIONS, "activation"), residual,
-                                             offsets, f32, out, _handle(stream, a))
+    act = 0 if activation is None else _one_of(activation, ACTIVATIONS, "activation")
+    r = (_binding or _load_binding()).linear(a, w, ws, bias, act, residual, offsets, f32, out,
+                                             None if stream is None else _handle(stream, a))
     if type(r) is int:
         raise MoeError(r, "moe_linear")
     return r
@@ -808,7 +810,8 @@ def combine_rows(y, inv_pos, topk_w, residual=None, out_dtype=None, out=None, st
     :func:`permute`) outside [0, R) adds nothing; out and residual [T,H] are of
     ``out_dtype`` (y's by default), and may be the same memory."""
     code = -1 if out_dtype is None else _one_of(out_dtype, DTYPES, "out_dtype")
-    r = (_binding or _load_binding()).combine_rows(y, inv_pos, topk_w, residual, code, out, _handle(stream, y))
+    r = (_binding or _load_binding()).combine_rows(y, inv_pos, topk_w, residual, code, out,
+                                                   None if stream is None else _handle(stream, y))
     if type(r) is int:
         raise MoeError(r, "moe_combine_rows")
     return r
