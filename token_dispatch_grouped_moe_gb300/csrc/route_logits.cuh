@@ -22,10 +22,11 @@
 // 32768 tokens x 256 fp32 logits, top 8, us: by logits 15.2, sigmoid with bias 20, and
 // with 4 of 8 groups by the sum of their two best 26 (the logits' bytes: 5); top 2 of 8
 // 7.8; 5003 x 160 in 8 groups 7.0; one token 2.3, as any launch. One row in a thousand
-// wants fp64, 1.5 us of its warp's time (softmax with a bias 9: the sum's exponentials
-// again, 40 us in place of 26). Measured on the way, the third of these (us): each of the
-// k maxima by a search of all registers 122; fp64 in functions that were unrolled, cold
-// code fetched for 40 us, 62; in calls from the loop, which spill its registers, 29.
+// wants fp64, 1.5 us of its warp's time; a softmax with a bias, where its sum has to be
+// taken again, 9 (26 us without groups, 34 with: the last such row ends the launch).
+// Measured on the way, the third of these (us): each of the k maxima by a search of all
+// registers 122; fp64 in functions that were unrolled, cold code fetched for 40 us, 62; in
+// calls from the loop, which spill its registers, 29.
 #pragma once
 
 #include <cstdint>
@@ -712,7 +713,27 @@ __device__ __forceinline__ unsigned order_listed(const RouteLogitsArgs& a, const
                 if (o >= close) ++maybe;
             }
         }
-        if (__any_sync(kAll, mine && place < a.k && maybe - place != 1)) {
+        bool open = __any_sync(kAll, mine && place < a.k && maybe - place != 1);
+        if (open && !a.sigmoid) {
+            // fp64 but for the sum over all experts, whose error moves two keys against one
+            // another by 47 * 2^-24 of their scores' difference; compared as pairs of fp32
+            const double s64 = score64(le, 0, m, (double)inv), k64 = s64 + (double)be;
+            const float high = mine ? (float)k64 : kNegInf, s32 = (float)s64;
+            const float low = high > kNegInf ? (float)(k64 - (double)high) : 0.0f;
+            place = maybe = 0;
+#pragma unroll 4
+            for (int i = 0; i < most; ++i) {
+                const float oh = __shfl_sync(kAll, high, i, W), ol = __shfl_sync(kAll, low, i, W);
+                const float os = __shfl_sync(kAll, s32, i, W);
+                const float d = (oh - high) + (ol - low), u = 48.0f * 0x1p-24f * fabsf(os - s32) + 0x1p-44f * fabsf(high);
+                const bool same = oh == high && ol == low && (os == s32 || oh == kNegInf);
+                const bool first = same ? i < sub : d > u;
+                place += first;
+                maybe += first || (!same && d >= -u);
+            }
+            open = __any_sync(kAll, mine && place < a.k && maybe != place);
+        }
+        if (open) {
             // ties by index
             double inv64 = 1.0;
             if (!a.sigmoid) {
