@@ -20,7 +20,7 @@
 namespace moe {
 namespace {
 
-constexpr int kVersion = 401;   // 0.4.1
+constexpr int kVersion = 500;   // 0.5.0
 constexpr int kMaxDevices = 64;
 
 // ------------------------------------------------------------ device info --
