@@ -637,8 +637,8 @@ moe_status moe_linear(int64_t R, int32_t K, int32_t N, int32_t G, moe_dtype dtyp
                       moe_stream_t stream);
 
 /* Test hook (host only): which kernel a product of these sizes runs on a device of
- * num_sms SMs: 0 tiles of up to 32 rows, 1 of up to 128 (one CTA per MMA), 2 a CTA
- * pair; -1 for sizes that the call refuses. The result does not depend on it but for
+ * num_sms SMs: 0 tiles of up to 32 rows, 1 of up to 128 (one CTA per MMA), 2 and 3 a
+ * CTA pair with up to 256 and 128; -1 for sizes that the call refuses. The result does not depend on it but for
  * the order of its sums. */
 int32_t moe_selftest_linear_form(int64_t R, int32_t K, int32_t N, int32_t G, int32_t num_sms);
 

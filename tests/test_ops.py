@@ -429,6 +429,7 @@ LINEARS = [   # K, N, rows of each group
     (256, 320, [2085]), (400, 272, [5000, 0, 5001, 100]), (4096, 14336, [1, 1]), (2048, 40960, [17]), (16384, 512, [1]),
     (8192, 272, [130]), (8192, 144, [20, 40, 0, 33]), (1024, 2064, [1]), (520, 264, [257, 255, 16, 17, 512, 513]),
     (576, 4096, [4600]), (64, 64, [20000]), (4096, 256, [2048]), (4160, 4096, [900]),
+    (4096, 128, [4500]), (20480, 128, [3900]), (320, 2048, [700, 1, 900]), (14336, 2048, [1000]), (1024, 256, [97]), (4096, 512, [31, 33, 64, 65]),
 ]
 
 
@@ -457,9 +458,9 @@ def test_linear(lib, ws, K, N, counts, dtype, out_dtype, layout):
 
 def test_linear_forms(lib):
     """The form of each size, and sizes that have none."""
-    few, one, pair = lib.LINEAR_FORM_FEW, lib.LINEAR_FORM_ONE, lib.LINEAR_FORM_PAIR
-    for (R, K, N, G), want in {(1, 4096, 14336, 1): few, (16, 64, 64, 1): few, (17, 64, 64, 1): one, (1, 64, 64, 2): one,
-                               (100, 4096, 4096, 1): one, (8192, 4096, 256, 1): one, (20000, 4096, 128, 1): one,
+    few, one, pair, half = lib.LINEAR_FORM_FEW, lib.LINEAR_FORM_ONE, lib.LINEAR_FORM_PAIR, lib.LINEAR_FORM_PAIR_HALF
+    for (R, K, N, G), want in {(1, 4096, 14336, 1): few, (16, 64, 64, 1): few, (17, 64, 64, 1): half, (1, 64, 64, 2): one,
+                               (100, 4096, 4096, 1): half, (8192, 4096, 256, 1): half, (20000, 4096, 128, 1): one,
                                (768, 2048, 1408, 64): one, (8192, 4096, 4096, 1): pair, (160, 4096, 14336, 1): pair,
                                (16384, 4096, 14336, 8): pair, (20000, 2048, 1408, 64): pair}.items():
         assert lib.linear_form_selftest(R, K, N, G) == want, (R, K, N, G)
@@ -468,11 +469,11 @@ def test_linear_forms(lib):
     assert lib.linear_form_selftest(4, 64, 64, 1, num_sms=0) == -1
     assert lib.linear_form_selftest(8192, 4096, 4096, 1, num_sms=1) == one      # no SM for a pair's second CTA
     forms = {lib.linear_form_selftest(max(1, sum(c)), K, N, len(c)) for K, N, c in LINEARS}
-    assert forms == {few, one, pair}                                          # what test_linear runs
+    assert forms == {few, one, pair, half}                                    # what test_linear runs
 
 
 @gpu
-@pytest.mark.parametrize("R,K,N", [(1, 2048, 2048), (300, 4096, 512), (2048, 1024, 4096)])
+@pytest.mark.parametrize("R,K,N", [(1, 2048, 2048), (300, 4096, 512), (2048, 1024, 4096), (20000, 1024, 128)])
 def test_linear_captured_beside_eager(lib, R, K, N):
     """Each form captured and replayed on new inputs, with eager calls of another form and
     of the same one between the replays (their workspace is another)."""

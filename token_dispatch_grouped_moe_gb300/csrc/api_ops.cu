@@ -34,9 +34,10 @@ moe_status check_linear(int64_t R, int32_t K, int32_t N, int32_t G)
 }
 
 // The estimated cycles of a product in tiles of up to `cap` rows, for groups of equal size.
-float linear_cycles(bool pair, int cap, int64_t R, int32_t K, int32_t N, int32_t G, int sms)
+float linear_cycles(LinearForm form, int64_t R, int32_t K, int32_t N, int32_t G, int sms)
 {
-    const int step = pair ? 32 : 16, cols = pair ? 256 : 128, units = pair ? sms / 2 : sms;
+    const bool pair = linear_pair(form);
+    const int cap = linear_rows(form), step = pair ? 32 : 16, cols = pair ? 256 : 128, units = pair ? sms / 2 : sms;
     if (units <= 0) return INFINITY;
     const int64_t active = R < G ? R : G, rows = (R + active - 1) / active;
     const int64_t m_tiles = (rows + cap - 1) / cap, n_tiles = ((int64_t)N + cols - 1) / cols;
@@ -45,7 +46,7 @@ float linear_cycles(bool pair, int cap, int64_t R, int32_t K, int32_t N, int32_t
     if (tiles >= ((int64_t)1 << 31)) return INFINITY;
     float best = INFINITY;
     for (int l = 0; l < 32; ++l) {
-        const LinearCandidate c = linear_candidate(pair, l, (int)tiles, (int)(active * n_tiles), per,
+        const LinearCandidate c = linear_candidate(form, l, (int)tiles, (int)(active * n_tiles), per,
                                                    (K + kLinearBK - 1) / kLinearBK, units);
         if (c.fits && c.cycles < best) best = c.cycles;
     }
@@ -53,18 +54,25 @@ float linear_cycles(bool pair, int cap, int64_t R, int32_t K, int32_t N, int32_t
 }
 
 // The form of a product over R rows in G groups: a pair where its estimate is less by a
-// thirtieth at least; few rows in the form that leaves room for the next kernel's CTA.
+// thirtieth at least, in the pairs' two heights the lesser; few rows in the form that
+// leaves room for the next kernel's CTA.
 // Measured, one CTA / pair, us, K x N: 4096 x 256, 8192 rows 20.8 / 25.5; 4096 x 1024, 2000
 // 20.5 / 24.4, 4096 35.0 / 27.1; 1024 x 4096, 400 9.8 / 10.5, 700 13.1 / 12.7; 4096 x 4096,
 // 400 20.1 / 22.3, 700 31.8 / 25.4; 4096 x 14336, 100 24.3 / 26.5, 160 39.1 / 27.8; 14336 x
 // 4096, 100 30.0 / 40.7, 160 42.4 / 40.0; 64 groups 2048 x 1408, 128 each 69.1 / 80.3, 180
-// 94.6 / 78.9. Up to 32 / 128 rows, one CTA: 1 row 4096 x 14336 23.5 / 24.1, 8 rows 4096 x
+// 94.6 / 78.9. The lesser of those / a pair of 128 rows: 14336 x 4096, 160 35.6 / 30.5, 256
+// 37.8 / 32.4; 8192 x 8192, 256 37.2 / 31.3, 400 41.1 / 48.3; 4096 x 4096, 256 17.8 / 15.7,
+// 400 20.7 / 18.0, 1000 27.3 / 28.8; 8192 x 512, 400 17.6 / 16.2; 2048 x 128, 100 11.5 / 9.7;
+// 64 groups 2048 x 1408, 50 each 63.9 / 66.0, 256 86.7 / 90.0. Up to 32 / 128 rows, one CTA: 1 row 4096 x 14336 23.5 / 24.1, 8 rows 4096 x
 // 4096 9.5 / 10.4, 14336 x 4096 24.0 / 23.7, 32 rows 1024 x 4096 8.3 / 7.1.
 LinearForm linear_form(int64_t R, int32_t K, int32_t N, int32_t G, int sms)
 {
     if (G == 1 && R <= 16) return kLinearFew;
-    const bool pair = linear_cycles(true, 256, R, K, N, G, sms) * (30.0f / 29.0f) < linear_cycles(false, 128, R, K, N, G, sms);
-    return pair ? kLinearPair : kLinearOne;
+    const float one = linear_cycles(kLinearOne, R, K, N, G, sms);
+    const float pair = linear_cycles(kLinearPair, R, K, N, G, sms) * (30.0f / 29.0f);
+    const float half = linear_cycles(kLinearPairHalf, R, K, N, G, sms);
+    if (one <= pair && one <= half) return kLinearOne;
+    return pair <= half ? kLinearPair : kLinearPairHalf;
 }
 
 bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
@@ -162,7 +170,7 @@ moe_status moe_linear(int64_t R, int32_t K, int32_t N, int32_t G, moe_dtype dtyp
     args.part = reinterpret_cast<float*>(b + kLinearPartOffset);
     args.err = static_cast<uint32_t*>(ws);
     const LinearForm form = linear_form(R, K, N, G, sms);
-    args.tile_rows = form == kLinearFew ? 32 : form == kLinearOne ? 128 : 256;
+    args.tile_rows = linear_rows(form);
     args.stretch = out_dtype == MOE_FP32 ? 8 : 32;
     return finish(launch_linear(form, out_dtype, tm_a, tm_a_small, tm_w, args, sms, (cudaStream_t)stream), ws,
                   (cudaStream_t)stream);

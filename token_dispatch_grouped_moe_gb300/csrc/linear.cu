@@ -30,7 +30,9 @@
 // CTA pairs (PAIR): a 2-CTA cluster shares one tcgen05.mma.cta_group::2 of 256
 // columns n, each CTA staging its 128 of them and half of the rows; both CTAs'
 // boxes complete on rank 0's barrier, rank 0 issues, its commits arrive in both CTAs,
-// and both CTAs' epilogue warps release a TMEM buffer on rank 0.
+// and both CTAs' epilogue warps release a TMEM buffer on rank 0. A pair takes 256 rows, or
+// 128: as many MMAs a block as one CTA with twice the columns, its 16 KB of weights and 8 of
+// rows leave room for nine stages instead of six, and a block takes 380-460 cycles.
 // When the tiles do not fill the SMs evenly (few rows), K is cut: the blocks of the
 // tiles that are left over, end to end, go to the CTAs in equal runs; each CTA writes
 // the sums of a tile that it has only a part of to the workspace and takes a ticket,
@@ -44,13 +46,15 @@
 //     a plain library product reaches 1902 for a moment and 1712 at the power cap). A
 //     block's 512 cycles of MMAs are also what shared memory takes to pass its operands
 //     in and out (128 bytes a cycle), so one CTA per MMA, which passes twice as much for
-//     the same sums, stays at 1290 TFLOP/s: pairs, wherever there are tiles enough.
-//   - few rows: the weights' bytes. 789 tokens' top 8 of 64 experts 3584 -> 2560 195-199 us
-//     (6.3-6.4 TB/s), 128 tokens' top 6 2048 -> 1408 60 us (6.2).
+//     the same sums, stays at 1290 TFLOP/s: pairs, wherever there are tiles enough. 8192 x
+//     4096 x 256 with fp32 outputs 19.8 us (one CTA 22.2, pairs of 256 rows 25.6).
+//   - few rows: the weights' bytes. 789 tokens' top 8 of 64 experts 3584 -> 2560 190 us
+//     (6.6 TB/s; one CTA 196, pairs of 256 rows 198), 128 tokens' top 6 2048 -> 1408 60 us (6.2).
 //   - one token, 4096 -> 14336: 23.5 us, of which 17 stream the weights at 7 TB/s; the
 //     first loads, the last tile's epilogue and the launch are the rest.
 //   - in between (100 to 1000 rows of one group): the join of cut tiles, or tiles that do
-//     not fill the SMs: 400 x 4096 x 4096 20 us.
+//     not fill the SMs: 400 x 4096 x 4096 18 us (20.7 on one CTA),
+//     256 x 14336 x 4096 32 (38).
 #include <atomic>
 #include <cstdint>
 #include <type_traits>
@@ -88,7 +92,7 @@ struct Cfg {
     static constexpr int CTAS = BN <= 32 ? 2 : 1;               // that fit on an SM
     static constexpr int A_ROWS = PAIR ? BN / 2 : BN;           // rows that a CTA stages
     static constexpr int STAGE_BYTES = W_BYTES + A_ROWS * BK * 2;
-    static constexpr int STAGES = BN <= 32 ? 5 : 6;
+    static constexpr int STAGES = BN <= 32 ? 5 : STAGE_BYTES == 24 * 1024 ? 9 : 6;
     static constexpr int TMEM_COLS = 2 * BN;                    // two buffers
     static constexpr int TILE_N = PAIR ? 2 * BM : BM;           // columns of one work item
     static constexpr int ROW_STEP = PAIR ? 32 : 16;             // the MMA's N is a multiple of this
@@ -129,7 +133,7 @@ constexpr size_t smem_bytes()
     return 1024 + (size_t)C::STAGES * C::STAGE_BYTES + sizeof(SmemTail<C::STAGES>);
 }
 static_assert(smem_bytes<false, 32>() <= 113 * 1024 && smem_bytes<false, 128>() <= 227 * 1024 &&
-                  smem_bytes<true, 256>() <= 227 * 1024, "shared memory");
+                  smem_bytes<true, 128>() <= 227 * 1024 && smem_bytes<true, 256>() <= 227 * 1024, "shared memory");
 
 // A group's rows are spread evenly over its row tiles.
 template <int STEP>
@@ -211,10 +215,10 @@ __device__ __forceinline__ int first_part(const Plan& p, int q, int k_blocks, in
 
 // The plan with the least estimated time (linear_candidate), one candidate a lane; the
 // warp calls it together.
-template <bool PAIR>
+template <bool PAIR, int BN>
 __device__ __forceinline__ Plan make_plan(int tiles, int w_tiles, int rows, int k_blocks, int n_units, int lane)
 {
-    const LinearCandidate c = linear_candidate(PAIR, lane, tiles, w_tiles, rows, k_blocks, n_units);
+    const LinearCandidate c = linear_candidate(linear_form_of(PAIR, BN), lane, tiles, w_tiles, rows, k_blocks, n_units);
     // the least cost (its low bits give way to the lane)
     const uint32_t key = c.fits ? (__float_as_uint(c.cycles) & ~31u) | (uint32_t)lane : 0xffffffffu;
     const int best = (int)(__reduce_min_sync(0xffffffffu, key) & 31u);
@@ -473,7 +477,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     const uint32_t tmem_base = st->tmem_base;
     const int n_tiles = (args.N + C::TILE_N - 1) / C::TILE_N;
     const int k_blocks = (args.K + BK - 1) / BK;
-    const Plan plan = make_plan<PAIR>(st->tile_start[G] * n_tiles, st->groups * n_tiles, st->most_rows, k_blocks, n_units, lane);
+    const Plan plan = make_plan<PAIR, BN>(st->tile_start[G] * n_tiles, st->groups * n_tiles, st->most_rows, k_blocks, n_units, lane);
     volatile int* abort = &st->abort;
     auto decode = [&](int tile) {
         return decode_tile<C::TILE_N, C::ROW_STEP>(tile, n_tiles, st->tile_start, st->offsets, G);
@@ -825,6 +829,7 @@ cudaError_t launch_out(LinearForm form, const CUtensorMap& tm_a, const CUtensorM
     switch (form) {
     case kLinearFew: return launch<OUT, false, 32>(tm_a, tm_a_small, tm_w, a, num_sms, s);
     case kLinearOne: return launch<OUT, false, 128>(tm_a, tm_a_small, tm_w, a, num_sms, s);
+    case kLinearPairHalf: return launch<OUT, true, 128>(tm_a, tm_a_small, tm_w, a, num_sms, s);
     case kLinearPair: return launch<OUT, true, 256>(tm_a, tm_a_small, tm_w, a, num_sms, s);
     }
     return cudaErrorInvalidValue;

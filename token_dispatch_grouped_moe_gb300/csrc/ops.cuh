@@ -25,23 +25,38 @@ constexpr int kLinearMaxSplit = 16;
 constexpr int kLinearMaxTickets = 512;
 constexpr int kLinearPartRows = 81920;
 
+// The kernel's forms: one CTA per MMA, tiles of 128 columns and up to 32 or 128 rows; a CTA
+// pair per MMA, 256 columns and up to 256 or 128 rows.
+enum LinearForm { kLinearFew = 0, kLinearOne = 1, kLinearPair = 2, kLinearPairHalf = 3 };
+constexpr __host__ __device__ LinearForm linear_form_of(bool pair, int rows)
+{
+    return pair ? (rows == 256 ? kLinearPair : kLinearPairHalf) : (rows == 128 ? kLinearOne : kLinearFew);
+}
+inline __host__ __device__ bool linear_pair(LinearForm f) { return f >= kLinearPair; }
+inline __host__ __device__ int linear_rows(LinearForm f) { return f == kLinearFew ? 32 : f == kLinearPair ? 256 : 128; }
+
 // What the plan and the form are chosen by, in cycles. A K block (64) of a tile of r
 // rows: shared memory passes the operands twice (128 bytes a cycle), 128 columns and r
 // rows of one CTA, or r / 2 of each of a pair; that is more than the MMAs' own time for
 // fewer than 256 rows of a pair, and for any of one CTA. Measured (cycles a block):
-// pair, 256 rows 520; one CTA, 128 rows 480. Where every tile of the weights is read
-// once, from memory, a CTA has no more than its stages in flight: 520.
+// pair, 256 rows 520; one CTA, 128 rows 480; a pair of 128 rows 380-460, and no less for
+// fewer rows. Where every tile of the weights is read once, from memory, a CTA has no more
+// than its stages in flight: 520, with nine of them instead of six 380.
 constexpr float kLinearBytesPerCycle = 3580.0f;   // of the memory (6.8 TB/s at 1.9 GHz)
-inline __host__ __device__ float linear_block_cycles(bool pair, int rows, bool streamed)
+constexpr float kLinearL2Cycles = 80e6f / kLinearBytesPerCycle;   // of weights that L2 keeps beside the rows
+inline __host__ __device__ float linear_block_cycles(LinearForm form, int rows, bool streamed)
 {
-    const float block = 256.0f + (pair ? 1.0f : 2.0f) * (float)rows;
-    return streamed && block < 520.0f ? 520.0f : block;
+    const float block = 256.0f + (linear_pair(form) ? 1.0f : 2.0f) * (float)rows;
+    const float least = form == kLinearPairHalf ? 384.0f : streamed ? 520.0f : 0.0f;
+    return block < least ? least : block;
 }
+// The last tile's epilogue, with nothing beside it.
+constexpr float kLinearRowCycles = 16.0f;
 // Publishing and joining the parts of a cut tile (measured: 128 rows in two parts on one
-// CTA 10000 cycles, 256 on a pair 24000).
-inline __host__ __device__ float linear_cut_cycles(bool pair, int rows, int parts, bool even)
+// CTA 10000 cycles, on a pair 9000, 256 on a pair 24000).
+inline __host__ __device__ float linear_cut_cycles(LinearForm form, int rows, int parts, bool even)
 {
-    return (pair ? 1.5f : 1.0f) *
+    return (form == kLinearPair ? 1.5f : form == kLinearPairHalf ? 0.9f : 1.0f) *
            ((even ? 1.0f : 2.0f) * (2500.0f + 20.0f * (float)rows) + 1500.0f + 13.0f * (float)(rows * parts));
 }
 inline __host__ __device__ int linear_part_rows(int rows) { return (rows + 31) / 32 * 32; }
@@ -59,19 +74,21 @@ struct LinearCandidate {
     int full, segments;
     float cycles;
 };
-inline __host__ __device__ LinearCandidate linear_candidate(bool pair, int l, int tiles, int w_tiles, int rows,
+inline __host__ __device__ LinearCandidate linear_candidate(LinearForm form, int l, int tiles, int w_tiles, int rows,
                                                             int k_blocks, int n_units)
 {
-    const int cg = pair ? 2 : 1;
+    const int cg = linear_pair(form) ? 2 : 1;
     const int rounds = (int)((unsigned)tiles / (unsigned)n_units), last = tiles - rounds * n_units;
-    const float block = linear_block_cycles(pair, rows, w_tiles == tiles);
-    const float bytes = (float)w_tiles * (float)k_blocks * (float)(cg * 128 * kLinearBK * 2) * (1.0f / kLinearBytesPerCycle);
+    const float block = linear_block_cycles(form, rows, w_tiles == tiles);
+    const float tile_bytes = (float)k_blocks * (float)(cg * 128 * kLinearBK * 2) * (1.0f / kLinearBytesPerCycle);
+    float bytes = (float)w_tiles * tile_bytes;
     LinearCandidate c{l == 0, tiles, 0, 0.0f};
     if (l == 0) {
         const float whole = tiles ? bytes * ((float)(tiles - last) / (float)tiles) : 0.0f;
         const float run = (float)rounds * (float)k_blocks * block;
         c.cycles = run > whole ? run : whole;
         if (last) c.cycles += bytes - whole > (float)k_blocks * block ? bytes - whole : (float)k_blocks * block;
+        c.cycles += kLinearRowCycles * (float)rows;
         return c;
     }
     // parts have room (and one more: a join reads up to 63 rows on), and the products of the
@@ -88,8 +105,11 @@ inline __host__ __device__ LinearCandidate linear_candidate(bool pair, int l, in
     const unsigned total = left * (unsigned)k_blocks;
     const int parts = even ? l + 1 : (int)((unsigned)n_units / left) + 2;
     c.fits = total >= 2u * (unsigned)c.segments;
+    // runs that do not line up are at different places of K at a time: weights beyond L2 come
+    // from memory again for each tile (700 x 14336 x 4096 in 128 rows: 109 us, now 76)
+    if (!even && bytes > kLinearL2Cycles) bytes = (float)tiles * tile_bytes;
     const float run = ((float)(whole_rounds * k_blocks) + (float)total / (float)c.segments + 0.5f) * block;
-    c.cycles = (run > bytes ? run : bytes) + linear_cut_cycles(pair, rows, parts, even);
+    c.cycles = (run > bytes ? run : bytes) + linear_cut_cycles(form, rows, parts, even);
     return c;
 }
 
@@ -98,9 +118,6 @@ inline __host__ __device__ LinearCandidate linear_candidate(bool pair, int l, in
 constexpr size_t kLinearTicketOffset = 256;
 constexpr size_t kLinearPartOffset = 256 + (size_t)kLinearMaxTickets * 4;
 constexpr size_t kLinearWorkspaceBytes = kLinearPartOffset + (size_t)kLinearPartRows * 128 * 4;
-
-// one CTA per MMA, tiles of 128 columns and up to 32 or 128 rows; a CTA pair per MMA, 256 and 256
-enum LinearForm { kLinearFew = 0, kLinearOne = 1, kLinearPair = 2 };
 
 struct LinearArgs {
     int32_t R;                  // rows of a

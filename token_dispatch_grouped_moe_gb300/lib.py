@@ -795,7 +795,7 @@ def linear(a, w, ws, bias=None, activation=None, residual=None, offsets=None, ou
     return r
 
 
-LINEAR_FORM_FEW, LINEAR_FORM_ONE, LINEAR_FORM_PAIR = 0, 1, 2
+LINEAR_FORM_FEW, LINEAR_FORM_ONE, LINEAR_FORM_PAIR, LINEAR_FORM_PAIR_HALF = 0, 1, 2, 3
 
 
 def linear_form_selftest(R, K, N, G=1, num_sms=152) -> int:
