@@ -171,7 +171,6 @@ moe_status moe_linear(int64_t R, int32_t K, int32_t N, int32_t G, moe_dtype dtyp
     args.err = static_cast<uint32_t*>(ws);
     const LinearForm form = linear_form(R, K, N, G, sms);
     args.tile_rows = linear_rows(form);
-    args.stretch = out_dtype == MOE_FP32 ? 8 : 32;
     return finish(launch_linear(form, out_dtype, tm_a, tm_a_small, tm_w, args, sms, (cudaStream_t)stream), ws,
                   (cudaStream_t)stream);
 }

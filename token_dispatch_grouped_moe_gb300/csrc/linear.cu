@@ -12,11 +12,15 @@
 // form serves a token of a decode step and a prefill. The operands are read as
 // they lie in memory: w with contiguous n (an M-major operand) or contiguous k.
 //
-// The tensor cores' running sum is cut every 2048 k (512 for fp32 outputs): the
-// epilogue warps add each stretch to fp32 registers while the next one is computed
-// into the other TMEM buffer. Its 128 partial sums of 16 products, rounded towards
-// zero, are off by 4e-6 of the result at most times, far below a 16-bit step; those
-// of 32 by 5e-7, as a sum in fp32 is.
+// The tensor cores' running sum is cut every 512 k, whatever the output's type: the epilogue
+// warps add each stretch to fp32 registers while the next one is computed into the other
+// TMEM buffer. The sum in TMEM is rounded towards zero at every step, so a long one drifts:
+// of the result at K = 4096, sums that cancel / sums of one sign, 512 k 4.8e-7 / 0.7e-6 in
+// bf16 and 6.5e-7 / 2.5e-6 in fp16 (a sum in fp32, one product after another, 9e-7); 1024 k
+// 1.0e-6 / 1.7e-6 and 1.3e-6 / 5.5e-6; 2048 k 2.1e-6 / 4.3e-6 and 2.5e-6 / 11e-6. Longer
+// stretches are faster where the tensor cores bound the product (16384 rows of 8 experts 4096
+// -> 14336, sustained, us: 512 k 1233, 1024 1167, 2048 1152; 8192 x 4096 x 4096 with
+// residual 188, 175, 177), but no sum in fp32.
 //
 // Kernel shape: one CTA per SM (384 threads), persistent over (group, row tile, n
 // tile) tiles computed from the group offsets:
@@ -81,6 +85,7 @@ constexpr int EPI_REGS = 216;
 constexpr int OTHER_REGS = 72;
 constexpr int MAX_GROUPS = 256;
 constexpr int BAND = 16;            // row tiles that are taken together
+constexpr int STRETCH = 8;          // K blocks between two reads of the tensor cores' sums
 
 // BN: rows of a tile at most. The form for few rows (32) leaves room for a second
 // CTA on its SM: that of the next kernel, which gets ready meanwhile.
@@ -581,7 +586,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                                                                          abort, args.err)));
                     if (!ok) break;
                     tc_fence_after();
-                    const bool closes = ++in == args.stretch || kb == pc.kb1 - 1;
+                    const bool closes = ++in == STRETCH || kb == pc.kb1 - 1;
                     const int at_stage = stage;
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                     // whether the next block is there, asked before this one's MMAs
@@ -659,7 +664,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
 #pragma unroll
                 for (int c = 0; c < HALF; ++c) acc[c] = of_raw<OUT>(raw[c]);
             }
-            for (int kb = pc.kb0; kb < pc.kb1 && ok; kb += args.stretch) {
+            for (int kb = pc.kb0; kb < pc.kb1 && ok; kb += STRETCH) {
                 ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&st->tfull[buf]), buf_phase, abort, args.err));
                 if (!ok) break;
                 tc_fence_after();

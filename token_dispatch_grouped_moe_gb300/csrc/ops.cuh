@@ -135,7 +135,6 @@ struct LinearArgs {
     int32_t fp16;               // operands: fp16, or bf16
     int32_t w_nk;               // the weights' layout: [G, N, K], or [G, K, N]
     int32_t tile_rows;          // rows of a tile at most
-    int32_t stretch;            // K blocks between two reads of the tensor cores' sums
     int32_t* ticket;            // [kLinearMaxTickets], zero
     float* part;                // [kLinearPartRows, 128]
     uint32_t* err;
