@@ -583,7 +583,8 @@ typedef struct {
  * A logit of -inf is an expert with score 0 (selected, with weight 0, where no
  * other is left; a softmax of nothing but -inf is all 0, and so is the
  * renormalization of a sum of 0). A NaN logit comes after all others, and makes
- * its row's k weights NaN.
+ * its row's k weights NaN. A bias of +inf puts an expert before all others, one of -inf
+ * behind them; several of them are ties.
  * In:  logits[T,E] of type dtype, rows `stride` elements apart; scoring (null:
  *      softmax, no bias, no groups, not renormalized, scale 1).
  * Out: topk_idx[T,k], topk_w[T,k].

@@ -38,3 +38,32 @@ def test_linear_rounds_the_fp32_output_once(lib, ws, R, K, N, G, dtype, one_sign
                           out_dtype=torch.float32)
         assert lib.check(ws) == lib.MOE_OK
         assert torch.equal(out, wide.to(dt)), (act, int((out != wide.to(dt)).sum()), out.numel())
+
+
+# ------------------------------------------------- route_logits: infinities --
+
+@gpu
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("forced", [(5,), (5, 6), (30, 2), (1, 9, 17, 25), (0, 1, 2, 3, 4, 5, 6, 7)])
+@pytest.mark.parametrize("groups,top_groups,group_top", [(1, 1, 1), (4, 2, 1), (4, 2, 2), (8, 1, 2)])
+@pytest.mark.parametrize("T", [1, 301, 8192])
+def test_route_forced_experts(lib, scores, forced, groups, top_groups, group_top, T):
+    """A bias of +inf forces an expert in, by index among several; the others are ordered
+    as ever, also where fp32 does not tell them apart."""
+    g = gen(len(forced) + T)
+    E, k = 32, 4
+    few = torch.randint(0, 3, (T, E), generator=g, device="cuda").float() * 0.5
+    near = (0.75 - (torch.sigmoid(few[0].double()) if scores == "sigmoid" else torch.softmax(few[0].double(), 0))).float()
+    for x, bias in ((few, torch.zeros(E, device="cuda")), (few[:1].expand(T, E).contiguous(), near),
+                    (randn(g, T, E), 0.01 * randn(g, E))):
+        bias[list(forced)] = math.inf
+        for drop in (False, True):
+            if drop:
+                bias[[10, 13, 20]] = -math.inf
+            for renorm in (False, True):
+                opts = dict(scores=scores, bias=bias, groups=groups, top_groups=top_groups, group_top=group_top,
+                            renormalize=renorm)
+                idx = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+                w = torch.full((T, k), math.nan, device="cuda")
+                lib.route_logits(x, k, topk_idx=idx, topk_w=w, **opts)
+                check_route((idx, w), route64(x, k, **opts))

@@ -718,15 +718,17 @@ __device__ __forceinline__ unsigned order_listed(const RouteLogitsArgs& a, const
             // fp64 but for the sum over all experts, whose error moves two keys against one
             // another by 47 * 2^-24 of their scores' difference; compared as pairs of fp32
             const double s64 = score64(le, 0, m, (double)inv), k64 = s64 + (double)be;
+            // (an infinite key, of an infinite bias, has no low part and no error: equal ones are a tie)
             const float high = mine ? (float)k64 : kNegInf, s32 = (float)s64;
-            const float low = high > kNegInf ? (float)(k64 - (double)high) : 0.0f;
+            const float size = fabsf(high) < __builtin_huge_valf() ? fabsf(high) : 0.0f;
+            const float low = fabsf(high) < __builtin_huge_valf() ? (float)(k64 - (double)high) : 0.0f;
             place = maybe = 0;
 #pragma unroll 4
             for (int i = 0; i < most; ++i) {
                 const float oh = __shfl_sync(kAll, high, i, W), ol = __shfl_sync(kAll, low, i, W);
                 const float os = __shfl_sync(kAll, s32, i, W);
-                const float d = (oh - high) + (ol - low), u = 48.0f * 0x1p-24f * fabsf(os - s32) + 0x1p-44f * fabsf(high);
-                const bool same = oh == high && ol == low && (os == s32 || oh == kNegInf);
+                const float d = (oh - high) + (ol - low), u = 48.0f * 0x1p-24f * fabsf(os - s32) + 0x1p-44f * size;
+                const bool same = oh == high && ol == low && (os == s32 || !(fabsf(oh) < __builtin_huge_valf()));
                 const bool first = same ? i < sub : d > u;
                 place += first;
                 maybe += first || (!same && d >= -u);
