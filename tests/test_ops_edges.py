@@ -67,3 +67,20 @@ def test_route_forced_experts(lib, scores, forced, groups, top_groups, group_top
                 w = torch.full((T, k), math.nan, device="cuda")
                 lib.route_logits(x, k, topk_idx=idx, topk_w=w, **opts)
                 check_route((idx, w), route64(x, k, **opts))
+
+
+# ---------------------------------------------------- route_logits: outputs --
+
+@gpu
+def test_route_outputs_can_be_stored(lib):
+    """The two outputs are tensors of their own: stored together, and neither holds the
+    other's memory."""
+    x = randn(gen(1), 40, 64)
+    ids, w = lib.route_logits(x, 6)
+    for t in (ids, w):
+        assert t.storage_offset() == 0 and t.untyped_storage().nbytes() == 40 * 6 * 4
+    memory = io.BytesIO()
+    torch.save({"ids": ids, "w": w}, memory)
+    memory.seek(0)
+    back = torch.load(memory)
+    assert torch.equal(back["ids"], ids) and torch.equal(back["w"], w)
