@@ -310,8 +310,9 @@ moe_status moe_route_ex(const moe_dims* dims, const moe_bf16* x, const moe_bf16*
  * Out: counts[E]; offsets[E+1] (exclusive scan, offsets[E] = R);
  *      src_row[R] (src_row[p] = f, experts in increasing order, f increasing
  *      within an expert); inv_pos[R] (inv_pos[f] = p).
- *      x_perm[R,H] (bf16, may be null): x_perm[p] = x[src_row[p] / k]; x
- *      must be given when x_perm is.
+ *      x_perm[R,H] (may be null): x_perm[p] = x[src_row[p] / k]; x must be
+ *      given when x_perm is. (Rows are copied as they are: bf16, or fp16
+ *      behind the same pointers.)
  * An id outside [0, E) sets MOE_ERR_INVALID_ARG in the device error word and
  * that assignment is skipped (no out-of-bounds write).
  * Also writes the GEMM tile table into `ws` for a later moe_expert_ffn /

@@ -84,3 +84,56 @@ def test_route_outputs_can_be_stored(lib):
     memory.seek(0)
     back = torch.load(memory)
     assert torch.equal(back["ids"], ids) and torch.equal(back["w"], w)
+
+
+# ------------------------------------------------------- permute's row types --
+
+def test_permute_refuses_other_rows(lib):
+    """permute copies rows of 16-bit values as they are: others, of other sizes or not
+    contiguous, are refused before anything is launched."""
+    d = lib.make_dims(4, 64, 64, 8, 2)
+    ids, x = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 64, dtype=torch.bfloat16)
+    one = torch.zeros(256, dtype=torch.uint8)
+    for bad in (x.float(), x.to(torch.int16), x[:3], x[:, :32], x.t(), torch.zeros(4, 128, dtype=torch.bfloat16)[:, ::2]):
+        with pytest.raises(ValueError, match="^x:"):
+            lib.permute(d, ids, one, x=bad, want_x_perm=True)
+        with pytest.raises(ValueError, match="^x:"):
+            lib.permute_static(d, ids, x=bad, want_x_perm=True)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_permute_keeps_the_rows_type(lib, dtype):
+    T, H, E, k = 100, 128, 16, 3
+    g = gen(4)
+    d = lib.make_dims(T, H, 64, E, k)
+    x = randn(g, T, H).to(DTYPES[dtype])
+    ids = randn(g, T, E).topk(k, -1).indices.int()
+    for got in (lib.permute(d, ids, lib.workspace(d), x=x, want_x_perm=True), lib.permute_static(d, ids, x=x, want_x_perm=True)):
+        src, rows = got[2], got[4]
+        # (row p is assignment src[p] = t k + j; indexed on the host)
+        assert rows.dtype == x.dtype and torch.equal(rows.cpu(), x.cpu()[src.cpu().long() // k])
+
+
+@gpu
+@pytest.mark.parametrize("T", [1, 150])
+def test_chain_in_fp16(lib, ws, T):
+    """An expert layer on fp16 rows: router, dispatch, biased gelu experts, weighted sum."""
+    g = gen(T)
+    H, F, E, k = 256, 384, 16, 3
+    d = lib.make_dims(T, H, 64, E, k)
+    x, Wg = randn(g, T, H).half(), (0.1 * randn(g, 1, H, E)).half()
+    w1, b1, w2 = weight(g, E, H, F, torch.float16, "nk"), 0.3 * randn(g, E, F), weight(g, E, F, H, torch.float16, "kn")
+    ids, tw = lib.route_logits(lib.linear(x, Wg, ws, out_dtype=torch.float32), k, renormalize=True)
+    _, offsets, _, inv_pos, rows = lib.permute(d, ids, lib.workspace(d), x=x, want_x_perm=True)
+    y = lib.linear(lib.linear(rows, w1, ws, bias=b1, activation="gelu", offsets=offsets), w2, ws, offsets=offsets)
+    out = lib.combine_rows(y, inv_pos, tw, residual=x)
+    assert out.dtype == torch.float16 and lib.check(ws) == lib.MOE_OK
+    want = x.double()
+    for j in range(k):
+        e = ids[:, j].long()
+        hid = act64("gelu", torch.einsum("th,thf->tf", x.double(), w1.double()[e]) + b1.double()[e])
+        want = want + tw[:, j, None].double() * torch.einsum("tf,tfh->th", hid, w2.double()[e])
+    # h and y are rounded to fp16 on the way, and the output: three half steps
+    rel = float((out.double() - want).norm() / want.norm())
+    assert rel <= 2.0 ** -11 * 3 ** 0.5, rel

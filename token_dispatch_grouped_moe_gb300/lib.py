@@ -361,15 +361,30 @@ def route(dims: Dims, x, Wg, bias=None, topk_idx=None, topk_w=None, stream=None,
         return topk_idx, topk_w
 
 
+def _row_type(dims: Dims, x, dev):
+    """The type of the rows that a dispatch copies: x's, bf16 or fp16 (16-bit values, as they are)."""
+    if x is None:
+        return torch.bfloat16
+    if (x.dtype not in (torch.bfloat16, torch.float16) or tuple(x.shape) != (dims.T, dims.H) or not x.is_contiguous()
+            or x.device != dev):
+        raise ValueError(f"x: expected a contiguous bf16 or fp16 tensor of shape {(dims.T, dims.H)} on {dev}, got "
+                         f"{x.dtype} {tuple(x.shape)} (strides {x.stride()}) on {x.device}")
+    return x.dtype
+
+
 def permute(dims: Dims, topk_idx, ws, x=None, want_x_perm=False, stream=None):
+    """The assignments sorted by expert: (counts [E], offsets [E+1], src_row [T*k],
+    inv_pos [T*k], and with ``want_x_perm`` the rows of x [T,H], bf16 or fp16, in that
+    order, else None)."""
     R, E = dims.T * dims.k, dims.E
     dev = topk_idx.device
+    row_type = _row_type(dims, x, dev) if want_x_perm else None
     with _on(dev, stream):
         counts = torch.empty(E, dtype=torch.int32, device=dev)
         offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
         src_row = torch.empty(R, dtype=torch.int32, device=dev)
         inv_pos = torch.empty(R, dtype=torch.int32, device=dev)
-        x_perm = torch.empty(R, dims.H, dtype=torch.bfloat16, device=dev) if want_x_perm else None
+        x_perm = torch.empty(R, dims.H, dtype=row_type, device=dev) if want_x_perm else None
         _ok(load().moe_permute(ctypes.byref(dims), _p(topk_idx), _p(counts), _p(offsets), _p(src_row),
                                _p(inv_pos), _p(x), _p(x_perm), _p(ws), ws.numel(), _stream(stream)),
             "moe_permute")
@@ -381,12 +396,13 @@ def permute_static(dims: Dims, topk_idx, x=None, want_x_perm=False, stream=None)
     library; calls on one device must not overlap on the GPU)."""
     R, E = dims.T * dims.k, dims.E
     dev = topk_idx.device
+    row_type = _row_type(dims, x, dev) if want_x_perm else None
     with _on(dev, stream):
         counts = torch.empty(E, dtype=torch.int32, device=dev)
         offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
         src_row = torch.empty(R, dtype=torch.int32, device=dev)
         inv_pos = torch.empty(R, dtype=torch.int32, device=dev)
-        x_perm = torch.empty(R, dims.H, dtype=torch.bfloat16, device=dev) if want_x_perm else None
+        x_perm = torch.empty(R, dims.H, dtype=row_type, device=dev) if want_x_perm else None
         _ok(load().moe_permute_static(ctypes.byref(dims), _p(topk_idx), _p(counts), _p(offsets),
                                       _p(src_row), _p(inv_pos), _p(x), _p(x_perm), _stream(stream)),
             "moe_permute_static")
