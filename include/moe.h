@@ -250,6 +250,11 @@ moe_status moe_layer_plan(const moe_dims* dims, moe_plan* plan);
  * device stays usable. Synchronises `stream`. */
 moe_status moe_selftest_wait_timeout(int32_t limit_ms, moe_stream_t stream);
 
+/* Test hook: one device thread that sleeps for `ms` (1..6000) of %globaltimer
+ * time and lets the next kernel of the stream become resident meanwhile. Does
+ * not synchronise. */
+moe_status moe_selftest_hold(int32_t ms, moe_stream_t stream);
+
 /* Test hook of the tensor-core router (MOE_ROUTER_TENSOR): routes x with it
  * as moe_layer_forward would, writing topk_idx[T,k] / topk_w[T,k] and
  * optionally

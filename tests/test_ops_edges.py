@@ -137,3 +137,27 @@ def test_chain_in_fp16(lib, ws, T):
     # h and y are rounded to fp16 on the way, and the output: three half steps
     rel = float((out.double() - want).norm() / want.norm())
     assert rel <= 2.0 ** -11 * 3 ** 0.5, rel
+
+
+# ------------------------------------------- linear behind a long kernel --
+
+def test_hold_limits(lib):
+    for ms in (0, -1, 6001):
+        assert lib.load().moe_selftest_hold(ms, None) == 1
+
+
+@gpu
+@pytest.mark.parametrize("R", [5, 3000])
+def test_linear_behind_a_long_kernel(lib, R):
+    """A dense product is resident while the kernel before it still runs, here for longer
+    than a wait's limit of 4 s: that is no time of its own waits."""
+    g = gen(R)
+    K, N = 1024, 2048
+    a, w = randn(g, R, K).bfloat16(), weight(g, 1, K, N, torch.bfloat16, "kn")
+    own = lib.linear_workspace()
+    want = lib.linear(a, w, own)
+    out = torch.zeros_like(want)
+    lib.selftest_hold(4500)
+    lib.linear(a, w, own, out=out)
+    assert lib.check(own) == lib.MOE_OK
+    assert torch.equal(out, want)

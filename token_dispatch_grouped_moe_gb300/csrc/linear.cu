@@ -573,6 +573,9 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             bool any = false;
             bool ready = false;    // the next block is known to be there
             Walk walk(plan, unit, n_units, k_blocks);
+            // (the limit of the waits below is not to count the kernel before this one, for which
+            // the producers wait)
+            if (!args.offsets) pdl_wait();
             for (Piece pc; ok && rank == 0 && walk.next(pc);) {
                 const Tile it = decode(pc.tile);
                 const uint32_t idesc =

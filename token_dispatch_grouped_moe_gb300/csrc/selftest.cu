@@ -4,7 +4,9 @@
 // readiness counters) gives up after a %globaltimer limit, records
 // MOE_DEV_ERR_TIMEOUT in a device error word and lets the kernel finish, so a
 // fault elsewhere never hangs the GPU. moe_selftest_wait_timeout runs that
-// path on purpose: one thread waits on a flag that nothing sets.
+// path on purpose: one thread waits on a flag that nothing sets. moe_selftest_hold
+// keeps a stream busy behind which the next call's kernel is already resident, so
+// that a wait whose limit counted the kernel before it would run out.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -21,6 +23,20 @@ static __global__ void selftest_wait_kernel(unsigned long long limit_ns)
     __shared__ int abort_flag;
     abort_flag = 0;
     moe::wait_count(&g_never_set, 1, &abort_flag, &g_selftest_err, limit_ns);
+}
+
+static __global__ void selftest_hold_kernel(unsigned long long ns)
+{
+    moe::pdl_launch_dependents();
+    moe::sleep_ns(ns);
+}
+
+extern "C" moe_status moe_selftest_hold(int32_t ms, moe_stream_t stream)
+{
+    if (ms < 1 || ms > 6000) return MOE_ERR_INVALID_ARG;
+    selftest_hold_kernel<<<1, 1, 0, (cudaStream_t)stream>>>((unsigned long long)ms * 1000000ull);
+    moe::count_launch();
+    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 extern "C" moe_status moe_selftest_wait_timeout(int32_t limit_ms, moe_stream_t stream)

@@ -29,7 +29,7 @@ EXPORTS = ["moe_version", "moe_status_string", "moe_workspace_size", "moe_check"
            "moe_layer_forward_host", "moe_host_chunks", "moe_fp8_workspace_size", "moe_add_rmsnorm_fp8",
            "moe_fp8_quantize_weight", "moe_fp8_matmul", "moe_fp8_gated", "moe_fp8_layer_forward",
            "moe_selftest_fp8_form", "moe_route_logits", "moe_linear_workspace_size", "moe_linear", "moe_combine_rows",
-           "moe_selftest_linear_form"]
+           "moe_selftest_linear_form", "moe_selftest_hold"]
 
 OPT_GEMM0_A = 0
 GEMM0_A_PERMUTED = 0      # dispatch copies token rows to x_perm; GEMM0 loads dense tiles
@@ -152,6 +152,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                          ctypes.POINTER(RoutingOut), P, sz, ctypes.POINTER(StageEvents), P]
     lib.moe_selftest_wait_timeout.restype = ctypes.c_int
     lib.moe_selftest_wait_timeout.argtypes = [i32, P]
+    lib.moe_selftest_hold.restype = ctypes.c_int
+    lib.moe_selftest_hold.argtypes = [i32, P]
     lib.moe_selftest_route_tc.restype = ctypes.c_int
     lib.moe_selftest_route_tc.argtypes = [D, P, P, P, i32, i32, P, P, P, P, ctypes.POINTER(ctypes.c_int64),
                                           P, sz, P]
@@ -305,6 +307,11 @@ def launch_count() -> int:
 def selftest_wait_timeout(limit_ms: int = 200, stream=None) -> int:
     """Status of the bounded-wait self-test (MOE_ERR_TIMEOUT is the expected one)."""
     return int(load().moe_selftest_wait_timeout(int(limit_ms), _stream(stream)))
+
+
+def selftest_hold(ms: int, stream=None) -> None:
+    """Keeps the stream busy for ``ms`` with the next kernel resident beside it (test hook)."""
+    _ok(load().moe_selftest_hold(int(ms), _stream(stream)), "moe_selftest_hold")
 
 
 def layer_plan(dims: Dims) -> Plan:
