@@ -601,7 +601,9 @@ moe_status moe_route_logits(int64_t T, int32_t E, int32_t k, moe_dtype dtype, co
                             const moe_scoring* scoring, int32_t* topk_idx, float* topk_w, moe_stream_t stream);
 
 /* relu: max(x, 0); silu: x / (1 + e^-x); gelu: x (1 + erf(x / sqrt 2)) / 2; gelu_tanh:
- * x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2 */
+ * x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2. In fp32, before the output's rounding:
+ * gelu within 2^-19 of itself (for 16-bit outputs 2^-15), silu and gelu_tanh within (5 + 3 |u|)
+ * 2^-23, e^-u being their exponential (0 where that passes 2^126). */
 typedef enum {
     MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_GELU_TANH = 4
 } moe_activation;

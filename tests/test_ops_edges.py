@@ -161,3 +161,50 @@ def test_linear_behind_a_long_kernel(lib, R):
     lib.linear(a, w, own, out=out)
     assert lib.check(own) == lib.MOE_OK
     assert torch.equal(out, want)
+
+
+# ---------------------------------------------- linear: activations' values --
+
+@gpu
+def test_linear_gelu_of_each_value(lib, ws):
+    """gelu point by point (through the bias, the sums being zero), relative to its value
+    also where that is small. In steps of fp32: the fit of erfc 0.9; t = 1 / (1 + 0.305 |x|)
+    2.5, 2.6 times that in the result; its polynomial 3; e^x 2 for ex2 and 1 for its
+    argument; the products 1.5: below 16. Under the smallest normal number it may be 0."""
+    N = 1 << 16
+    a = torch.zeros(1, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(1, 64, N, dtype=torch.bfloat16, device="cuda")
+    for lo, hi in ((-14.0, 9.0), (-4.0, 0.0), (-1e-3, 1e-3), (-9.0, -4.0)):
+        x = torch.linspace(lo, hi, N, device="cuda")[None]
+        got = lib.linear(a, w, ws, bias=x, activation="gelu", out_dtype=torch.float32)[0].double()
+        want = act64("gelu", x[0].double())
+        off = (got - want).abs() - 14 * 2.0 ** -126
+        assert bool((off <= 16 * 2.0 ** -23 * want.abs()).all()), float((off / want.abs()).max()) * 2 ** 23
+        # 16 bits: the fit 4.0e-6, the rest of it as above and the exponent's rounding, x^2 / 2 2.5 half
+        # steps: below 2^-15, and the output's own half step
+        for dt in (torch.bfloat16, torch.float16):
+            got = lib.linear(a.to(dt), w.to(dt), ws, bias=x, activation="gelu")[0].double()
+            least = 14 * 2.0 ** -126 if dt == torch.bfloat16 else 2.0 ** -25
+            tol = torch.finfo(dt).eps / 2 * (1 + 2.0 ** -15) + 2.0 ** -15
+            assert bool(((got - want).abs() <= tol * want.abs() + least).all())
+    x = torch.tensor([[math.inf, -math.inf, math.nan, 0.0, -0.0, 3e38, -3e38, 1e-40]], device="cuda")
+    for dt in (torch.float32, torch.bfloat16):
+        got = lib.linear(a, w[:, :, :8].contiguous(), ws, bias=x, activation="gelu", out_dtype=dt)[0]
+        assert got[0] == math.inf and got[1] == 0 and got[2].isnan() and bool((got[3:5] == 0).all())
+        assert got[5] == x[0, 5].to(dt) and got[6] == 0 and abs(float(got[7])) <= 1e-40
+
+
+@gpu
+@pytest.mark.parametrize("act,lo", [("silu", -80.0), ("gelu_tanh", -9.0)])
+def test_linear_silu_and_gelu_tanh_of_each_value(lib, ws, act, lo):
+    """Their exponential e^-u is within 2.5 steps + 1.2 for each |u| of itself, u 1.5 steps, the sum
+    and the quotient 2.5: 5 + 3 |u| together."""
+    N = 1 << 16
+    a = torch.zeros(1, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(1, 64, N, dtype=torch.bfloat16, device="cuda")
+    x = torch.linspace(lo, 10.0, N, device="cuda")[None]
+    got = lib.linear(a, w, ws, bias=x, activation=act, out_dtype=torch.float32)[0].double()
+    v = x[0].double()
+    u = v if act == "silu" else 2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)
+    want = act64(act, v)
+    assert bool(((got - want).abs() <= (5 + 3 * u.abs()) * 2.0 ** -23 * want.abs()).all())
