@@ -651,6 +651,22 @@ moe_status moe_linear(int64_t R, int32_t K, int32_t N, int32_t G, moe_dtype dtyp
  * the order of its sums. */
 int32_t moe_selftest_linear_form(int64_t R, int32_t K, int32_t N, int32_t G, int32_t num_sms);
 
+/* Test hook (host only): the schedule of a product on a device of num_sms SMs, as its
+ * kernel derives it from the offsets (offsets[G+1] on the host, null = one group): the first
+ * `whole` tiles one a CTA (or pair), the K blocks of the others, end to end, in `segments`
+ * equal runs, one a CTA. */
+typedef struct {
+    int32_t form;         /* moe_selftest_linear_form */
+    int32_t units;        /* CTAs (or pairs) */
+    int32_t tiles;
+    int32_t whole;
+    int32_t segments;     /* 0: no tile is cut */
+    int32_t part_rows;    /* rows that a part of a cut tile has room for in the workspace */
+    int32_t most_parts;   /* of a cut tile */
+} moe_linear_schedule;
+moe_status moe_selftest_linear_schedule(int64_t R, int32_t K, int32_t N, int32_t G, const int32_t* offsets,
+                                        int32_t num_sms, moe_linear_schedule* schedule);
+
 /*
  * The weighted sum of experts' rows, back in token order:
  *   out[t,:] = sum over ranks j (in order) of topk_w[t,j] y[inv_pos[t,j],:]

@@ -4,6 +4,7 @@ test_ops.py holds them to. Tolerances are derived where they stand, in steps of 
 """
 import io
 import math
+import random
 
 import pytest
 import torch
@@ -208,3 +209,152 @@ def test_linear_silu_and_gelu_tanh_of_each_value(lib, ws, act, lo):
     u = v if act == "silu" else 2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)
     want = act64(act, v)
     assert bool(((got - want).abs() <= (5 + 3 * u.abs()) * 2.0 ** -23 * want.abs()).all())
+
+
+# ----------------------------------------------------- linear: its schedules --
+
+FEW, ONE, PAIR, HALF = range(4)
+SCHEDULES = [   # form, how its tiles are cut, parts of a cut tile at most, K, N, rows of each group
+    (FEW, "even", 2, 1280, 7552, [1]), (FEW, "even", 3, 1064, 4976, [3]), (FEW, "even", 15, 8192, 1000, [16]),
+    (FEW, "uneven", 2, 984, 20496, [1]), (FEW, "uneven", 2, 1512, 40320, [7]), (FEW, "uneven", 3, 3008, 9840, [1]),
+    (FEW, "uneven", 3, 9592, 12096, [16]), (FEW, "uneven", 4, 7176, 6480, [2]),
+    (ONE, "even", 2, 4144, 8, [8653]), (ONE, "even", 2, 2496, 3680, [1, 1]), (ONE, "even", 3, 3184, 8, [5179]),
+    (ONE, "even", 3, 1480, 8, [1, 0, 1, 0, 1, 5, 72, 1]), (ONE, "even", 5, 4368, 8, [3442]),
+    (ONE, "uneven", 2, 2504, 16, [19486]), (ONE, "uneven", 2, 1376, 9896, [0, 1, 1]), (ONE, "uneven", 2, 2944, 39488, [38]),
+    (ONE, "uneven", 3, 4376, 8, [9867]), (ONE, "uneven", 2, 2040, 104, [22554]), (ONE, "uneven", 4, 7296, 8, [6822]),
+    (ONE, "uneven", 4, 14664, 1640, [0, 0, 1, 1, 0, 1, 1, 0]),
+    (PAIR, "even", 2, 10232, 6480, [130]), (PAIR, "even", 3, 7464, 5408, [147]), (PAIR, "even", 3, 12856, 1208, [1280]),
+    (PAIR, "even", 3, 8848, 136, [154, 0, 3, 0, 0, 1, 400, 353, 0, 0, 1013, 0, 0, 570, 2129, 11]),
+    (PAIR, "uneven", 2, 4440, 20048, [161]), (PAIR, "uneven", 2, 6048, 3624, [1299]), (PAIR, "uneven", 2, 4384, 7872, [1270]),
+    (PAIR, "uneven", 2, 4720, 3888, [786, 1]), (PAIR, "uneven", 2, 5312, 2624, [1580, 1710]),
+    (PAIR, "uneven", 3, 11568, 10464, [132]),
+    (PAIR, "uneven", 3, 15768, 272, [1, 1, 1, 0, 1, 40, 1, 1, 1, 0, 9, 66, 2255, 0, 0, 1]),
+    (HALF, "even", 2, 2408, 8, [3698]), (HALF, "even", 2, 1656, 5800, [0, 1]), (HALF, "even", 3, 2200, 776, [500]),
+    (HALF, "even", 5, 6000, 264, [330]), (HALF, "uneven", 2, 1440, 19624, [20]), (HALF, "uneven", 2, 1592, 39016, [18]),
+    (HALF, "uneven", 2, 1552, 3304, [1, 0, 2, 1, 1, 1, 0, 1]), (HALF, "uneven", 3, 5576, 144, [4891]),
+    (HALF, "uneven", 3, 4688, 464, [910, 0, 1, 1, 121, 2, 1, 1, 0, 0, 0, 1, 1, 366, 0, 1]),
+    (HALF, "uneven", 4, 8872, 136, [3395]), (HALF, "uneven", 4, 8848, 24, [0, 1, 1, 1, 2641, 8, 38, 1]),
+]
+
+
+def how_cut(s):
+    if not s.segments:
+        return "whole"
+    left = s.tiles - s.whole
+    return "even" if s.segments % left == 0 and s.segments // left == s.most_parts else "uneven"
+
+
+def walk_schedule(s, K, form):
+    """Every run of a schedule, block by block, as the kernel walks it: each cut tile's blocks are
+    computed once, its parts lie where its join reads them, and all of it in the workspace."""
+    k_blocks, left, ctas = -(-K // 64), s.tiles - s.whole, 2 if form >= PAIR else 1
+    total, pieces = left * k_blocks, {}
+    assert total * (s.segments + 1) < 2 ** 32 and s.segments <= s.units
+    for unit in range(s.segments):
+        pos, end = total * unit // s.segments, total * (unit + 1) // s.segments
+        assert pos < end
+        while pos < end:
+            q, kb0 = divmod(pos, k_blocks)
+            kb1 = min(k_blocks, kb0 + end - pos)
+            pieces.setdefault(q, []).append((kb0, kb1, unit))
+            pos += kb1 - kb0
+    assert sorted(pieces) == list(range(left))
+    slots = set()
+    for q, found in pieces.items():
+        assert [a for a, _, _ in found] == [0] + [b for _, b, _ in found[:-1]] and found[-1][1] == k_blocks
+        if len(found) == 1:
+            continue
+        first = ((q * k_blocks + 1) * s.segments - 1) // total
+        last = ((q + 1) * k_blocks * s.segments - 1) // total
+        written = [2 * unit + (kb0 == 0) for kb0, _, unit in found]
+        assert [u for _, _, u in found] == list(range(first, last + 1)) and len(found) <= s.most_parts
+        assert written == [2 * first + 1] + [2 * (first + i) for i in range(1, len(found))]
+        assert not slots & set(written)
+        slots |= set(written)
+    # 512 tickets, one for each tile and CTA; 81920 rows of parts, of which a join reads up to 63 past its own
+    assert left * ctas <= 512 and s.part_rows % 32 == 0
+    assert not slots or (max(slots) + 1) * s.part_rows * ctas + 63 <= 81920
+
+
+def test_linear_schedules(lib):
+    """What test_linear_of_every_schedule runs is what its list says; of each form whole tiles, even and
+    uneven cuts and joins of two, three and more parts are there."""
+    seen = set()
+    for form, cut, parts, K, N, counts in SCHEDULES:
+        s = lib.linear_schedule_selftest(counts, K, N)
+        assert (s.form, how_cut(s), s.most_parts) == (form, cut, parts), (K, N, counts, s.form, how_cut(s), s.most_parts)
+        walk_schedule(s, K, form)
+        seen.add((form, cut, min(parts, 4), s.whole > 0))
+        assert s.form == lib.linear_form_selftest(sum(counts), K, N, len(counts))
+    assert {(f, c, p) for f, c, p, _ in seen} >= {(f, c, p) for f in range(4) for c in ("even", "uneven") for p in (2, 3)}
+    assert {(f, p) for f, c, p, _ in seen if c == "uneven"} >= {(FEW, 4), (ONE, 4), (HALF, 4)}
+    assert {f for f, c, _, rounds in seen if c == "uneven" and rounds} == {FEW, ONE, PAIR, HALF}
+    assert lib.linear_schedule_selftest([0, 0], 64, 64).tiles == 0
+    for bad in ([-1], [0, -1], [5, -1, 3]):
+        with pytest.raises(lib.MoeError):
+            lib.linear_schedule_selftest(bad, 64, 64)
+
+
+def test_linear_schedules_fit_the_workspace(lib):
+    rng = random.Random(7)
+
+    def log_int(lo, hi, step=1):
+        return max(lo, round(math.exp(rng.uniform(math.log(lo), math.log(hi))) / step) * step)
+
+    cuts = set()
+    for _ in range(4000):
+        G = rng.choice([1, 1, 2, 8, 64, 256])
+        counts = [log_int(1, 100000) if G == 1 else rng.choice([0, 1, log_int(1, 4000)]) for _ in range(G)]
+        K, N, sms = log_int(8, 60000, 8), log_int(8, 60000, 8), rng.choice([152, 152, 148, 76, 20, 2, 1])
+        if not sum(counts):
+            continue
+        s = lib.linear_schedule_selftest(counts, K, N, sms)
+        assert s.whole <= s.tiles and (s.segments > 0) == (s.whole < s.tiles)
+        if s.segments:
+            walk_schedule(s, K, s.form)
+            cuts.add((s.form, how_cut(s), sms >= 148))
+    assert len(cuts) >= 12
+
+
+@gpu
+@pytest.mark.parametrize("form,cut,parts,K,N,counts", SCHEDULES,
+                         ids=lambda v: str(v) if not isinstance(v, list) else f"{len(v)}g{sum(v)}r")
+@pytest.mark.parametrize("layout", ["kn", "nk"])
+def test_linear_of_every_schedule(lib, form, cut, parts, K, N, counts, layout):
+    """Joins of cut tiles of every form: with the whole epilogue, twice with the same bits, the
+    workspace's head left as found (no ticket, no error), rows of no group left alone."""
+    g = gen(K + N + form)
+    G, R = len(counts), sum(counts)
+    a, w = randn(g, R, K).bfloat16(), weight(g, G, K, N, torch.bfloat16, layout)
+    off, ends = offsets_of(counts)
+    bias, res = randn(g, G, N), randn(g, R, N)
+    ws = lib.linear_workspace()
+    out = [torch.full((R + 2, N), -7.0, device="cuda") for _ in range(2)]
+    for o in out:
+        lib.linear(a, w, ws, bias=bias, activation="silu", residual=res, offsets=off, out_dtype=torch.float32, out=o[1:R + 1])
+    assert not bool(ws[: lib.LINEAR_WORKSPACE_ZEROS].any())
+    assert torch.equal(out[0], out[1]) and bool((out[0][[0, -1]] == -7.0).all())
+    check_linear(out[0][1:-1], *linear64(a, w, ends, bias, "silu", res), K)
+    # the early residual (no activation), in place
+    both = torch.cat([res, res]).bfloat16()[:R]
+    want = lib.linear(a, w, ws, bias=bias, residual=both, offsets=off)
+    assert torch.equal(lib.linear(a, w, ws, bias=bias, residual=both, offsets=off, out=both), want)
+    assert not bool(ws[: lib.LINEAR_WORKSPACE_ZEROS].any())
+
+
+@gpu
+@pytest.mark.parametrize("G,K,N", [(8, 4096, 256), (16, 2048, 1408), (4, 7168, 2048)])
+def test_linear_of_skewed_groups(lib, ws, G, K, N):
+    """The form goes by the rows' mean, the schedule by the rows that there are: nearly all rows in
+    one group, in the first, the last, and none but one."""
+    R = 1024
+    for hot in (0, G // 2, G - 1):
+        for rest in (0, 3):
+            g = gen(hot + rest)
+            counts = [rest] * G
+            counts[hot] = R - rest * (G - 1)
+            off, ends = offsets_of(counts)
+            a, w = randn(g, R, K).bfloat16(), weight(g, G, K, N, torch.bfloat16, "kn")
+            out = lib.linear(a, w, ws, offsets=off, out_dtype=torch.float32)
+            assert lib.check(ws) == lib.MOE_OK
+            check_linear(out, *linear64(a, w, ends), K)

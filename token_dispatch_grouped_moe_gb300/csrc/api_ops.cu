@@ -181,6 +181,47 @@ int32_t moe_selftest_linear_form(int64_t R, int32_t K, int32_t N, int32_t G, int
     return linear_form(R, K, N, G, num_sms);
 }
 
+moe_status moe_selftest_linear_schedule(int64_t R, int32_t K, int32_t N, int32_t G, const int32_t* offsets,
+                                        int32_t num_sms, moe_linear_schedule* schedule)
+{
+    if (!schedule || num_sms <= 0 || (!offsets && G != 1)) return MOE_ERR_INVALID_ARG;
+    MOE_TRY_STATUS(check_linear(R, K, N, G));
+    *schedule = moe_linear_schedule{};
+    if (R == 0) return MOE_OK;   // nothing is launched
+    const LinearForm form = linear_form(R, K, N, G, num_sms);
+    const bool pair = linear_pair(form);
+    const int step = pair ? 32 : 16, cap = linear_rows(form), units = pair ? num_sms / 2 : num_sms;
+    const int n_tiles = (int)(((int64_t)N + (pair ? 255 : 127)) / (pair ? 256 : 128));
+    const int k_blocks = (K + kLinearBK - 1) / kLinearBK;
+    int row_tiles = 0, most = 0, groups = 0;
+    for (int g = 0; g < G; ++g) {
+        const int64_t lo = offsets ? offsets[g] : 0, hi = offsets ? offsets[g + 1] : R;
+        if (lo < 0 || hi < lo || hi > R) return MOE_ERR_INVALID_ARG;
+        if (hi == lo) continue;
+        const int rows = (int)(hi - lo), tiles = (int)((hi - lo + cap - 1) / cap);
+        const int per = (int)(((int64_t)rows + tiles - 1) / tiles + step - 1) / step * step;
+        most = per > most ? per : most;
+        row_tiles += tiles;
+        ++groups;
+    }
+    const int tiles = row_tiles * n_tiles;
+    LinearCandidate best{};
+    uint32_t least = 0xffffffffu;
+    for (int l = 0; l < 32; ++l) {
+        const LinearCandidate c = linear_candidate(form, l, tiles, groups * n_tiles, most, k_blocks, units);
+        const uint32_t key = linear_candidate_key(c, l);
+        if (key < least) { least = key; best = c; }
+    }
+    *schedule = moe_linear_schedule{form, units, tiles, best.full, best.segments, linear_part_rows(most), 0};
+    const uint32_t total = (uint32_t)(tiles - best.full) * (uint32_t)k_blocks, runs = (uint32_t)best.segments;
+    for (int q = 0; runs && q < tiles - best.full; ++q) {
+        const int parts = linear_segment_of((uint32_t)(q + 1) * (uint32_t)k_blocks - 1, runs, total) -
+                          linear_segment_of((uint32_t)q * (uint32_t)k_blocks, runs, total) + 1;
+        if (parts > schedule->most_parts) schedule->most_parts = parts;
+    }
+    return MOE_OK;
+}
+
 moe_status moe_combine_rows(int64_t T, int32_t H, int32_t k, int64_t R, moe_dtype dtype, const void* y,
                             int64_t y_stride, const int32_t* inv_pos, const float* topk_w, moe_dtype out_dtype,
                             const void* residual, int64_t residual_stride, void* out, int64_t out_stride,

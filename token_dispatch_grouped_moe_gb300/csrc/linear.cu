@@ -212,7 +212,7 @@ struct Walk {   // make_plan keeps the products below 2^32
 __device__ __forceinline__ int first_part(const Plan& p, int q, int k_blocks, int& parts)
 {
     const uint32_t total = (uint32_t)(p.tiles - p.full) * (uint32_t)k_blocks;
-    auto segment_of = [&](uint32_t block) { return (int)(((block + 1) * (uint32_t)p.segments - 1) / total); };
+    auto segment_of = [&](uint32_t block) { return linear_segment_of(block, (uint32_t)p.segments, total); };
     const int first = segment_of((uint32_t)q * (uint32_t)k_blocks);
     parts = segment_of((uint32_t)(q + 1) * (uint32_t)k_blocks - 1) - first + 1;
     return first;
@@ -224,9 +224,7 @@ template <bool PAIR, int BN>
 __device__ __forceinline__ Plan make_plan(int tiles, int w_tiles, int rows, int k_blocks, int n_units, int lane)
 {
     const LinearCandidate c = linear_candidate(linear_form_of(PAIR, BN), lane, tiles, w_tiles, rows, k_blocks, n_units);
-    // the least cost (its low bits give way to the lane)
-    const uint32_t key = c.fits ? (__float_as_uint(c.cycles) & ~31u) | (uint32_t)lane : 0xffffffffu;
-    const int best = (int)(__reduce_min_sync(0xffffffffu, key) & 31u);
+    const int best = (int)(__reduce_min_sync(0xffffffffu, linear_candidate_key(c, lane)) & 31u);
     return Plan{tiles, __shfl_sync(0xffffffffu, c.full, best), __shfl_sync(0xffffffffu, c.segments, best),
                 linear_part_rows(rows)};
 }

@@ -113,6 +113,18 @@ inline __host__ __device__ LinearCandidate linear_candidate(LinearForm form, int
     return c;
 }
 
+// The candidate of the least cost: the lesser key (the cost's low bits give way to l).
+inline __host__ __device__ uint32_t linear_candidate_key(const LinearCandidate& c, int l)
+{
+    union { float f; uint32_t u; } cycles = {c.cycles};
+    return c.fits ? (cycles.u & ~31u) | (uint32_t)l : 0xffffffffu;
+}
+// The run (of `segments` equal ones over `total` K blocks) that holds a block.
+inline __host__ __device__ int linear_segment_of(uint32_t block, uint32_t segments, uint32_t total)
+{
+    return (int)(((block + 1) * segments - 1) / total);
+}
+
 // The workspace of the product: the error word, the tiles' tickets (zero between
 // calls), the parts.
 constexpr size_t kLinearTicketOffset = 256;

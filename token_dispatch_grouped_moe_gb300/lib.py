@@ -29,7 +29,7 @@ EXPORTS = ["moe_version", "moe_status_string", "moe_workspace_size", "moe_check"
            "moe_layer_forward_host", "moe_host_chunks", "moe_fp8_workspace_size", "moe_add_rmsnorm_fp8",
            "moe_fp8_quantize_weight", "moe_fp8_matmul", "moe_fp8_gated", "moe_fp8_layer_forward",
            "moe_selftest_fp8_form", "moe_route_logits", "moe_linear_workspace_size", "moe_linear", "moe_combine_rows",
-           "moe_selftest_linear_form", "moe_selftest_hold"]
+           "moe_selftest_linear_form", "moe_selftest_linear_schedule", "moe_selftest_hold"]
 
 OPT_GEMM0_A = 0
 GEMM0_A_PERMUTED = 0      # dispatch copies token rows to x_perm; GEMM0 loads dense tiles
@@ -98,6 +98,10 @@ class Scoring(ctypes.Structure):
 class Epilogue(ctypes.Structure):
     _fields_ = [("bias", ctypes.c_void_p), ("bias_dtype", ctypes.c_int32), ("activation", ctypes.c_int32),
                 ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64)]
+
+
+class LinearSchedule(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("form", "units", "tiles", "whole", "segments", "part_rows", "most_parts")]
 
 
 class Fp8Ffn(ctypes.Structure):
@@ -190,6 +194,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_linear.argtypes = [i64, i32, i32, i32, i32, P, i64, P, P, i32, ctypes.POINTER(Epilogue), i32, P, i64, P, sz, P]
     lib.moe_selftest_linear_form.restype = i32
     lib.moe_selftest_linear_form.argtypes = [i64, i32, i32, i32, i32]
+    lib.moe_selftest_linear_schedule.restype = ctypes.c_int
+    lib.moe_selftest_linear_schedule.argtypes = [i64, i32, i32, i32, P, i32, ctypes.POINTER(LinearSchedule)]
     lib.moe_combine_rows.restype = ctypes.c_int
     lib.moe_combine_rows.argtypes = [i64, i32, i32, i64, i32, P, i64, P, P, i32, P, i64, P, i64, P]
     _lib = lib
@@ -824,6 +830,17 @@ LINEAR_FORM_FEW, LINEAR_FORM_ONE, LINEAR_FORM_PAIR, LINEAR_FORM_PAIR_HALF = 0, 1
 def linear_form_selftest(R, K, N, G=1, num_sms=152) -> int:
     """Which kernel a product of these sizes runs (test hook moe_selftest_linear_form)."""
     return int(load().moe_selftest_linear_form(R, K, N, G, num_sms))
+
+
+def linear_schedule_selftest(counts, K, N, num_sms=152) -> LinearSchedule:
+    """The schedule of a product over groups of ``counts`` rows (test hook moe_selftest_linear_schedule)."""
+    offsets = (ctypes.c_int32 * (len(counts) + 1))()
+    for g, c in enumerate(counts):
+        offsets[g + 1] = offsets[g] + c
+    s = LinearSchedule()
+    _ok(load().moe_selftest_linear_schedule(sum(counts), K, N, len(counts), offsets, num_sms, ctypes.byref(s)),
+        "moe_selftest_linear_schedule")
+    return s
 
 
 def combine_rows(y, inv_pos, topk_w, residual=None, out_dtype=None, out=None, stream=None):
