@@ -637,7 +637,7 @@ size_t moe_linear_workspace_size(void);
  *      offsets[G+1] (device); w of type dtype; epilogue (nullable).
  * Out: out[R,N] of type out_dtype (dtype or fp32), rows out_stride apart; its memory
  *      may be the residual's, and no other input's.
- * K and N multiples of 8 up to 2^30, G <= 256; a and w 16-byte aligned, a_stride a multiple of 8,
+ * K a multiple of 8, for MOE_WEIGHT_KN N too, both up to 2^30; G <= 256; a and w 16-byte aligned, a_stride a multiple of 8,
  * the others aligned to their type.
  */
 moe_status moe_linear(int64_t R, int32_t K, int32_t N, int32_t G, moe_dtype dtype, const void* a, int64_t a_stride,
@@ -647,7 +647,7 @@ moe_status moe_linear(int64_t R, int32_t K, int32_t N, int32_t G, moe_dtype dtyp
 
 /* Test hook (host only): which kernel a product of these sizes runs on a device of
  * num_sms SMs: 0 tiles of up to 32 rows, 1 of up to 128 (one CTA per MMA), 2 and 3 a
- * CTA pair with up to 256 and 128; -1 for sizes that the call refuses. The result does not depend on it but for
+ * CTA pair with up to 256 and 128; -1 for sizes that the call refuses (with MOE_WEIGHT_KN). The result does not depend on it but for
  * the order of its sums. */
 int32_t moe_selftest_linear_form(int64_t R, int32_t K, int32_t N, int32_t G, int32_t num_sms);
 

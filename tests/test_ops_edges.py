@@ -2,6 +2,7 @@
 test_ops.py holds them to. Tolerances are derived where they stand, in steps of fp32
 (2^-23 of a value; half of one for a rounding).
 """
+import ctypes
 import io
 import math
 import random
@@ -358,3 +359,53 @@ def test_linear_of_skewed_groups(lib, ws, G, K, N):
             out = lib.linear(a, w, ws, offsets=off, out_dtype=torch.float32)
             assert lib.check(ws) == lib.MOE_OK
             check_linear(out, *linear64(a, w, ends), K)
+
+
+# ------------------------------------------------------- linear: any number of columns --
+
+def test_linear_columns_on_the_host(lib):
+    """Weights with contiguous k may have any number of columns; those with contiguous n a
+    multiple of 8. (No GPU here: what is accepted ends at the missing device.)"""
+    need = lib.load().moe_linear_workspace_size()
+    p, ws = ctypes.c_void_p(256), ctypes.c_void_p(4096)
+
+    def call(layout, K, N):
+        return lib.load().moe_linear(4, K, N, 1, 0, p, K, None, p, layout, None, 0, p, N, ws, need, None)
+
+    assert call(0, 64, 60) == 2 and call(0, 64, 1) == 2 and call(1, 60, 64) == 2 and call(1, 64, 0) == 1
+    if not torch.cuda.is_available():
+        assert call(1, 64, 60) == call(1, 64, 1) == call(0, 64, 64) not in (0, 1, 2, 3)
+
+
+@gpu
+@pytest.mark.parametrize("N", [1, 4, 60, 65, 129, 255, 261])
+@pytest.mark.parametrize("K,counts", [(2048, [3]), (264, [200]), (4096, [300]), (512, [6000]), (4160, [900]), (72, [5, 0, 130, 1]),
+                                      (128, [700, 1, 900]), (14336, [2, 40])])
+@pytest.mark.parametrize("out_dtype", ["bf16", "fp32"])
+def test_linear_of_any_number_of_columns(lib, ws, N, K, counts, out_dtype):
+    g = gen(N + K)
+    R, G, od = sum(counts), len(counts), DTYPES[out_dtype]
+    a, w = randn(g, R, K).bfloat16(), weight(g, G, K, N, torch.bfloat16, "nk")
+    off, ends = offsets_of(counts)
+    bias, res = randn(g, G, N), randn(g, R, N).to(od)
+    wide = torch.full((R, N + 6), -7.0, dtype=od, device="cuda")
+    out = lib.linear(a, w, ws, offsets=off, out_dtype=od, out=wide[:, 3:3 + N])
+    assert lib.check(ws) == lib.MOE_OK
+    assert bool((wide[:, :3] == -7).all()) and bool((wide[:, 3 + N:] == -7).all())
+    check_linear(out, *linear64(a, w, ends), K)
+    for act in (None, "gelu"):
+        out = lib.linear(a, w, ws, bias=bias, activation=act, residual=res, offsets=off, out_dtype=od)
+        check_linear(out, *linear64(a, w, ends, bias, act, res), K)
+    if N % 8 and N > 1:
+        with pytest.raises(lib.MoeError):
+            lib.linear(a, w.contiguous(), ws, offsets=off)
+
+
+@gpu
+def test_route_from_the_logits_of_any_number_of_experts(lib, ws):
+    g = gen(60)
+    T, H, E, k = 333, 512, 60, 4
+    x, Wg = randn(g, T, H).bfloat16(), randn(g, E, H).bfloat16() * 0.1
+    logits = lib.linear(x, Wg[None].transpose(1, 2), ws, out_dtype=torch.float32)
+    check_linear(logits, *linear64(x, Wg[None].transpose(1, 2), [0, T]), H)
+    check_route(lib.route_logits(logits, k, renormalize=True), route64(logits, k, renormalize=True))

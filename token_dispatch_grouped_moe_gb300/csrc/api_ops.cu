@@ -22,11 +22,12 @@ static_assert(kLinearPartOffset == MOE_LINEAR_WORKSPACE_ZEROS, "what has to be z
 
 bool is_dtype(moe_dtype t) { return t == MOE_BF16 || t == MOE_FP16 || t == MOE_FP32; }
 int size_of(moe_dtype t) { return t == MOE_FP32 ? 4 : 2; }
-// The sizes of a product: R rows, G weights of [K, N].
-moe_status check_linear(int64_t R, int32_t K, int32_t N, int32_t G)
+// The sizes of a product: R rows, G weights of [K, N] (a copy's rows of contiguous values, n
+// or k, are 16 bytes apart).
+moe_status check_linear(int64_t R, int32_t K, int32_t N, int32_t G, moe_weight_layout layout)
 {
     if (R < 0 || K <= 0 || N <= 0 || G <= 0) return MOE_ERR_INVALID_ARG;
-    if (K % 8 || N % 8 || K > (1 << 30) || N > (1 << 30) || G > kMaxExperts || R >= ((int64_t)1 << 31) - 256)
+    if (K % 8 || (layout == MOE_WEIGHT_KN && N % 8) || K > (1 << 30) || N > (1 << 30) || G > kMaxExperts || R >= ((int64_t)1 << 31) - 256)
         return MOE_ERR_UNSUPPORTED;
     // tiles, and a round of them more, are counted in 32 bits
     if ((R / 128 + G) * (((int64_t)N + 127) / 128) >= ((int64_t)1 << 31) - (1 << 16)) return MOE_ERR_UNSUPPORTED;
@@ -127,7 +128,7 @@ moe_status moe_linear(int64_t R, int32_t K, int32_t N, int32_t G, moe_dtype dtyp
     if (dtype != MOE_BF16 && dtype != MOE_FP16) return MOE_ERR_UNSUPPORTED;
     if (out_dtype != dtype && out_dtype != MOE_FP32) return MOE_ERR_UNSUPPORTED;
     if (e.bias && e.bias_dtype != dtype && e.bias_dtype != MOE_FP32) return MOE_ERR_UNSUPPORTED;
-    MOE_TRY_STATUS(check_linear(R, K, N, G));
+    MOE_TRY_STATUS(check_linear(R, K, N, G, layout));
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < kLinearWorkspaceBytes) return MOE_ERR_WORKSPACE;
     if (R == 0) return MOE_OK;
     if (!a || !w || !out || !aligned16(a) || !aligned16(w)) return MOE_ERR_INVALID_ARG;
@@ -177,7 +178,7 @@ moe_status moe_linear(int64_t R, int32_t K, int32_t N, int32_t G, moe_dtype dtyp
 
 int32_t moe_selftest_linear_form(int64_t R, int32_t K, int32_t N, int32_t G, int32_t num_sms)
 {
-    if (check_linear(R, K, N, G) != MOE_OK || R == 0 || num_sms <= 0) return -1;
+    if (check_linear(R, K, N, G, MOE_WEIGHT_KN) != MOE_OK || R == 0 || num_sms <= 0) return -1;
     return linear_form(R, K, N, G, num_sms);
 }
 
@@ -185,7 +186,7 @@ moe_status moe_selftest_linear_schedule(int64_t R, int32_t K, int32_t N, int32_t
                                         int32_t num_sms, moe_linear_schedule* schedule)
 {
     if (!schedule || num_sms <= 0 || (!offsets && G != 1)) return MOE_ERR_INVALID_ARG;
-    MOE_TRY_STATUS(check_linear(R, K, N, G));
+    MOE_TRY_STATUS(check_linear(R, K, N, G, MOE_WEIGHT_NK));
     *schedule = moe_linear_schedule{};
     if (R == 0) return MOE_OK;   // nothing is launched
     const LinearForm form = linear_form(R, K, N, G, num_sms);

@@ -338,8 +338,8 @@ PyObject* linear(PyObject* const* a)
     const at::ScalarType type = A.scalar_type(), out_type = f32 ? at::kFloat : type;
     const at::Device dev = A.device();
     expect_rows("a", A, type, R, K, dev);
-    // [G, K, N] with contiguous n, or the view of [G, N, K] with contiguous k
-    const bool kn = w.is_contiguous(), nk = !kn && w.transpose(1, 2).is_contiguous();
+    // [G, K, N] with contiguous n, or the view of [G, N, K] with contiguous k (one column may be either)
+    const bool kn = w.is_contiguous(), nk = (!kn || N % 8) && w.transpose(1, 2).is_contiguous();
     if (w.scalar_type() != type || !is_size(w, {G, K, N}) || w.device() != dev || !(kn || nk))
         refuse("w", w, described("(contiguous, or the transpose of a contiguous) a", type, {G, K, N}, dev));
     if (bias) expect("bias", *bias, bias->scalar_type() == at::kFloat ? at::kFloat : type, {G, N}, dev);

@@ -809,7 +809,8 @@ def linear(a, w, ws, bias=None, activation=None, residual=None, offsets=None, ou
     """out[p] = act(a[p] w[g] + bias[g]) + residual[p] for the rows p of group g,
     offsets[g] <= p < offsets[g+1] (one group without offsets): a [R,K] in bf16 or
     fp16 (any row stride that is a multiple of 8), w [G,K,N] of its type, contiguous
-    or the transpose of a contiguous [G,N,K]; bias [G,N] in fp32 or a's type;
+    (N then a multiple of 8, as K) or the transpose of a contiguous [G,N,K] (any N); bias
+    [G,N] in fp32 or a's type;
     ``activation`` None, "relu", "silu", "gelu" or "gelu_tanh"; out and residual [R,N]
     (any row stride from N on) in a's type or, with ``out_dtype``, fp32. ``out`` may be
     the residual's memory. Rows outside every group are not written."""
