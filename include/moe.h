@@ -591,6 +591,8 @@ typedef struct {
  * renormalization of a sum of 0). A NaN logit comes after all others, and makes
  * its row's k weights NaN. A bias of +inf puts an expert before all others, one of -inf
  * behind them; several of them are ties.
+ * Weights are fp32: within (56 + 2 d) 2^-24 of themselves, d the logit's distance from its
+ * row's largest (sigmoid: 28 * 2^-24); scores below 2^-126 may be 0.
  * In:  logits[T,E] of type dtype, rows `stride` elements apart; scoring (null:
  *      softmax, no bias, no groups, not renormalized, scale 1).
  * Out: topk_idx[T,k], topk_w[T,k].

@@ -409,3 +409,28 @@ def test_route_from_the_logits_of_any_number_of_experts(lib, ws):
     logits = lib.linear(x, Wg[None].transpose(1, 2), ws, out_dtype=torch.float32)
     check_linear(logits, *linear64(x, Wg[None].transpose(1, 2), [0, T]), H)
     check_route(lib.route_logits(logits, k, renormalize=True), route64(logits, k, renormalize=True))
+
+
+# ------------------------------------------------- route_logits: the weights' accuracy --
+
+@gpu
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,spread", [(256, 8, 1, 1.0), (256, 8, 8, 12.0), (60, 4, 1, 30.0), (16, 8, 4, 4.0), (8, 2, 1, 3.0)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_route_weights_accuracy(lib, scores, E, k, groups, spread, biased):
+    """Half steps of fp32 (2^-24): a softmax score is e^d / the sum, d the distance to the largest
+    logit: d's rounding |d|, e^d 6, the sum of 256 46, its reciprocal 2, a product and the scale 2;
+    a sigmoid's e^-l 6, the sum 1, the reciprocal 2, the scale 1. Renormalized: twice a score's own
+    (the sum over all experts cancels), 5 for the sum of 8, 4 for the quotient, the scale."""
+    g = gen(E + k)
+    x = spread * randn(g, 3000, E)
+    bias = 0.05 * randn(g, E) if biased else None
+    for renorm in (False, True):
+        opts = dict(scores=scores, bias=bias, groups=groups, top_groups=max(1, groups // 2), renormalize=renorm, scale=2.5)
+        ids, w = lib.route_logits(x, k, **opts)
+        want_ids, want = route64(x, k, **opts)
+        assert torch.equal(ids, want_ids)
+        d = (x.amax(1, keepdim=True) - x.gather(1, ids.long())).double()
+        steps = 56 + 2 * d if scores == "softmax" else 28.0
+        off = ((w.double() - want).abs() - 2.5 * 2.0 ** -126) / want
+        assert bool((off <= steps * 2.0 ** -24).all()), float((off / steps).max()) * 2 ** 24
