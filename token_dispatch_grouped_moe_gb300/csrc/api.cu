@@ -20,7 +20,7 @@
 namespace moe {
 namespace {
 
-constexpr int kVersion = 500;   // 0.5.0
+constexpr int kVersion = 501;   // 0.5.1
 constexpr int kMaxDevices = 64;
 
 // ------------------------------------------------------------ device info --

@@ -57,15 +57,16 @@ float linear_cycles(LinearForm form, int64_t R, int32_t K, int32_t N, int32_t G,
 // The form of a product over R rows in G groups: a pair where its estimate is less by a
 // thirtieth at least, in the pairs' two heights the lesser; few rows in the form that
 // leaves room for the next kernel's CTA.
-// Measured, one CTA / pair, us, K x N: 4096 x 256, 8192 rows 20.8 / 25.5; 4096 x 1024, 2000
-// 20.5 / 24.4, 4096 35.0 / 27.1; 1024 x 4096, 400 9.8 / 10.5, 700 13.1 / 12.7; 4096 x 4096,
-// 400 20.1 / 22.3, 700 31.8 / 25.4; 4096 x 14336, 100 24.3 / 26.5, 160 39.1 / 27.8; 14336 x
-// 4096, 100 30.0 / 40.7, 160 42.4 / 40.0; 64 groups 2048 x 1408, 128 each 69.1 / 80.3, 180
-// 94.6 / 78.9. The lesser of those / a pair of 128 rows: 14336 x 4096, 160 35.6 / 30.5, 256
-// 37.8 / 32.4; 8192 x 8192, 256 37.2 / 31.3, 400 41.1 / 48.3; 4096 x 4096, 256 17.8 / 15.7,
-// 400 20.7 / 18.0, 1000 27.3 / 28.8; 8192 x 512, 400 17.6 / 16.2; 2048 x 128, 100 11.5 / 9.7;
-// 64 groups 2048 x 1408, 50 each 63.9 / 66.0, 256 86.7 / 90.0. Up to 32 / 128 rows, one CTA: 1 row 4096 x 14336 23.5 / 24.1, 8 rows 4096 x
-// 4096 9.5 / 10.4, 14336 x 4096 24.0 / 23.7, 32 rows 1024 x 4096 8.3 / 7.1.
+// Measured, one CTA / pair of 256 rows / pair of 128, us, K x N: 4096 x 256, 8192 rows 21.9 / 24.5 /
+// 19.2; 4096 x 1024, 2000 21.4 / 24.3 / 18.7, 4096 36.4 / 27.5 / 29.2; 1024 x 4096, 400 10.1 / 10.8
+// / 10.1, 700 13.4 / 12.6 / 11.7; 4096 x 4096, 256 17.8 / 23.7 / 16.3, 400 21.0 / 22.0 / 18.2, 700
+// 31.8 / 25.5 / 29.4, 8192 219 / 147 / 175; 4096 x 14336, 100 25.2 / 26.7 / 23.9, 160 35.6 / 27.8 /
+// 30.1; 14336 x 4096, 160 38.5 / 41.7 / 32.5, 256 41.1 / 47.2 / 34.9; 8192 x 8192, 256 37.8 / 41.8 /
+// 32.0, 400 65.2 / 41.6 / 50.6; 8192 x 512, 400 17.8 / 25.0 / 16.6; 2048 x 128, 100 12.1 / 11.7 /
+// 10.0; 64 groups 2048 x 1408, 50 each 64.1 / 71.4 / 69.7, 128 70.0 / 75.1 / 72.2, 180 95.7 / 80.1 /
+// 85.8. The form taken is 0.7% off the best of the three on average over 187 such sizes, 10% at worst
+// (400 x 14336 x 4096 49.0 for 44.5). Up to 32 / 128 rows, one CTA: 1 row 4096 x 14336 23.5 / 24.1,
+// 8 rows 4096 x 4096 9.5 / 10.4, 14336 x 4096 24.0 / 23.7, 32 rows 1024 x 4096 8.3 / 7.1.
 LinearForm linear_form(int64_t R, int32_t K, int32_t N, int32_t G, int sms)
 {
     if (G == 1 && R <= 16) return kLinearFew;

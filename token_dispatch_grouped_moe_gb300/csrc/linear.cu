@@ -15,22 +15,22 @@
 // The tensor cores' running sum is cut every 512 k, whatever the output's type: the epilogue
 // warps add each stretch to fp32 registers while the next one is computed into the other
 // TMEM buffer. The sum in TMEM is rounded towards zero at every step, so a long one drifts:
-// of the result at K = 4096, sums that cancel / sums of one sign, 512 k 4.8e-7 / 0.7e-6 in
-// bf16 and 6.5e-7 / 2.5e-6 in fp16 (a sum in fp32, one product after another, 9e-7); 1024 k
+// of the result, sums that cancel / sums of one sign, 512 k 4.8e-7 / 0.7e-6 in bf16 (K =
+// 4096) and 6.5e-7 / 2.5e-6 in fp16 (K = 2048; an fp32 sum of its products one by one 9e-7); 1024 k
 // 1.0e-6 / 1.7e-6 and 1.3e-6 / 5.5e-6; 2048 k 2.1e-6 / 4.3e-6 and 2.5e-6 / 11e-6. Longer
 // stretches are faster where the tensor cores bound the product (16384 rows of 8 experts 4096
 // -> 14336, sustained, us: 512 k 1233, 1024 1167, 2048 1152; 8192 x 4096 x 4096 with
 // residual 188, 175, 177), but no sum in fp32.
 //
-// Kernel shape: one CTA per SM (384 threads), persistent over (group, row tile, n
-// tile) tiles computed from the group offsets:
+// Kernel shape: one CTA per SM (384 threads; the form for up to 32 rows 256, two of which
+// fit on an SM), persistent over (group, row tile, n tile) tiles computed from the group
+// offsets:
 //   warps 0..7  epilogue: warp w reads TMEM lanes 32 (w mod 4) .. + 31 (columns n,
 //               one a thread) and half of the rows (up to 32 rows: warps 0..3, all);
 //   the others  TMEM allocator and MMA issuer; three TMA producers, every third K
 //               block each: the wait, the barrier's bytes and three to six copies take
-//               one thread 650-850 cycles, more than the block's MMAs (one producer:
-//               8192 x 4096 x 4096 161 us instead of 150, 16384 rows of 8 experts 4096 ->
-//               14336 1260 instead of 1120).
+//               one thread 650-850 cycles, more than the block's MMAs (with sums of 2048 k,
+//               where it showed most: one producer 8192 x 4096 x 4096 161 us instead of 150).
 // CTA pairs (PAIR): a 2-CTA cluster shares one tcgen05.mma.cta_group::2 of 256
 // columns n, each CTA staging its 128 of them and half of the rows; both CTAs'
 // boxes complete on rank 0's barrier, rank 0 issues, its commits arrive in both CTAs,
@@ -44,21 +44,22 @@
 // not depend on which came last) and runs the epilogue. No CTA waits for another.
 // Every wait is bounded (ptx.cuh).
 //
-// What bounds it (one GB300):
-//   - many rows: the tensor cores. 8192 x 4096 x 4096 with bias and residual 150 us (1830
-//     TFLOP/s), 16384 rows of 8 experts 4096 -> 14336 with gelu_tanh 1110-1140 us (1690-1730;
-//     a plain library product reaches 1902 for a moment and 1712 at the power cap). A
-//     block's 512 cycles of MMAs are also what shared memory takes to pass its operands
-//     in and out (128 bytes a cycle), so one CTA per MMA, which passes twice as much for
-//     the same sums, stays at 1290 TFLOP/s: pairs, wherever there are tiles enough. 8192 x
-//     4096 x 256 with fp32 outputs 19.8 us (one CTA 22.2, pairs of 256 rows 25.6).
-//   - few rows: the weights' bytes. 789 tokens' top 8 of 64 experts 3584 -> 2560 190 us
-//     (6.6 TB/s; one CTA 196, pairs of 256 rows 198), 128 tokens' top 6 2048 -> 1408 60 us (6.2).
-//   - one token, 4096 -> 14336: 23.5 us, of which 17 stream the weights at 7 TB/s; the
+// What bounds it (one GB300; us in about a second of passes, at the power cap, and in 20):
+//   - many rows: the tensor cores, and the reading of their sums every 512 k. 8192 x 4096 x
+//     4096 with bias and residual 188 (1460 TFLOP/s) and 165 (1660), the tensor pipe busy 74%
+//     of the cycles; 16384 rows of 8 experts 4096 -> 14336 with gelu_tanh 1280 (1500) and 1110
+//     (1730); a plain library product reaches 1902 TFLOP/s for a moment and 1712 at the
+//     power cap. A block's 512 cycles of MMAs are also what shared memory takes to pass its
+//     operands in and out (128 bytes a cycle), so one CTA per MMA, which passes twice as
+//     much for the same sums, takes half as long again (8192 x 4096 x 4096 219 for 147 without
+//     an epilogue): pairs, wherever there are tiles enough. 8192 x 4096 x 256 with fp32
+//     outputs 20 (one CTA 22, pairs of 256 rows 25).
+//   - few rows: the weights' bytes. 789 tokens' top 8 of 64 experts 3584 -> 2560 190
+//     (6.6 TB/s; one CTA 196, pairs of 256 rows 198), 128 tokens' top 6 2048 -> 1408 61 (6.1).
+//   - one token, 4096 -> 14336: 23.5, of which 17 stream the weights at 7 TB/s; the
 //     first loads, the last tile's epilogue and the launch are the rest.
 //   - in between (100 to 1000 rows of one group): the join of cut tiles, or tiles that do
-//     not fill the SMs: 400 x 4096 x 4096 18 us (20.7 on one CTA),
-//     256 x 14336 x 4096 32 (38).
+//     not fill the SMs: 400 x 4096 x 4096 18.2 (21 on one CTA), 256 x 14336 x 4096 35 (41).
 #include <atomic>
 #include <cstdint>
 #include <type_traits>
@@ -684,8 +685,8 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             const bool whole = pc.kb1 - pc.kb0 == k_blocks;
             // without an activation the sums begin with the residual, whose loads pass while
             // the tensor cores work; else it is added at the end, from L2, where it is asked
-            // for now (8192 x 4096 x 4096, us: 149 without a residual, 168 with; silu 158 and
-            // 184)
+            // for now (8192 x 4096 x 4096, sums of 2048 k, us: 149 without a residual, 168 with;
+            // silu 158 and 184)
             const bool early = args.residual && whole && args.act == MOE_ACT_NONE;
             if (args.residual && !early && pc.kb1 == k_blocks) prefetch_residual<OUT, 32 * EPI_WARPS>(args, it, rank);
             const int q = pc.tile - plan.full;         // of a cut tile: its number and parts

@@ -23,7 +23,11 @@
 // with 4 of 8 groups by the sum of their two best 26 (the logits' bytes: 5); top 2 of 8
 // 7.8; 5003 x 160 in 8 groups 7.0; one token 2.3, as any launch. One row in a thousand
 // wants fp64, 1.5 us of its warp's time; a softmax with a bias, where its sum has to be
-// taken again, 9 (26 us without groups, 34 with: the last such row ends the launch).
+// taken again, 9 (28 us without groups, 32 with: the last such row ends the launch).
+// 15 local accesses a token by logits, 44 with scores, bias and groups, are in it at 48
+// registers; they are not the limit's alone: compiled for 64 and 80 (4 and 3 blocks an SM
+// instead of 5) a thread still spills 41 and 42 registers and loads 97 and 98 in place of 62
+// and 135, and the third of the times above is 26.7 and 31 us.
 // Measured on the way, the third of these (us): each of the k maxima by a search of all
 // registers 122; fp64 in functions that were unrolled, cold code fetched for 40 us, 62; in
 // calls from the loop, which spill its registers, 29.
@@ -431,8 +435,8 @@ __device__ __forceinline__ void merge_two(float& x, float& y, float ox, float oy
 }
 
 // e^x in fp64, |x| up to 700 (beyond: of 700): 2^n e^r, |r| <= ln(2) / 2, by the power
-// series of e^r up to r^13. (What follows in fp64 is inlined, without calls: a call in
-// the short way's loop would have its registers spilled for it: 22 accesses a row.)
+// series of e^r up to r^13. (What follows in fp64 is inlined, without calls: with calls from
+// the short way's loop, for which its registers are spilled, 29 us instead of 26.)
 __device__ __forceinline__ double exp64(double x)
 {
     constexpr double kLog2e64 = 1.4426950408889634074, kLn2High = 0.69314718055994530942, kLn2Low = 2.3190468138462996e-17;
