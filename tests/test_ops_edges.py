@@ -115,6 +115,9 @@ def test_permute_keeps_the_rows_type(lib, dtype):
         src, rows = got[2], got[4]
         # (row p is assignment src[p] = t k + j; indexed on the host)
         assert rows.dtype == x.dtype and torch.equal(rows.cpu(), x.cpu()[src.cpu().long() // k])
+    # the rows in another shape, and the first of a longer buffer
+    for y in (x.view(4, T // 4, H), torch.cat([x, x])):
+        assert torch.equal(lib.permute(d, ids, lib.workspace(d), x=y, want_x_perm=True)[4], rows)
 
 
 @gpu

@@ -378,9 +378,10 @@ def _row_type(dims: Dims, x, dev):
     """The type of the rows that a dispatch copies: x's, bf16 or fp16 (16-bit values, as they are)."""
     if x is None:
         return torch.bfloat16
-    if (x.dtype not in (torch.bfloat16, torch.float16) or tuple(x.shape) != (dims.T, dims.H) or not x.is_contiguous()
+    # (T * H values and more in any shape: a batch of sequences, a longer buffer)
+    if (x.dtype not in (torch.bfloat16, torch.float16) or x.numel() < dims.T * dims.H or not x.is_contiguous()
             or x.device != dev):
-        raise ValueError(f"x: expected a contiguous bf16 or fp16 tensor of shape {(dims.T, dims.H)} on {dev}, got "
+        raise ValueError(f"x: expected a contiguous bf16 or fp16 tensor of {dims.T} x {dims.H} values on {dev}, got "
                          f"{x.dtype} {tuple(x.shape)} (strides {x.stride()}) on {x.device}")
     return x.dtype
 
