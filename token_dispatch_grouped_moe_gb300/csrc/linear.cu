@@ -16,7 +16,7 @@
 // warps add each stretch to fp32 registers while the next one is computed into the other
 // TMEM buffer. The sum in TMEM is rounded towards zero at every step, so a long one drifts:
 // of the result, sums that cancel / sums of one sign, 512 k 4.8e-7 / 0.7e-6 in bf16 (K =
-// 4096) and 6.5e-7 / 2.5e-6 in fp16 (K = 2048; an fp32 sum of its products one by one 9e-7); 1024 k
+// 4096) and 6.5e-7 / 2.5e-6 in fp16 (K = 2048; an fp32 sum of its products one by one 6e-7); 1024 k
 // 1.0e-6 / 1.7e-6 and 1.3e-6 / 5.5e-6; 2048 k 2.1e-6 / 4.3e-6 and 2.5e-6 / 11e-6. Longer
 // stretches are faster where the tensor cores bound the product (16384 rows of 8 experts 4096
 // -> 14336, sustained, us: 512 k 1233, 1024 1167, 2048 1152; 8192 x 4096 x 4096 with
