@@ -437,3 +437,25 @@ def test_route_weights_accuracy(lib, scores, E, k, groups, spread, biased):
         steps = 56 + 2 * d if scores == "softmax" else 28.0
         off = ((w.double() - want).abs() - 2.5 * 2.0 ** -126) / want
         assert bool((off <= steps * 2.0 ** -24).all()), float((off / steps).max()) * 2 ** 24
+
+
+@gpu
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [96, 160, 256])
+@pytest.mark.parametrize("groups,top_groups,group_top", [(1, 1, 1), (8, 3, 1), (8, 3, 2)])
+def test_route_forced_experts_of_many(lib, scores, E, groups, top_groups, group_top):
+    """Infinite biases among several experts a lane, next to one another and in all groups; a
+    bias of NaN puts its expert last."""
+    g = gen(E)
+    T, k = 4001, 8
+    x = torch.randint(0, 4, (T, E), generator=g, device="cuda").float()
+    for plus, minus, nan in (((5, 6, E - 1), (), ()), (range(0, E, 12), (3, 4), ()), (range(40), range(60, 80), (1, 90)), ((), (), (7,))):
+        bias = torch.randint(0, 2, (E,), generator=g, device="cuda").float() * 2.0 ** -24
+        for at, v in ((plus, math.inf), (minus, -math.inf), (nan, math.nan)):
+            bias[list(at)] = v
+        for renorm in (False, True):
+            opts = dict(scores=scores, bias=bias, groups=groups, top_groups=top_groups, group_top=group_top, renormalize=renorm)
+            idx = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+            w = torch.full((T, k), math.nan, device="cuda")
+            lib.route_logits(x, k, topk_idx=idx, topk_w=w, **opts)
+            check_route((idx, w), route64(x, k, **opts))
